@@ -22,7 +22,7 @@
  *     Scratch memory is passed in as `ws` (sized by the matching *_ws query).
  *   - All GPU work is enqueued on the stream `s` (0 = null stream) and is
  *     asynchronous; no call synchronises the stream or copies device data to
- *     the host.
+ *     the host (set-up calls that wait say so: sm_param_set_create).
  *   - Arguments are validated on the host before any HIP call; a bad
  *     argument returns an SM_ERR_* code and enqueues nothing.  A failed
  *     launch returns SM_ERR_HIP; sm_last_hip_error() then gives the HIP code.
@@ -364,6 +364,163 @@ sm_status sm_graph_launch(sm_graph g, hipStream_t s);
 sm_status sm_graph_destroy(sm_graph g);
 
 /* ------------------------------------------------------------------------
+ * Sets of parameters.
+ * The Muon steps work on weight matrices; embeddings, the head, norms and
+ * biases of the same model take an AdamW step instead.  A set is a list of
+ * such parameters, of any lengths and types, that one launch works on.
+ *
+ * sm_param: one parameter of `count` entries (0 allowed: nothing to do).
+ *   w      : [count] in wdt, the weights, updated in place.
+ *   master : optional float32 [count] (only with bf16 weights): the weights
+ *            in float32, updated in place; w then receives their rounding
+ *            to bf16 and is not read.
+ *   grad   : [M] rows of [count] in gdt, grad_stride entries apart, one per
+ *            worker (read-only; the gradient is the workers' mean).
+ *   m, v   : [count], first and second moment, updated in place; zero them
+ *            before the first step.  state SM_STATE_F32: float32.  state
+ *            SM_STATE_FP8: one byte per entry (see sm_state8_pack), with
+ *            m_scale, v_scale: float32 [ceil(count/256)].
+ *   weight_decay >= 0, lr_mult >= 0 (a factor on the step's lr): finite.
+ *   w, m and v NULL: a parameter that only sm_grad_norm takes (a Muon
+ *   step's matrices enter the norm this way); wdt, state and master are
+ *   ignored.
+ * Pointers are aligned to their elements; a parameter whose pointers (and
+ * worker rows) all are 16-byte aligned (8-bit states: 8-byte) takes the
+ * vector path.
+ *
+ * sm_param_set_create validates the list and writes its tables into ws (at
+ * least sm_param_set_ws bytes, 256-byte aligned).  It is the set-up call:
+ * it waits for the tables to be written, so that the set may be used on any
+ * stream of the device afterwards.  The buffers that the list names, and
+ * ws, must stay allocated, in place, until sm_param_set_destroy, which does
+ * not wait: call it once the work enqueued with the set has finished.
+ * Errors: SM_ERR_ARG (n < 1, null or misaligned pointers, missing or
+ *   unexpected scales or master, bad weight_decay or lr_mult, grad_stride <
+ *   count with M > 1, a buffer that is written overlapping any other of the
+ *   list or ws), SM_ERR_SHAPE (count < 0 or > 2^40, grad_stride > 2^40, n >
+ *   2^20, or more than 2^24 - 1 work items), SM_ERR_DTYPE, SM_ERR_WORKSPACE,
+ *   SM_ERR_UNSUPPORTED (M outside 1..64; s in graph capture), SM_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef enum { SM_STATE_F32 = 0, SM_STATE_FP8 = 1 } sm_state;
+
+typedef struct {
+  int64_t count;
+  int64_t grad_stride;
+  void* w;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int32_t wdt, gdt;
+  int32_t state;        /* sm_state                                        */
+  float weight_decay;
+  float lr_mult;
+} sm_param;
+
+typedef struct sm_param_set_s* sm_param_set;
+sm_status sm_param_set_ws(const sm_param* params, int n, size_t* ws_bytes);
+sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, size_t ws_bytes,
+                              hipStream_t s, sm_param_set* out);
+sm_status sm_param_set_destroy(sm_param_set set);
+
+/* ------------------------------------------------------------------------
+ * One AdamW step (decoupled weight decay) over a set of parameters.
+ *   g = (gscale / M) * sum_k grad_k       (the sum in float64 for M > 1)
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+ *   w <- w (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in float32 (the step's scalars in float64), w rounded once to its type.
+ * 8-bit states are decoded, updated in float32 (the weights' update uses
+ * those values) and encoded again with stochastic rounding: with beta2 =
+ * 0.999 a step moves v by a tenth of a percent while neighbouring codes lie
+ * 14-25 % apart, so rounding to nearest would leave v where it is.
+ * rounding: SM_ROUND_STOCHASTIC rounds bf16 weights without a master
+ *   stochastically as well (unbiased over steps, where a nearest rounding
+ *   loses updates below half a bf16 step); other weights ignore it.
+ * The random bits are a fixed function of (seed, t, the parameter's index in
+ * the set, the entry's index): the same call gives the same bits.
+ *   With C = 0x9E3779B9 and mix(x) = { x ^= x >> 16; x *= 0x9E3779B1;
+ *   x ^= x >> 15; x *= 0x85A308D3; x ^= x >> 16 } on uint32: key = 0, then
+ *   key = mix((key ^ d) + C) for d = the low and high halves of seed and of
+ *   t, the parameter's index, and the high half of the entry's; r = mix(low
+ *   half of the entry's index ^ key).  m takes the low 16 bits of r, v the
+ *   high ones, w the low 16 of mix(r ^ 0x9E3779B1).
+ *
+ * t: 1-based step index if step is NULL.  step: device int64, the number of
+ *   steps done so far; then t must be 0, the step has index *step + 1, and
+ *   *step is advanced on the device (so that a captured call replays as a
+ *   training loop's next step).
+ * gscale: optional device float, a factor on the gradients (sm_grad_norm's
+ *   out + 1).  lr_scale: optional device float >= 0, a factor on lr (a
+ *   schedule's, for captured calls).  If one of them is not finite the whole
+ *   step is skipped: nothing is written and *step stays.
+ * Calls on one set must be ordered by the caller (they update the same
+ * tensors, and share the set's scratch).
+ * Errors: SM_ERR_ARG (null config or set, a set with sm_grad_norm-only
+ *   parameters, t < 1 without step, t != 0 with it, misaligned pointers, lr
+ *   < 0 or not finite, betas outside [0, 1), eps < 1e-15 or not finite, bad
+ *   rounding), SM_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef enum { SM_ROUND_NEAREST = 0, SM_ROUND_STOCHASTIC = 1 } sm_rounding;
+
+typedef struct {
+  float lr, beta1, beta2, eps;
+  int32_t rounding;     /* sm_rounding of bf16 weights without a master    */
+  uint64_t seed;
+} sm_adamw_config;
+
+sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_t* step,
+                   const float* gscale, const float* lr_scale, hipStream_t s);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm and clipping factor over sets of parameters.
+ *   out[0] = |scale| * sqrt(sum over all entries of ((1/M) sum_k grad_k)^2)
+ *   out[1] = scale * min(1, max_norm / (out[0] + 1e-6)), the factor that
+ *            sm_adamw takes as gscale; NaN if out[0] is not finite, so that
+ *            the step is skipped.
+ * scale undoes a loss scaling (1 if there is none); max_norm may be
+ * infinity (no clipping).  Sums of 8 squares in float32, beyond that in
+ * float64, in a fixed order; a square beyond float32's range (an entry above
+ * 1.8e19) makes the norm infinite.
+ * sets: 1..8 sets (of any M and types).  out: 2 floats.  ws: at least
+ * sm_grad_norm_ws bytes, 256-byte aligned; calls that may overlap need
+ * workspaces of their own.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, nsets < 1, scale not
+ *   finite, max_norm not > 0, out inside ws), SM_ERR_UNSUPPORTED (nsets >
+ *   8), SM_ERR_WORKSPACE, SM_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+sm_status sm_grad_norm_ws(int nsets, size_t* ws_bytes);
+sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float max_norm,
+                       float* out, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* ------------------------------------------------------------------------
+ * 8-bit AdamW states from float32 ones, and back (checkpoints, and a run
+ * that changes its states' type).
+ * Entries are taken in blocks of 256 (the last one may be shorter).  A
+ * block's scale is 2^e, e >= -126 the smallest exponent with
+ *   max |m| <= 1.75 * 2^8  * 2^e, codes of m: OCP e4m3 (448 the largest)
+ *   max v   <= 1.75 * 2^15 * 2^e, codes of v: OCP e5m2 (57344 the largest)
+ * over the block's finite entries, and a code stands for (its value) *
+ * 2^e: scaling is exact, and unpack then pack gives back the same values.
+ * Packing rounds to nearest even.  A positive v takes at least the smallest
+ * code, since v = 0 under a nonzero m would divide by eps alone; a negative
+ * v counts as 0.  A NaN or infinite m is stored as NaN, a NaN v as NaN, an
+ * infinite v as infinity; none of them touches its block's scale.
+ * m, v: float32 [count].  m8, v8: [count] bytes (any alignment; 8-byte
+ * alignment takes the vector path).  m_scale, v_scale: float32
+ * [ceil(count/256)].  count == 0 is a no-op.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, an output overlapping
+ *   another buffer), SM_ERR_SHAPE (count < 0 or > 2^40), SM_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+#define SM_STATE8_BLOCK 256
+sm_status sm_state8_pack(const float* m, const float* v, int64_t count, uint8_t* m8, uint8_t* v8,
+                         float* m_scale, float* v_scale, hipStream_t s);
+sm_status sm_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* m_scale,
+                           const float* v_scale, int64_t count, float* m, float* v,
+                           hipStream_t s);
+
+/* ------------------------------------------------------------------------
  * Kernel-time accounting (for benchmarks; not part of the method).
  * While enabled, every kernel the library launches is bracketed by a pair of
  * HIP events on its stream, tagged with its kind and its algorithmic work
@@ -393,7 +550,10 @@ enum {
   SM_K_POLAR_UPDATE = 9, /* W <- W - lr D                          bytes  */
   SM_K_MISC = 10,        /* small finalize / copy kernels          bytes  */
   SM_K_SPECTRAL = 11,    /* power-method passes (diagnostic)       bytes  */
-  SM_K_NUM_KINDS = 12
+  SM_K_ADAMW = 12,       /* AdamW step over a set                  bytes  */
+  SM_K_GRAD_NORM = 13,   /* global gradient norm                   bytes  */
+  SM_K_STATE8 = 14,      /* 8-bit states from float32 and back     bytes  */
+  SM_K_NUM_KINDS = 15
 };
 sm_status sm_profile_enable(int on);
 sm_status sm_profile_reset(void);

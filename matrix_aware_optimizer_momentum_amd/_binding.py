@@ -21,14 +21,19 @@ SIGN_MUON, CACHE_MUON, LION_MUON = 0, 1, 2
 UPDATE_VOTE, UPDATE_POLAR = 0, 1
 MODE_TRIGGER, MODE_FORCE_FRESH, MODE_FORCE_REUSE = 0, 1, 2
 ENC_BITS, ENC_INT8 = 0, 1
+STATE_F32, STATE_FP8 = 0, 1
+ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
+STATE8_BLOCK = 256             # SM_STATE8_BLOCK
 NS_NOALLOC_MAX_WS = 64 << 20   # SM_NS_NOALLOC_MAX_WS
 
 KERNEL_KINDS = ["ema", "norm", "gemm_gram", "gemm_apply", "gemm_rr", "probe", "sign_pack",
-                "vote_update", "lion", "polar_update", "misc", "spectral"]
+                "vote_update", "lion", "polar_update", "misc", "spectral", "adamw", "grad_norm",
+                "state8"]
 
 # Every function the header declares, with its ctypes signature.
 c_int, c_int32, c_int64, c_float, c_double = (ctypes.c_int, ctypes.c_int32, ctypes.c_int64,
                                              ctypes.c_float, ctypes.c_double)
+c_uint64 = ctypes.c_uint64
 c_void_p, c_size_t, c_char_p = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_char_p
 
 
@@ -47,6 +52,18 @@ class Config(ctypes.Structure):
                 ("mdt", c_int32), ("gdt", c_int32), ("lr", c_float), ("beta1", c_float),
                 ("beta2", c_float), ("period", c_int32), ("ns", NSParams), ("gamma", c_float),
                 ("cache_mode", c_int32), ("encoding", c_int32), ("vote_polar", c_int32)]
+
+
+class Param(ctypes.Structure):
+    _fields_ = [("count", c_int64), ("grad_stride", c_int64), ("w", c_void_p),
+                ("master", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p), ("wdt", c_int32), ("gdt", c_int32),
+                ("state", c_int32), ("weight_decay", c_float), ("lr_mult", c_float)]
+
+
+class AdamWConfig(ctypes.Structure):
+    _fields_ = [("lr", c_float), ("beta1", c_float), ("beta2", c_float), ("eps", c_float),
+                ("rounding", c_int32), ("seed", c_uint64)]
 
 
 P = ctypes.POINTER
@@ -81,6 +98,19 @@ SIGNATURES = {
                               c_void_p, P(c_void_p)]),
     "sm_graph_launch": (c_int, [c_void_p, c_void_p]),
     "sm_graph_destroy": (c_int, [c_void_p]),
+    "sm_param_set_ws": (c_int, [P(Param), c_int, P(c_size_t)]),
+    "sm_param_set_create": (c_int, [P(Param), c_int, c_int, c_void_p, c_size_t, c_void_p,
+                                    P(c_void_p)]),
+    "sm_param_set_destroy": (c_int, [c_void_p]),
+    "sm_adamw": (c_int, [P(AdamWConfig), c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                         c_void_p]),
+    "sm_grad_norm_ws": (c_int, [c_int, P(c_size_t)]),
+    "sm_grad_norm": (c_int, [P(c_void_p), c_int, c_float, c_float, c_void_p, c_void_p, c_size_t,
+                             c_void_p]),
+    "sm_state8_pack": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                               c_void_p, c_void_p]),
+    "sm_state8_unpack": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                 c_void_p, c_void_p]),
     "sm_profile_enable": (c_int, [c_int]),
     "sm_profile_reset": (c_int, []),
     "sm_profile_read": (c_int, [c_int, P(c_double), P(c_int64), P(c_double)]),

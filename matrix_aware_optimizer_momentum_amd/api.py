@@ -441,6 +441,293 @@ class StepGraph:
             pass
 
 
+# ------------------------------------------------------------------ AdamW
+
+STATE8_DTYPES = (torch.float8_e4m3fn, torch.float8_e5m2)   # first, second moment
+
+
+def _state_blocks(count: int) -> int:
+    return (count + B.STATE8_BLOCK - 1) // B.STATE8_BLOCK
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's device, whichever device is current."""
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _dev_all(**tensors: torch.Tensor):
+    """Contiguous GPU tensors, all on one device."""
+    for name, t in tensors.items():
+        _dev(t, name)
+    if len({t.device for t in tensors.values()}) > 1:
+        raise ValueError(f"{', '.join(tensors)} must be on one device")
+
+
+@dataclass
+class AdamWConfig:
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    rounding: int = B.ROUND_NEAREST   # of bf16 weights without a master
+    seed: int = 0                     # of the stochastic rounding, 0 .. 2^64 - 1
+
+    def c_struct(self) -> B.AdamWConfig:
+        if not 0 <= self.seed < 1 << 64:
+            raise ValueError("seed must be in 0 .. 2^64 - 1")
+        return B.AdamWConfig(self.lr, self.beta1, self.beta2, self.eps, self.rounding, self.seed)
+
+
+@dataclass
+class ParamBuffers:
+    """Caller-owned buffers of one parameter (all on the GPU, any shape).
+
+    Without w, m and v the parameter only enters grad_norm (a Muon step's
+    gradients)."""
+    grad: torch.Tensor                    # [M, *shape], rows contiguous; M = 1: also [*shape]
+    w: Optional[torch.Tensor] = None      # [*shape] float32 / bfloat16
+    m: Optional[torch.Tensor] = None      # [*shape] float32, or float8_e4m3fn
+    v: Optional[torch.Tensor] = None      # [*shape] float32, or float8_e5m2
+    m_scale: Optional[torch.Tensor] = None   # float32 [ceil(count/256)] of 8-bit states
+    v_scale: Optional[torch.Tensor] = None
+    master: Optional[torch.Tensor] = None    # [*shape] float32 of bfloat16 weights
+    weight_decay: float = 0.0
+    lr_mult: float = 1.0
+
+    @classmethod
+    def with_state(cls, w: torch.Tensor, grad: torch.Tensor, fp8: bool = False,
+                   master: bool = False, weight_decay: float = 0.0,
+                   lr_mult: float = 1.0) -> "ParamBuffers":
+        """The buffers of w before its first step: zero moments (8-bit ones with
+        fp8), and a float32 copy of w with master."""
+        def zeros(dtype):
+            size = 4 if dtype == torch.float32 else 1
+            return torch.zeros(w.numel() * size, dtype=torch.uint8,
+                               device=w.device).view(dtype).view(w.shape)
+        m, v = (zeros(d) for d in (STATE8_DTYPES if fp8 else (torch.float32,) * 2))
+        ms, vs = ((torch.zeros(_state_blocks(w.numel()), device=w.device) for _ in range(2))
+                  if fp8 else (None, None))
+        return cls(grad=grad, w=w, m=m, v=v, m_scale=ms, v_scale=vs,
+                   master=w.detach().float() if master else None, weight_decay=weight_decay,
+                   lr_mult=lr_mult)
+
+    def c_struct(self, M: int) -> B.Param:
+        p = lambda t: t.data_ptr() if t is not None else None
+        count = (self.w.numel() if self.w is not None else self.grad.numel() // M)
+        stride = self.grad.stride(0) if M > 1 else count
+        return B.Param(count, stride, p(self.w), p(self.master), p(self.grad), p(self.m),
+                       p(self.v), p(self.m_scale), p(self.v_scale),
+                       _dt(self.w) if self.w is not None else B.F32, _dt(self.grad),
+                       B.STATE_FP8 if self.m is not None and self.m.dtype != torch.float32
+                       else B.STATE_F32, self.weight_decay, self.lr_mult)
+
+
+def _check_param(j: int, p: ParamBuffers, M: int):
+    """The shapes and dtypes of one parameter agree, and every tensor is a
+    contiguous GPU tensor (the gradient: every worker's row)."""
+    def expect(name, shape, dtype=None):
+        _expect(getattr(p, name), f"parameter {j} {name}", shape, dtype, dev=False)
+
+    def some_dt(t, name):
+        if t.dtype not in _DT:
+            raise ValueError(f"parameter {j} {name} must be float32 or bfloat16, got {t.dtype}")
+
+    some_dt(p.grad, "grad")
+    tensors = []
+    if p.w is None:
+        for name in ("m", "v", "m_scale", "v_scale", "master"):
+            if getattr(p, name) is not None:
+                raise ValueError(f"parameter {j}: {name} without w")
+        if M > 1 and (p.grad.dim() < 1 or p.grad.shape[0] != M):
+            raise ValueError(f"parameter {j} grad must have {M} rows, got {tuple(p.grad.shape)}")
+        rows = p.grad[0] if M > 1 else p.grad
+    else:
+        some_dt(p.w, "w")
+        shape = tuple(p.w.shape)
+        if tuple(p.grad.shape) != (M, *shape) and not (M == 1 and tuple(p.grad.shape) == shape):
+            raise ValueError(f"parameter {j} grad must have shape {(M, *shape)}, "
+                             f"got {tuple(p.grad.shape)}")
+        rows = p.grad[0] if tuple(p.grad.shape) != shape else p.grad
+        if p.m is None or p.v is None:
+            raise ValueError(f"parameter {j}: w needs m and v")
+        if p.m.dtype == torch.float32:
+            dts = (torch.float32, torch.float32)
+            if p.m_scale is not None or p.v_scale is not None:
+                raise ValueError(f"parameter {j}: float32 states have no scales")
+        else:
+            dts = STATE8_DTYPES
+            if p.m_scale is None or p.v_scale is None:
+                raise ValueError(f"parameter {j}: 8-bit states need m_scale and v_scale")
+            for name in ("m_scale", "v_scale"):
+                expect(name, (_state_blocks(p.w.numel()),), torch.float32)
+                tensors.append((getattr(p, name), name))
+        expect("m", shape, dts[0])
+        expect("v", shape, dts[1])
+        tensors += [(p.w, "w"), (p.m, "m"), (p.v, "v")]
+        if p.master is not None:
+            if p.w.dtype != torch.bfloat16:
+                raise ValueError(f"parameter {j}: only bfloat16 weights have a master")
+            expect("master", shape, torch.float32)
+            tensors.append((p.master, "master"))
+    for t, name in tensors + [(rows, "grad")]:
+        _dev(t, f"parameter {j} {name}")
+    return [t for t, _ in tensors] + [p.grad]
+
+
+class ParamSet:
+    """A list of parameters that one call works on (sm_param_set): its tables
+    on the GPU, made once.
+
+    The buffers are bound at construction and must stay in place while the
+    set, or a graph captured from its calls, lives.  Calls on one set must be
+    ordered (they update the same tensors)."""
+
+    def __init__(self, params: Sequence[ParamBuffers], M: int = 1,
+                 ws: Optional[torch.Tensor] = None):
+        self._h = None
+        if len(params) == 0:
+            raise ValueError("a set needs at least one parameter")
+        if M < 1:
+            raise ValueError("M must be at least 1")
+        self.params = list(params)
+        self.M = M
+        tensors = [t for j, p in enumerate(self.params) for t in _check_param(j, p, M)]
+        self.device = tensors[0].device
+        if any(t.device != self.device for t in tensors):
+            raise ValueError("all tensors of a set must be on one device")
+        arr = (B.Param * len(self.params))(*[p.c_struct(M) for p in self.params])
+        need = ctypes.c_size_t(0)
+        B.check(B.lib().sm_param_set_ws(arr, len(self.params), ctypes.byref(need)),
+                "sm_param_set_ws")
+        if ws is not None:
+            _dev(ws, "ws")
+        self.ws = _ws(need.value, self.device, ws)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            code = B.lib().sm_param_set_create(arr, len(self.params), M, self.ws.data_ptr(),
+                                               self.ws.numel() * self.ws.element_size(),
+                                               _stream_of(self.ws), ctypes.byref(h))
+        B.check(code, "sm_param_set_create")
+        self._h = h
+
+    def _use(self):
+        """The handle, for work on the device's current stream, which the
+        tables then outlive."""
+        if self._h is None:
+            raise RuntimeError("ParamSet: use after close()")
+        self.ws.record_stream(torch.cuda.current_stream(self.device))
+        return self._h
+
+    def close(self):
+        if self._h is not None:
+            h, self._h = self._h, None
+            B.lib().sm_param_set_destroy(h)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _scalar(t: Optional[torch.Tensor], name: str, dtype, device):
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError(f"{name} must hold one element, has {t.numel()}")
+    _expect(t, name, dtype=dtype)
+    if t.device != device:
+        raise ValueError(f"{name} must be on the set's device")
+    return t.data_ptr()
+
+
+def adamw(cfg: AdamWConfig, pset: ParamSet, t: Optional[int] = None,
+          step: Optional[torch.Tensor] = None, gscale: Optional[torch.Tensor] = None,
+          lr_scale: Optional[torch.Tensor] = None):
+    """One AdamW step over the set's parameters, in place.
+
+    Either t (1-based) or step (int64 device tensor, the steps done so far,
+    advanced by the call) gives the step's index.  gscale (grad_norm's second
+    result) and lr_scale are float32 device scalars; a non-finite one skips
+    the step."""
+    if (t is None) == (step is None):
+        raise ValueError("adamw needs t or step (one of them)")
+    if t is not None and t < 1:
+        raise ValueError("t must be at least 1")
+    c = cfg.c_struct()
+    dev = pset.device
+    sp = _scalar(step, "step", torch.int64, dev)
+    gp = _scalar(gscale, "gscale", torch.float32, dev)
+    lp = _scalar(lr_scale, "lr_scale", torch.float32, dev)
+    h = pset._use()
+    with torch.cuda.device(dev):
+        code = B.lib().sm_adamw(ctypes.byref(c), h, t or 0, sp, gp, lp, _stream_of(pset.ws))
+    B.check(code, "sm_adamw")
+
+
+def grad_norm(psets: Sequence[ParamSet], max_norm: float, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """float32 [2]: the global norm of the sets' (mean) gradients times |scale|,
+    and the factor scale * min(1, max_norm / (norm + 1e-6)) for adamw's gscale
+    (out[1:2]), NaN where the norm is not finite."""
+    if len(psets) == 0:
+        raise ValueError("grad_norm needs at least one set")
+    dev = psets[0].device
+    if any(p.device != dev for p in psets):
+        raise ValueError("all sets must be on one device")
+    need = ctypes.c_size_t(0)
+    B.check(B.lib().sm_grad_norm_ws(len(psets), ctypes.byref(need)), "sm_grad_norm_ws")
+    out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
+    _expect(out, "out", (2,), torch.float32)
+    if ws is not None:
+        _dev(ws, "ws")
+    ws = _ws(need.value, dev, ws)
+    if out.device != dev or ws.device != dev:
+        raise ValueError("out and ws must be on the sets' device")
+    arr = (ctypes.c_void_p * len(psets))(*[p._use() for p in psets])
+    with torch.cuda.device(dev):
+        code = B.lib().sm_grad_norm(arr, len(psets), scale, max_norm, out.data_ptr(),
+                                    ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _stream_of(ws))
+    B.check(code, "sm_grad_norm")
+    return out
+
+
+def state8_pack(m: torch.Tensor, v: torch.Tensor):
+    """(m8, v8, m_scale, v_scale): 8-bit AdamW states of float32 ones, rounded
+    to nearest.  m8 is float8_e4m3fn and v8 float8_e5m2, in m's shape; the
+    scales are float32, one per 256 entries."""
+    _expect(m, "m", dtype=torch.float32, dev=False)
+    _expect(v, "v", m.shape, torch.float32, dev=False)
+    _dev_all(m=m, v=v)
+    m8, v8 = (torch.empty(m.shape, dtype=d, device=m.device) for d in STATE8_DTYPES)
+    ms, vs = (torch.empty(_state_blocks(m.numel()), device=m.device) for _ in range(2))
+    with torch.cuda.device(m.device):
+        code = B.lib().sm_state8_pack(m.data_ptr(), v.data_ptr(), m.numel(), m8.data_ptr(),
+                                      v8.data_ptr(), ms.data_ptr(), vs.data_ptr(), _stream_of(m))
+    B.check(code, "sm_state8_pack")
+    return m8, v8, ms, vs
+
+
+def state8_unpack(m8: torch.Tensor, v8: torch.Tensor, m_scale: torch.Tensor,
+                  v_scale: torch.Tensor):
+    """(m, v): the float32 values of 8-bit AdamW states, in m8's shape."""
+    blocks = (_state_blocks(m8.numel()),)
+    _expect(m8, "m8", dtype=STATE8_DTYPES[0], dev=False)
+    _expect(v8, "v8", m8.shape, STATE8_DTYPES[1], dev=False)
+    _expect(m_scale, "m_scale", blocks, torch.float32, dev=False)
+    _expect(v_scale, "v_scale", blocks, torch.float32, dev=False)
+    _dev_all(m8=m8, v8=v8, m_scale=m_scale, v_scale=v_scale)
+    m, v = (torch.empty(m8.shape, dtype=torch.float32, device=m8.device) for _ in range(2))
+    with torch.cuda.device(m8.device):
+        code = B.lib().sm_state8_unpack(m8.data_ptr(), v8.data_ptr(), m_scale.data_ptr(),
+                                        v_scale.data_ptr(), m8.numel(), m.data_ptr(),
+                                        v.data_ptr(), _stream_of(m8))
+    B.check(code, "sm_state8_unpack")
+    return m, v
+
+
 # ------------------------------------------------------------------ kernel accounting
 
 def mfma_ceiling(out: torch.Tensor, blocks: int, iters: int, mode: int = 1,

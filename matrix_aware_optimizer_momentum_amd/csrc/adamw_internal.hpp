@@ -1,0 +1,127 @@
+// Declarations shared by the AdamW kernels (k_adamw.hip) and their C ABI
+// (sm_adamw.hip): the device tables of a parameter set and the launchers.
+#pragma once
+
+#include "sm_internal.hpp"
+
+namespace sm {
+
+// Entries that a workgroup takes at a time, 8 per thread, and the block of
+// entries that share an 8-bit state's scales (32 threads of a unit).
+constexpr int kUnit = 2048;
+constexpr int kStateBlock = SM_STATE8_BLOCK;
+
+// One parameter in a set's device table.
+enum : uint32_t {
+  kPF_W16 = 1,     // bf16 weights
+  kPF_G16 = 2,     // bf16 gradients
+  kPF_FP8 = 4,     // 8-bit states
+  kPF_VEC = 8,     // every pointer and worker row takes 16-byte accesses
+};
+struct ParamEnt {
+  void* w;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  int64_t count, gstride;
+  float wd, lr_mult;
+  uint32_t flags;
+};
+
+// A workgroup's share of a set: `units` units (see ParamSetDev) of parameter
+// `tensor` from entry chunk * units * kUnit on.
+struct WorkItem {
+  uint32_t tensor, chunk;
+};
+
+// The 32-bit mixing behind the random bits of stochastic rounding: two
+// multiplications (2^32 / golden ratio, digits of pi) between shifts.
+__host__ __device__ inline uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0x85A308D3u;
+  return x ^ (x >> 16);
+}
+__host__ __device__ inline uint32_t mix_key(uint32_t key, uint32_t word) {
+  return mix32((key ^ word) + 0x9E3779B9u);
+}
+__host__ __device__ inline uint32_t step_key(uint64_t seed, int64_t t) {
+  uint32_t k = mix_key(0u, (uint32_t)seed);
+  k = mix_key(k, (uint32_t)(seed >> 32));
+  k = mix_key(k, (uint32_t)(uint64_t)t);
+  return mix_key(k, (uint32_t)((uint64_t)t >> 32));
+}
+
+// Scalars of a step, computed in float64 and rounded once.
+struct AdamwScalars {
+  float lr, b1, a1, b2, a2;   // a = 1 - b
+  float step;                 // lr / (1 - b1^t)
+  float root;                 // 1 / sqrt(1 - b2^t)
+  float eps;
+  uint32_t key;               // of (seed, t)
+  int32_t stochastic;
+  int32_t skip;
+};
+
+__host__ __device__ inline AdamwScalars adamw_scalars(const sm_adamw_config& c, int64_t t) {
+  AdamwScalars a;
+  a.lr = c.lr;
+  a.b1 = c.beta1;
+  a.a1 = 1.0f - c.beta1;
+  a.b2 = c.beta2;
+  a.a2 = 1.0f - c.beta2;
+  a.step = (float)((double)c.lr / (1.0 - pow((double)c.beta1, (double)t)));
+  a.root = (float)(1.0 / sqrt(1.0 - pow((double)c.beta2, (double)t)));
+  a.eps = c.eps;
+  a.key = step_key(c.seed, t);
+  a.stochastic = c.rounding;
+  a.skip = 0;
+  return a;
+}
+
+struct ParamSetDev {
+  const ParamEnt* ents;
+  const WorkItem* items;
+  AdamwScalars* scalars;      // of a step with a device-side index
+  int nitems, units, M;
+};
+
+// Tables of up to kFillMax parameters written per launch (they ride in the
+// arguments); first[i]: parameter i's first work item.
+constexpr int kFillMax = 32;
+struct FillTbl {
+  ParamEnt e[kFillMax];
+  int64_t first[kFillMax];
+};
+sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, WorkItem* items,
+                          int units, hipStream_t s);
+
+// The scalars of a step whose index *step holds, and *step + 1 written back
+// unless the step is skipped.
+sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float* gscale,
+                            const float* lr_scale, AdamwScalars* out, hipStream_t s);
+// The step itself: scalars from the arguments, or from set.scalars if
+// `device` (gscale and lr_scale are then checked already).  fp8: some
+// parameter has 8-bit states.  stream: past the caches.
+sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool device,
+                       const float* gscale, const float* lr_scale, bool fp8, bool stream,
+                       double bytes, hipStream_t s);
+
+// Sums of squares of a set's mean gradients: one double per workgroup,
+// norm_set_parts(nitems) of them, already divided by M^2.
+constexpr int kNormSetParts = 2048;
+inline int norm_set_parts(int nitems) { return nitems < kNormSetParts ? nitems : kNormSetParts; }
+sm_status launch_grad_sumsq(const ParamSetDev& set, double* parts, double bytes, hipStream_t s);
+sm_status launch_norm_finalize(const double* parts, int n, float scale, float max_norm,
+                               float* out, hipStream_t s);
+
+sm_status launch_state8_pack(const float* m, const float* v, int64_t count, uint8_t* m8,
+                             uint8_t* v8, float* ms, float* vs, hipStream_t s);
+sm_status launch_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* ms,
+                               const float* vs, int64_t count, float* m, float* v, hipStream_t s);
+
+}  // namespace sm
