@@ -6,17 +6,20 @@
 
 namespace sm {
 
-// Entries that a workgroup takes at a time, 8 per thread, and the block of
-// entries that share an 8-bit state's scales (32 threads of a unit).
-constexpr int kUnit = 2048;
+// The block of entries that share an 8-bit state's scales: one wave's, 4 per
+// lane.
 constexpr int kStateBlock = SM_STATE8_BLOCK;
+static_assert(kStateBlock == 64 * 4, "a wave holds one block");
+// Entries of a work item of the step (one workgroup) and of the norm.
+constexpr int kStepSpan = 2048;
+constexpr int kNormSpan = 16384;
 
 // One parameter in a set's device table.
 enum : uint32_t {
   kPF_W16 = 1,     // bf16 weights
   kPF_G16 = 2,     // bf16 gradients
   kPF_FP8 = 4,     // 8-bit states
-  kPF_VEC = 8,     // every pointer and worker row takes 16-byte accesses
+  kPF_VEC = 8,     // every pointer and worker row is aligned to 4 of its entries
 };
 struct ParamEnt {
   void* w;
@@ -31,8 +34,8 @@ struct ParamEnt {
   uint32_t flags;
 };
 
-// A workgroup's share of a set: `units` units (see ParamSetDev) of parameter
-// `tensor` from entry chunk * units * kUnit on.
+// A share of a set: `span` entries (kStepSpan or kNormSpan) of parameter
+// `tensor` from entry chunk * span on.
 struct WorkItem {
   uint32_t tensor, chunk;
 };
@@ -85,36 +88,39 @@ __host__ __device__ inline AdamwScalars adamw_scalars(const sm_adamw_config& c, 
 
 struct ParamSetDev {
   const ParamEnt* ents;
-  const WorkItem* items;
+  const WorkItem* items;      // the step's
+  const WorkItem* norm_at;  // the norm's
   AdamwScalars* scalars;      // of a step with a device-side index
-  int nitems, units, M;
+  int nitems, norm_items, M;
+  float inv_M;
 };
 
 // Tables of up to kFillMax parameters written per launch (they ride in the
-// arguments); first[i]: parameter i's first work item.
+// arguments); first[i], norm_first[i]: parameter i's first work items.
 constexpr int kFillMax = 32;
 struct FillTbl {
   ParamEnt e[kFillMax];
-  int64_t first[kFillMax];
+  int64_t first[kFillMax], norm_first[kFillMax];
 };
+static_assert(sizeof(FillTbl) <= 3584, "the table rides in the arguments");
 sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, WorkItem* items,
-                          int units, hipStream_t s);
+                          WorkItem* norm_items, hipStream_t s);
 
 // The scalars of a step whose index *step holds, and *step + 1 written back
 // unless the step is skipped.
 sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float* gscale,
                             const float* lr_scale, AdamwScalars* out, hipStream_t s);
 // The step itself: scalars from the arguments, or from set.scalars if
-// `device` (gscale and lr_scale are then checked already).  fp8: some
-// parameter has 8-bit states.  stream: past the caches.
+// `device`.  fp8: some parameter has 8-bit states.  bytes: what the step
+// reads and writes.
 sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool device,
-                       const float* gscale, const float* lr_scale, bool fp8, bool stream,
-                       double bytes, hipStream_t s);
+                       const float* gscale, const float* lr_scale, bool fp8, double bytes,
+                       hipStream_t s);
 
 // Sums of squares of a set's mean gradients: one double per workgroup,
-// norm_set_parts(nitems) of them, already divided by M^2.
+// norm_set_parts(norm_items) of them, already divided by M^2.
 constexpr int kNormSetParts = 2048;
-inline int norm_set_parts(int nitems) { return nitems < kNormSetParts ? nitems : kNormSetParts; }
+inline int norm_set_parts(int items) { return items < kNormSetParts ? items : kNormSetParts; }
 sm_status launch_grad_sumsq(const ParamSetDev& set, double* parts, double bytes, hipStream_t s);
 sm_status launch_norm_finalize(const double* parts, int n, float scale, float max_norm,
                                float* out, hipStream_t s);

@@ -1,175 +1,404 @@
 // AdamW over sets of parameters (float32 or 8-bit states), the global
 // gradient norm, and the conversion of 8-bit states.  All of it is bound by
 // HBM: every entry's weights, gradients and states are read once and written
-// once, with 16-byte accesses where the addresses allow.
+// once, with accesses of up to 16 bytes per lane, contiguous across the wave.
 //
 // One launch works on a whole set, whatever its lengths and types: each
 // workgroup reads its work item (parameter, place) and the parameter's table
-// entry, both uniform (scalar loads), and takes units of 2048 entries, 8 per
-// thread.
+// entry, both uniform (scalar loads), and takes one unit of entries, 4 per
+// lane.
 #include "adamw_internal.hpp"
+
+#include <type_traits>
 
 namespace sm {
 
 namespace {
 
 constexpr int kThreads = 256;
-static_assert(kUnit == kThreads * 8, "8 entries per thread");
+constexpr int kUnit = kThreads * 4;          // 4 entries per thread
+constexpr int kUnits = kStepSpan / kUnit;    // of a work item
+static_assert(kUnits * kUnit == kStepSpan, "whole units");
+// A step that moves more than the 256 MB Infinity Cache streams with
+// non-temporal accesses; a smaller one stays cacheable.
+constexpr double kStreamBytes = 256.0 * 1024 * 1024;
 
-// Eight entries from e0 on (missing ones read as 0).
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+// Pointers that a kernel reads from a table carry no address space; these
+// say that they are global memory (else every access is a flat one), and,
+// for a kernel's tables and scalars, that nothing writes them while it runs
+// (so that uniform ones take scalar loads).
+#define SM_GLOBAL __attribute__((address_space(1)))
+#define SM_CONST __attribute__((address_space(4)))
 template <typename T>
-__device__ __forceinline__ void get8(const T* p, int64_t e0, int64_t count, bool vec, float* v) {
-  if (vec && e0 + 8 <= count) {
-    load8<T>(p + e0, v);
+__device__ __forceinline__ T load_const(const T* p) {
+  static_assert(sizeof(T) % 4 == 0, "whole words");
+  const SM_CONST uint32_t* q = (const SM_CONST uint32_t*)reinterpret_cast<uintptr_t>(p);
+  uint32_t w[sizeof(T) / 4];
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(T) / 4; ++i) w[i] = q[i];
+  T v;
+  __builtin_memcpy(&v, w, sizeof(T));
+  return v;
+}
+
+template <bool NT, typename V, typename P>
+__device__ __forceinline__ V load_v(const SM_GLOBAL P* p) {
+  if constexpr (NT) return __builtin_nontemporal_load((const SM_GLOBAL V*)p);
+  else return *(const SM_GLOBAL V*)p;
+}
+template <bool NT, typename V, typename P>
+__device__ __forceinline__ void store_v(SM_GLOBAL P* p, V v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, (SM_GLOBAL V*)p);
+  else *(SM_GLOBAL V*)p = v;
+}
+// A table's pointer, moved by a uniform number of entries.
+template <typename T>
+__device__ __forceinline__ SM_GLOBAL T* at(void* p, int64_t e) {
+  return (SM_GLOBAL T*)reinterpret_cast<uintptr_t>(p) + e;
+}
+template <typename T>
+__device__ __forceinline__ const SM_GLOBAL T* at(const void* p, int64_t e) {
+  return (const SM_GLOBAL T*)reinterpret_cast<uintptr_t>(p) + e;
+}
+__device__ __forceinline__ void from_f32(SM_GLOBAL float* p, float v) { *p = v; }
+__device__ __forceinline__ void from_f32(SM_GLOBAL bf16_t* p, float v) { *p = f2bf(v); }
+
+// Two float32 values as a pair of bf16 ones, to nearest even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x2 r;
+  r[0] = (__bf16)a;
+  r[1] = (__bf16)b;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Four entries as they are stored: two words of bf16 ones, four of float32.
+template <typename T>
+struct Raw4 {
+  typedef u32x4 type;
+};
+template <>
+struct Raw4<bf16_t> {
+  typedef u32x2 type;
+};
+__device__ __forceinline__ void expand4(u32x4 a, float* v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a[e]);
+}
+__device__ __forceinline__ void expand4(u32x2 a, float* v) {
+  v[0] = __uint_as_float(a.x << 16);
+  v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(a.y << 16);
+  v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+}
+
+// Four entries from p + l on, of which `left` from p on exist.  full: all of
+// them do, and the address takes one access; otherwise missing ones read as
+// 0 and are not written.  p is uniform and l the lane's offset, so that the
+// addresses are a scalar base and a 32-bit offset.
+template <typename T, bool NT>
+__device__ __forceinline__ typename Raw4<T>::type get4(const SM_GLOBAL T* p, uint32_t l,
+                                                       uint32_t left, bool full) {
+  typedef typename Raw4<T>::type V;
+  if (full) return load_v<NT, V>(p + l);
+  V a = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (l + e >= left) continue;
+    if constexpr (sizeof(T) == 2) a[e >> 1] |= (uint32_t)p[l + e] << (16 * (e & 1));
+    else a[e] = __float_as_uint(p[l + e]);
+  }
+  return a;
+}
+template <typename T, bool NT>
+__device__ __forceinline__ void put4(SM_GLOBAL T* p, uint32_t l, uint32_t left, bool full,
+                                     const float* v) {
+  if (full) {
+    if constexpr (sizeof(T) == 2) {
+      store_v<NT>(p + l, u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])});
+    } else {
+      store_v<NT>(p + l, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                               __float_as_uint(v[2]), __float_as_uint(v[3])});
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e0 + e < count ? Elem<T>::load(p + e0 + e) : 0.f;
+    for (int e = 0; e < 4; ++e)
+      if (l + e < left) from_f32(p + l + e, v[e]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void put8(T* p, int64_t e0, int64_t count, bool vec, const float* v) {
-  if (vec && e0 + 8 <= count) {
-    store8<T>(p + e0, v);
-  } else {
+// Four codes as a word, or four bf16 values as two.
+template <bool NT>
+__device__ __forceinline__ uint32_t get4_codes(const SM_GLOBAL uint8_t* p, uint32_t l,
+                                               uint32_t left, bool full) {
+  if (full) return load_v<NT, uint32_t>(p + l);
+  uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e0 + e < count) Elem<T>::store(p + e0 + e, v[e]);
-  }
+  for (int e = 0; e < 4; ++e)
+    if (l + e < left) w |= (uint32_t)p[l + e] << (8 * e);
+  return w;
 }
-// Eight codes, as two words (missing ones read as 0).
-__device__ __forceinline__ uint2 get8_codes(const uint8_t* p, int64_t e0, int64_t count,
-                                            bool vec) {
-  if (vec && e0 + 8 <= count) return *reinterpret_cast<const uint2*>(p + e0);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e0 + e < count) w[e >> 2] |= (uint32_t)p[e0 + e] << (8 * (e & 3));
-  return make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void put8_codes(uint8_t* p, int64_t e0, int64_t count, bool vec,
-                                           uint2 c) {
-  if (vec && e0 + 8 <= count) {
-    *reinterpret_cast<uint2*>(p + e0) = c;
+template <bool NT>
+__device__ __forceinline__ void put4_codes(SM_GLOBAL uint8_t* p, uint32_t l, uint32_t left,
+                                           bool full, uint32_t c) {
+  if (full) {
+    store_v<NT>(p + l, c);
     return;
   }
-  const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e0 + e < count) p[e0 + e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+  for (int e = 0; e < 4; ++e)
+    if (l + e < left) p[l + e] = (uint8_t)(c >> (8 * e));
+}
+template <bool NT>
+__device__ __forceinline__ void put4_bf16(SM_GLOBAL bf16_t* p, uint32_t l, uint32_t left,
+                                          bool full, uint32_t lo, uint32_t hi) {
+  if (full) {
+    store_v<NT>(p + l, u32x2{lo, hi});
+    return;
+  }
+  const uint32_t w[2] = {lo, hi};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (l + e < left) p[l + e] = (bf16_t)(w[e >> 1] >> (16 * (e & 1)));
+}
+
+// ------------------------------------------------------------------ random bits
+//
+// r = mix32(entry ^ key) gives m 16 bits (its low half) and v 16 (its high
+// half); mix32(r ^ 0x9E3779B1) gives the weight 16.  Written with y, the
+// value before mix32's last step, r = y ^ (y >> 16): r's high half is y's,
+// and since that step undoes itself the second mixing's first step leaves
+// y ^ (C ^ (C >> 16)), C = 0x9E3779B1.
+
+// y of entries e0 .. e0 + 3, e0 a multiple of 4.  The first multiplication
+// is done once: (e0 + i) ^ key differs from e0 ^ key in its two low bits,
+// which the first shift does not reach, and flipping bit b of a factor adds
+// or subtracts 2^b times the other.
+__device__ __forceinline__ void random4(uint32_t e0, uint32_t key, uint32_t* y) {
+  constexpr uint32_t A = 0x9E3779B1u;
+  uint32_t x = e0 ^ key;
+  x ^= x >> 16;
+  const uint32_t s0 = (x & 1u) ? 0u - A : A, s1 = (x & 2u) ? 0u - 2u * A : 2u * A;
+  y[0] = x * A;
+  y[1] = y[0] + s0;
+  y[2] = y[0] + s1;
+  y[3] = y[2] + s0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = (y[e] ^ (y[e] >> 15)) * 0x85A308D3u;
+}
+// Seeds of the hardware's stochastic conversions, which add a seed's top
+// bits below the result's last one and truncate: 16 random bits and a half
+// below them for the codes (codes' own values stay), 16 for bf16.
+__device__ __forceinline__ uint32_t seed_v(uint32_t y) { return (y & 0xFFFF0000u) | 0x8000u; }
+__device__ __forceinline__ uint32_t seed_m(uint32_t y) { return seed_v(y) ^ (y << 16); }
+__device__ __forceinline__ uint32_t seed_w(uint32_t y) {
+  uint32_t x = (y ^ (0x9E3779B1u ^ (0x9E3779B1u >> 16))) * 0x9E3779B1u;
+  x = (x ^ (x >> 15)) * 0x85A308D3u;
+  // the top half: the low one of x ^ (x >> 16); as a rotation, since a shift
+  // would be drawn into one more multiplication
+  return x ^ __builtin_amdgcn_alignbit(x, x, 16);
+}
+__device__ __forceinline__ uint32_t bf16_pair_stochastic(float a, float b, uint32_t ya,
+                                                         uint32_t yb) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x2 r = {};
+  r = __builtin_amdgcn_cvt_sr_bf16_f32(r, a, seed_w(ya), false);
+  r = __builtin_amdgcn_cvt_sr_bf16_f32(r, b, seed_w(yb), true);
+  return __builtin_bit_cast(uint32_t, r);
 }
 
 // ------------------------------------------------------------------ 8-bit codes
-
-// Values of eight codes times the block's scale (a power of two: exact).
-__device__ __forceinline__ void decode8_m(uint2 c, float scale, float* v) {
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(w[q], false);
-    const auto b = __builtin_amdgcn_cvt_pk_f32_fp8(w[q], true);
-    v[4 * q] = a[0] * scale;
-    v[4 * q + 1] = a[1] * scale;
-    v[4 * q + 2] = b[0] * scale;
-    v[4 * q + 3] = b[1] * scale;
-  }
-}
-__device__ __forceinline__ void decode8_v(uint2 c, float scale, float* v) {
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const auto a = __builtin_amdgcn_cvt_pk_f32_bf8(w[q], false);
-    const auto b = __builtin_amdgcn_cvt_pk_f32_bf8(w[q], true);
-    v[4 * q] = a[0] * scale;
-    v[4 * q + 1] = a[1] * scale;
-    v[4 * q + 2] = b[0] * scale;
-    v[4 * q + 3] = b[1] * scale;
-  }
-}
+//
+// The conversions are gfx950's scaled ones: they multiply (decode) or divide
+// (encode) by the scale, a power of two, so nothing but the code's own
+// rounding is lost.
 
 constexpr uint32_t kInf = 0x7F800000u;
 
-// The largest finite magnitude of the thread's eight values, as bits
-// (magnitudes order like their bits).
-__device__ __forceinline__ uint32_t amax8(const float* v) {
+__device__ __forceinline__ void decode4_m(uint32_t c, float scale, float* v) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, true);
+  v[0] = a[0];
+  v[1] = a[1];
+  v[2] = b[0];
+  v[3] = b[1];
+}
+__device__ __forceinline__ void decode4_v(uint32_t c, float scale, float* v) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(c, scale, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(c, scale, true);
+  v[0] = a[0];
+  v[1] = a[1];
+  v[2] = b[0];
+  v[3] = b[1];
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The wave's largest value, uniform.  Within rows of 16 lanes by
+// permutations, then rows 0 -> 1 and 2 -> 3, then both into row 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  // lanes that the control leaves out get 0, the identity
+  return umax(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = dpp_max<0xB1, 0xF>(x);    // quad_perm [1, 0, 3, 2]
+  x = dpp_max<0x4E, 0xF>(x);    // quad_perm [2, 3, 0, 1]
+  x = dpp_max<0x141, 0xF>(x);   // row_half_mirror
+  x = dpp_max<0x140, 0xF>(x);   // row_mirror
+  x = dpp_max<0x142, 0xA>(x);   // row_bcast:15
+  x = dpp_max<0x143, 0xC>(x);   // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// Largest magnitude of a block's first moments, and largest second moment,
+// as bits (magnitudes order like their bits).  kInf or more if some value is
+// not finite (a negative second moment counts as such).
+__device__ __forceinline__ uint32_t amax_m(const float* m) {
+  int pos = 0;         // the largest positive value; any negative one is
+  uint32_t any = 0;    // above it as unsigned, the largest magnitude on top
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t b = __float_as_uint(m[e]);
+    pos = (int)b > pos ? (int)b : pos;
+    any = umax(any, b);
+  }
+  return wave_max(umax((uint32_t)pos, any & 0x7FFFFFFFu));
+}
+__device__ __forceinline__ uint32_t amax_v(const float* v) {
   uint32_t a = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = __float_as_uint(v[e]) & 0x7FFFFFFFu;
-    a = b < kInf && b > a ? b : a;
-  }
-  return a;
+  for (int e = 0; e < 4; ++e) a = umax(a, __float_as_uint(v[e]));
+  return wave_max(a);
 }
-// ... of the 32 threads that share a block.  All lanes must call it.
-__device__ __forceinline__ uint32_t block_amax(uint32_t a) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t b = (uint32_t)__shfl_xor((int)a, o, 64);
-    a = b > a ? b : a;
-  }
-  return a;
-}
-// Biased exponent (>= 1) of the block's scale: the smallest with amax <=
-// 1.75 * 2^top * scale.
-__device__ __forceinline__ uint32_t scale_exp(uint32_t amax, int top) {
+
+// The block's scale, 2^e with e >= -126 the smallest with amax <= 1.75 *
+// 2^top * 2^e.
+__device__ __forceinline__ float scale_for(uint32_t amax, int top) {
   const int e = (int)(amax >> 23) - top + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return (uint32_t)(e < 1 ? 1 : e);
-}
-__device__ __forceinline__ float exp_value(uint32_t e) { return __uint_as_float(e << 23); }
-__device__ __forceinline__ float exp_recip(uint32_t e) { return __uint_as_float((254u - e) << 23); }
-
-// Code of a magnitude x (scaled by its block) with KEEP mantissa bits and
-// normals from 2^LOWEST on, rounded stochastically by 16 random bits r.
-// Dropping the low mantissa bits after adding random ones rounds up with the
-// probability that the dropped part is of a code's step (to 2^-17; codes'
-// own values stay).  Below 2^LOWEST the codes are equally spaced: x +
-// 2^LOWEST lies in a binade with just that spacing.
-template <int KEEP, int LOWEST>
-__device__ __forceinline__ uint32_t code_stochastic(float x, uint32_t r) {
-  constexpr int DROP = 23 - KEEP;
-  constexpr uint32_t BASE = (uint32_t)(127 + LOWEST) << KEEP;
-  const float lim = __uint_as_float((uint32_t)(127 + LOWEST) << 23);
-  const bool low = x < lim;
-  const uint32_t bits = __float_as_uint(low ? x + lim : x);
-  const uint32_t up = (r << (DROP - 16)) | (1u << (DROP - 17));
-  return ((bits + up) >> DROP) - (low ? BASE : BASE - (1u << KEEP));
+  return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }
 
-__device__ __forceinline__ uint32_t code_m(float m, float recip, uint32_t r) {
-  const uint32_t b = __float_as_uint(m);
-  if ((b & 0x7FFFFFFFu) >= kInf) return 0x7Fu;
-  const float x = __uint_as_float(b & 0x7FFFFFFFu) * recip;
-  return code_stochastic<3, -6>(x, r) | ((b >> 24) & 0x80u);
+// Four first / second moments (finite) as codes, rounded stochastically: up
+// with the probability that the dropped part is of a code's step, to 2^-17.
+// y: the entries' random bits.
+__device__ __forceinline__ uint32_t encode4_m(const float* m, float scale, const uint32_t* y) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(0u, m[0], seed_m(y[0]), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[1], seed_m(y[1]), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[2], seed_m(y[2]), scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[3], seed_m(y[3]), scale, 3);
 }
-__device__ __forceinline__ uint32_t code_v(float v, float recip, uint32_t r) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7FFFFFFFu) >= kInf) return b == kInf ? 0x7Cu : 0x7Fu;
-  if (!(v > 0.f)) return 0u;
-  const uint32_t c = code_stochastic<2, -14>(v * recip, r);
-  return c == 0u ? 1u : c;
+// A positive v takes at least the smallest code, 2^-16 of the scale: the
+// median of v, that floor and v * 2^300 (infinite, or 0 for v = 0).
+__device__ __forceinline__ float floor_v(float v, float least) {
+  return __builtin_amdgcn_fmed3f(v, least, __builtin_amdgcn_ldexpf(v, 300));
+}
+__device__ __forceinline__ uint32_t encode4_v(const float* v, float scale, const uint32_t* y) {
+  const float least = scale * 0x1p-16f;
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(0u, floor_v(v[0], least), seed_v(y[0]),
+                                                        scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[1], least), seed_v(y[1]), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[2], least), seed_v(y[2]), scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[3], least), seed_v(y[3]), scale, 3);
+}
+__device__ __forceinline__ float reciprocal(float scale) {   // of 2^e, e >= -126: exact
+  return __uint_as_float(0x7F000000u - __float_as_uint(scale));
+}
+// The same to nearest even.
+__device__ __forceinline__ uint32_t encode4_m_nearest(const float* m, float scale) {
+  const float q = reciprocal(scale);
+  int c = __builtin_amdgcn_cvt_pk_fp8_f32(m[0] * q, m[1] * q, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2] * q, m[3] * q, c, true);
+}
+__device__ __forceinline__ uint32_t encode4_v_nearest(const float* v, float scale) {
+  const float q = reciprocal(scale), least = scale * 0x1p-16f;
+  int c = __builtin_amdgcn_cvt_pk_bf8_f32(floor_v(v[0], least) * q, floor_v(v[1], least) * q, 0,
+                                          false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(floor_v(v[2], least) * q,
+                                                   floor_v(v[3], least) * q, c, true);
 }
 
-// bf16 of v rounded stochastically by 16 random bits.
-__device__ __forceinline__ bf16_t f2bf_stochastic(float v, uint32_t r16) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & kInf) == kInf) return f2bf(v);
-  return (bf16_t)((b + r16) >> 16);
+// A block with values that are not finite: those (and negative second
+// moments) are taken out before the codes are made, and put in afterwards:
+// NaN for m; NaN, infinity or 0 for v.
+__device__ __forceinline__ void split_m(float* m, uint32_t* keep, uint32_t* put) {
+  *keep = 0xFFFFFFFFu;
+  *put = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((__float_as_uint(m[e]) & 0x7FFFFFFFu) < kInf) continue;
+    m[e] = 0.f;
+    *keep &= ~(0xFFu << (8 * e));
+    *put |= 0x7Fu << (8 * e);
+  }
+}
+__device__ __forceinline__ void split_v(float* v, uint32_t* keep, uint32_t* put) {
+  *keep = 0xFFFFFFFFu;
+  *put = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t b = __float_as_uint(v[e]);
+    if (b < kInf) continue;
+    v[e] = 0.f;
+    *keep &= ~(0xFFu << (8 * e));
+    *put |= (b == kInf ? 0x7Cu : (b & 0x7FFFFFFFu) > kInf ? 0x7Fu : 0u) << (8 * e);
+  }
+}
+
+struct Codes {
+  uint32_t m, v;
+  float ms, vs;
+};
+template <bool STOCHASTIC>
+__device__ __forceinline__ void encode_finite(const float* m, const float* v, uint32_t am,
+                                              uint32_t av, const uint32_t* y, Codes& c) {
+  c.ms = scale_for(am, 8);
+  c.vs = scale_for(av, 15);
+  if constexpr (STOCHASTIC) {
+    c.m = encode4_m(m, c.ms, y);
+    c.v = encode4_v(v, c.vs, y);
+  } else {
+    c.m = encode4_m_nearest(m, c.ms);
+    c.v = encode4_v_nearest(v, c.vs);
+  }
+}
+// Codes and scales of the wave's block; y: random bits (null: to nearest).
+// All lanes of the wave must call it.
+template <bool STOCHASTIC>
+__device__ __forceinline__ Codes encode_block(float* m, float* v, const uint32_t* y) {
+  const uint32_t am = amax_m(m), av = amax_v(v);
+  Codes c;
+  if (__builtin_expect(am >= kInf || av >= kInf, 0)) {   // uniform
+    uint32_t km, kv, pm, pv;
+    split_m(m, &km, &pm);
+    split_v(v, &kv, &pv);
+    encode_finite<STOCHASTIC>(m, v, amax_m(m), amax_v(v), y, c);
+    c.m = (c.m & km) | pm;
+    c.v = (c.v & kv) | pv;
+  } else {
+    encode_finite<STOCHASTIC>(m, v, am, av, y, c);
+  }
+  return c;
 }
 
 // ------------------------------------------------------------------ set tables
 
 __global__ __launch_bounds__(kThreads) void k_set_fill(FillTbl t, int index0, ParamEnt* ents,
-                                                       WorkItem* items, int units) {
+                                                       WorkItem* items, WorkItem* norm_items) {
   const int q = blockIdx.y;
-  const ParamEnt& e = t.e[q];
-  if (blockIdx.x == 0 && threadIdx.x == 0) ents[index0 + q] = e;
-  const int64_t span = (int64_t)units * kUnit;
-  const int64_t n = (e.count + span - 1) / span;
+  const int64_t count = t.e[q].count;
+  if (blockIdx.x == 0 && threadIdx.x == 0) ents[index0 + q] = t.e[q];
+  const int64_t n = (count + kStepSpan - 1) / kStepSpan;
+  const int64_t nn = (count + kNormSpan - 1) / kNormSpan;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * kThreads) {
     WorkItem it;
     it.tensor = (uint32_t)(index0 + q);
     it.chunk = (uint32_t)i;
     items[t.first[q] + i] = it;
+    if (i < nn) norm_items[t.norm_first[q] + i] = it;
   }
 }
 
@@ -189,140 +418,198 @@ __global__ void k_adamw_prep(sm_adamw_config c, int64_t* step, const float* gsca
   if (!a.skip) *step = t;
 }
 
-// The mean gradient of eight entries, times the step's factor f =
-// gscale / M.  Several workers' gradients are summed in float64: the sum
-// does not depend on their order, and is rounded once.
-template <typename TG>
-__device__ __forceinline__ void mean_grad8(const ParamEnt& p, int M, int64_t e0, bool vec,
-                                           float f, float* g) {
-  const TG* gp = static_cast<const TG*>(p.g);
-  if (M == 1) {
-    get8<TG>(gp, e0, p.count, vec, g);
-  } else {
-    double s[8] = {};
-    for (int k = 0; k < M; ++k) {
-      float x[8];
-      get8<TG>(gp + k * p.gstride, e0, p.count, vec, x);
+// Sum of the workers' gradients of four entries, in float64: it does not
+// depend on their order, and is rounded once.
+template <typename TG, bool NT>
+__device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0, uint32_t l,
+                                           uint32_t left, bool full) {
+  const SM_GLOBAL TG* gp = at<TG>(p.g, u0);
+  double s[4] = {};
+#pragma unroll 4
+  for (int k = 0; k < M; ++k) {
+    float x[4];
+    expand4(get4<TG, NT>(gp + k * p.gstride, l, left, full), x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += (double)x[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = (float)s[e];
+    for (int e = 0; e < 4; ++e) s[e] += (double)x[e];
   }
+  u32x4 g;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g[e] = g[e] * f;
+  for (int e = 0; e < 4; ++e) g[e] = __float_as_uint((float)s[e]);
+  return g;
 }
 
 // The moments' averages and the weights' change, the same for both kinds of
 // states.  sqrt and the reciprocal are the hardware's (each within an ulp):
 // their error is relative to one step's change, not to the weight.
-__device__ __forceinline__ void adamw8(const AdamwScalars& a, float keep, float step,
+__device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float step,
                                        const float* g, float* m, float* v, float* w) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 4; ++e) {
     m[e] = a.b1 * m[e] + a.a1 * g[e];
     v[e] = a.b2 * v[e] + a.a2 * (g[e] * g[e]);
-    const float den = __builtin_amdgcn_sqrtf(v[e]) * a.root + a.eps;
-    w[e] = w[e] * keep - step * (m[e] * __builtin_amdgcn_rcpf(den));
+    const float den = __fmaf_rn(__builtin_amdgcn_sqrtf(v[e]), a.root, a.eps);
+    w[e] = __fmaf_rn(-step, m[e] * __builtin_amdgcn_rcpf(den), w[e] * keep);
   }
 }
 
-template <typename TW, typename TG, bool FP8>
-__device__ __forceinline__ void adamw_unit(const ParamEnt& p, const AdamwScalars& a, int M,
-                                           float f, float keep, float step, uint32_t key0,
-                                           int64_t e0, bool vec) {
-  float g[8], m[8], v[8], w[8];
-  mean_grad8<TG>(p, M, e0, vec, f, g);
-  const int64_t blk = e0 / kStateBlock;
-  const bool inside = e0 < p.count;
-  if constexpr (FP8) {
-    const uint2 mc = get8_codes(static_cast<const uint8_t*>(p.m), e0, p.count, vec);
-    const uint2 vc = get8_codes(static_cast<const uint8_t*>(p.v), e0, p.count, vec);
-    decode8_m(mc, inside ? p.ms[blk] : 0.f, m);
-    decode8_v(vc, inside ? p.vs[blk] : 0.f, v);
-  } else {
-    get8<float>(static_cast<const float*>(p.m), e0, p.count, vec, m);
-    get8<float>(static_cast<const float*>(p.v), e0, p.count, vec, v);
-  }
-  const bool master = sizeof(TW) == 2 && p.master;
-  if (master) get8<float>(p.master, e0, p.count, vec, w);
-  else get8<TW>(static_cast<const TW*>(p.w), e0, p.count, vec, w);
+// What a thread holds of one unit (1024 entries of the workgroup, 256 of the
+// wave: an 8-bit state's block), as loaded: nothing waits for these loads
+// until finish_unit.  TS: the weights that are read; TG: the gradients, or
+// float for the sum of several workers'.
+template <typename TS, typename TG, bool FP8>
+struct Held {
+  typename Raw4<TG>::type g;
+  typename Raw4<TS>::type w;
+  u32x4 m, v;
+  uint32_t mc, vc;
+  float ms, vs;
+};
 
-  adamw8(a, keep, step, g, m, v, w);
-
-  uint32_t r[8];
-  if (FP8 || (sizeof(TW) == 2 && a.stochastic)) {
-    const uint32_t key = mix_key(key0, (uint32_t)((uint64_t)e0 >> 32));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = mix32(((uint32_t)e0 + e) ^ key);
-  }
-  if constexpr (FP8) {
-    const uint32_t em = scale_exp(block_amax(amax8(m)), 8);
-    const uint32_t ev = scale_exp(block_amax(amax8(v)), 15);
-    const float rm = exp_recip(em), rv = exp_recip(ev);
-    uint32_t cm[2] = {0u, 0u}, cv[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cm[e >> 2] |= code_m(m[e], rm, r[e] & 0xFFFFu) << (8 * (e & 3));
-      cv[e >> 2] |= code_v(v[e], rv, r[e] >> 16) << (8 * (e & 3));
-    }
-    put8_codes(static_cast<uint8_t*>(p.m), e0, p.count, vec, make_uint2(cm[0], cm[1]));
-    put8_codes(static_cast<uint8_t*>(p.v), e0, p.count, vec, make_uint2(cv[0], cv[1]));
-    if (inside && (threadIdx.x & 31) == 0) {
-      p.ms[blk] = exp_value(em);
-      p.vs[blk] = exp_value(ev);
-    }
-  } else {
-    put8<float>(static_cast<float*>(p.m), e0, p.count, vec, m);
-    put8<float>(static_cast<float*>(p.v), e0, p.count, vec, v);
-  }
-  if (master) {
-    put8<float>(p.master, e0, p.count, vec, w);
-  } else if (sizeof(TW) == 2 && a.stochastic) {
-    // the rounded values are bf16 values, which the store below keeps
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e] = bf2f(f2bf_stochastic(w[e], mix32(r[e] ^ 0x9E3779B1u) & 0xFFFFu));
-  }
-  put8<TW>(static_cast<TW*>(p.w), e0, p.count, vec, w);
+// Entries of a unit from u0 on, at most a unit.
+__device__ __forceinline__ uint32_t unit_left(int64_t count, int64_t u0) {
+  const int64_t n = count - u0;
+  return (uint32_t)(n < kUnit ? n : kUnit);
 }
 
-template <bool FP8>
+// full: the thread has all four entries, at addresses that take one access.
+// ONE: a single worker.
+template <typename TS, typename TG, bool FP8, bool ONE, bool NT, typename H>
+__device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, uint32_t left,
+                                          bool full, H& h) {
+  const uint32_t l = threadIdx.x * 4;
+  if constexpr (FP8) {
+    // the wave's block, uniform
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t blk = u0 / kStateBlock + wave;
+    const bool inside = wave * kStateBlock < left;
+    h.mc = get4_codes<NT>(at<uint8_t>(p.m, u0), l, left, full);
+    h.vc = get4_codes<NT>(at<uint8_t>(p.v, u0), l, left, full);
+    h.ms = inside ? *at<float>(p.ms, blk) : 1.0f;
+    h.vs = inside ? *at<float>(p.vs, blk) : 1.0f;
+  } else {
+    h.m = get4<float, NT>(at<float>(p.m, u0), l, left, full);
+    h.v = get4<float, NT>(at<float>(p.v, u0), l, left, full);
+  }
+  h.w = get4<TS, NT>(at<TS>(sizeof(TS) == 4 && p.master ? p.master : p.w, u0), l, left, full);
+  if constexpr (ONE) h.g = get4<TG, NT>(at<TG>(p.g, u0), l, left, full);
+  else h.g = sum_grad4<TG, NT>(p, M, u0, l, left, full);
+}
+
+// TW: the weights' type.  TS float32 with bf16 weights: they have a master.
+template <typename TW, typename TS, bool FP8, bool NT, typename H>
+__device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalars& a, float f,
+                                            float keep, float step, uint32_t key, int64_t u0,
+                                            uint32_t left, bool full, const H& h) {
+  const uint32_t l = threadIdx.x * 4;
+  float g[4], w[4], m[4], v[4];
+  expand4(h.g, g);
+  expand4(h.w, w);
+  if constexpr (FP8) {
+    decode4_m(h.mc, h.ms, m);
+    decode4_v(h.vc, h.vs, v);
+  } else {
+    expand4(h.m, m);
+    expand4(h.v, v);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) g[e] = g[e] * f;
+  adamw4(a, keep, step, g, m, v, w);
+  constexpr bool SR_W = sizeof(TS) == 2, MASTER = sizeof(TW) == 2 && sizeof(TS) == 4;
+  uint32_t y[4];
+  if (FP8 || (SR_W && a.stochastic)) random4((uint32_t)u0 + l, key, y);
+  SM_GLOBAL TW* wp = at<TW>(p.w, u0);
+  if constexpr (SR_W) {
+    if (a.stochastic)
+      put4_bf16<NT>(wp, l, left, full, bf16_pair_stochastic(w[0], w[1], y[0], y[1]),
+                    bf16_pair_stochastic(w[2], w[3], y[2], y[3]));
+    else
+      put4<TW, NT>(wp, l, left, full, w);
+  } else {
+    put4<TW, NT>(wp, l, left, full, w);
+  }
+  if constexpr (MASTER) put4<float, NT>(at<float>(p.master, u0), l, left, full, w);
+  if constexpr (FP8) {
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t blk = u0 / kStateBlock + wave;
+    const Codes c = encode_block<true>(m, v, y);
+    put4_codes<NT>(at<uint8_t>(p.m, u0), l, left, full, c.m);
+    put4_codes<NT>(at<uint8_t>(p.v, u0), l, left, full, c.v);
+    if (wave * kStateBlock < left && (threadIdx.x & 63) == 0) {
+      *at<float>(p.ms, blk) = c.ms;
+      *at<float>(p.vs, blk) = c.vs;
+    }
+  } else {
+    put4<float, NT>(at<float>(p.m, u0), l, left, full, m);
+    put4<float, NT>(at<float>(p.v, u0), l, left, full, v);
+  }
+}
+
+template <bool FP8, bool NT>
 __global__ __launch_bounds__(kThreads) void k_adamw(ParamSetDev set, AdamwScalars arg, bool device,
                                                     const float* gscale, const float* lr_scale) {
-  const WorkItem it = set.items[blockIdx.x];
-  const ParamEnt p = set.ents[it.tensor];
-  const AdamwScalars a = device ? *set.scalars : arg;
-  const float gs = gscale ? *gscale : 1.0f;
-  const float ls = lr_scale ? *lr_scale : 1.0f;
+  const WorkItem it = load_const(set.items + blockIdx.x);
+  const ParamEnt p = load_const(set.ents + it.tensor);
+  AdamwScalars a = arg;
+  if (device) a = load_const(set.scalars);
+  const float gs = gscale ? load_const(gscale) : 1.0f;
+  const float ls = lr_scale ? load_const(lr_scale) : 1.0f;
   if (a.skip || !is_finite(gs) || !is_finite(ls)) return;
   const float mult = ls * p.lr_mult;
   const float keep = (float)(1.0 - (double)(a.lr * mult) * (double)p.wd);
   const float step = a.step * mult;
-  const float f = gs * (1.0f / (float)set.M);
-  const uint32_t key0 = mix_key(a.key, it.tensor);
+  const float f = gs * set.inv_M;
   const bool vec = p.flags & kPF_VEC;
-  const int64_t first = (int64_t)it.chunk * set.units * kUnit;
-  for (int u = 0; u < set.units; ++u) {
-    const int64_t u0 = first + (int64_t)u * kUnit;
-    if (u0 >= p.count) break;
-    const int64_t e0 = u0 + threadIdx.x * 8;
-    auto run = [&](auto tw, auto tg) {
-      typedef decltype(tw) TW;
-      typedef decltype(tg) TG;
-      if (FP8 && (p.flags & kPF_FP8))
-        adamw_unit<TW, TG, FP8>(p, a, set.M, f, keep, step, key0, e0, vec);
-      else
-        adamw_unit<TW, TG, false>(p, a, set.M, f, keep, step, key0, e0, vec);
-    };
-    if (p.flags & kPF_W16) {
-      if (p.flags & kPF_G16) run(bf16_t(), bf16_t());
-      else run(bf16_t(), float());
+  const int64_t first = (int64_t)it.chunk * kStepSpan;
+  const uint32_t key = mix_key(mix_key(a.key, it.tensor), (uint32_t)((uint64_t)first >> 32));
+  auto item = [&](auto tw, auto ts, auto tg, auto fp8) {
+    typedef decltype(tw) TW;
+    typedef decltype(ts) TS;
+    typedef decltype(tg) TG;
+    constexpr bool F8 = decltype(fp8)::value;
+    if (vec && first + kStepSpan <= p.count) {
+      if (set.M == 1) {
+        // every unit's loads are in flight before the first one is used
+        Held<TS, TG, F8> h[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+          load_unit<TS, TG, F8, true, NT>(p, 1, first + u * kUnit, kUnit, true, h[u]);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u)
+          finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key, first + u * kUnit, kUnit, true,
+                                      h[u]);
+      } else {
+        for (int u = 0; u < kUnits; ++u) {
+          Held<TS, float, F8> h;
+          load_unit<TS, TG, F8, false, NT>(p, set.M, first + u * kUnit, kUnit, true, h);
+          finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key, first + u * kUnit, kUnit, true, h);
+        }
+      }
     } else {
-      if (p.flags & kPF_G16) run(float(), bf16_t());
-      else run(float(), float());
+      for (int64_t u0 = first; u0 < first + kStepSpan && u0 < p.count; u0 += kUnit) {
+        const uint32_t left = unit_left(p.count, u0);
+        const bool full = vec && threadIdx.x * 4 + 4 <= left;
+        Held<TS, float, F8> h;
+        load_unit<TS, TG, F8, false, false>(p, set.M, u0, left, full, h);
+        finish_unit<TW, TS, F8, false>(p, a, f, keep, step, key, u0, left, full, h);
+      }
+    }
+  };
+  auto grads = [&](auto tw, auto ts, auto fp8) {
+    if (p.flags & kPF_G16) item(tw, ts, bf16_t(), fp8);
+    else item(tw, ts, float(), fp8);
+  };
+  auto weights = [&](auto fp8) {
+    if (!(p.flags & kPF_W16)) grads(float(), float(), fp8);
+    else if (p.master) grads(bf16_t(), float(), fp8);
+    else grads(bf16_t(), bf16_t(), fp8);
+  };
+  if constexpr (FP8) {
+    if (p.flags & kPF_FP8) {
+      weights(std::true_type());
+      return;
     }
   }
+  weights(std::false_type());
 }
 
 // ------------------------------------------------------------------ gradient norm
@@ -336,24 +623,33 @@ __device__ double block_sum64(double v, double* red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// Sum of squares of the mean gradient over the thread's entries of a unit.
+template <typename TG>
+__device__ __forceinline__ float sumsq4(const ParamEnt& p, int M, int64_t u0, uint32_t left,
+                                        bool vec) {
+  const uint32_t l = threadIdx.x * 4;
+  const bool full = vec && l + 4 <= left;
+  float g[4];
+  if (M == 1) expand4(get4<TG, false>(at<TG>(p.g, u0), l, left, full), g);
+  else expand4(sum_grad4<TG, false>(p, M, u0, l, left, full), g);
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s = __fmaf_rn(g[e], g[e], s);
+  return s;
+}
+
 __global__ __launch_bounds__(kThreads) void k_grad_sumsq(ParamSetDev set, double* parts) {
   __shared__ double red[4];
   double acc = 0.0;
-  for (int i = blockIdx.x; i < set.nitems; i += gridDim.x) {
-    const WorkItem it = set.items[i];
-    const ParamEnt p = set.ents[it.tensor];
+  for (int i = blockIdx.x; i < set.norm_items; i += gridDim.x) {
+    const WorkItem it = load_const(set.norm_at + i);
+    const ParamEnt p = load_const(set.ents + it.tensor);
     const bool vec = p.flags & kPF_VEC;
-    const int64_t first = (int64_t)it.chunk * set.units * kUnit;
-    for (int u = 0; u < set.units; ++u) {
-      const int64_t e0 = first + (int64_t)u * kUnit + threadIdx.x * 8;
-      if (e0 >= p.count) break;
-      float g[8];
-      if (p.flags & kPF_G16) mean_grad8<bf16_t>(p, set.M, e0, vec, 1.0f, g);
-      else mean_grad8<float>(p, set.M, e0, vec, 1.0f, g);
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = __fmaf_rn(g[e], g[e], s);
-      acc += (double)s;
+    const int64_t first = (int64_t)it.chunk * kNormSpan;
+    for (int64_t u0 = first; u0 < first + kNormSpan && u0 < p.count; u0 += kUnit) {
+      const uint32_t left = unit_left(p.count, u0);
+      acc += (double)((p.flags & kPF_G16) ? sumsq4<bf16_t>(p, set.M, u0, left, vec)
+                                          : sumsq4<float>(p, set.M, u0, left, vec));
     }
   }
   const double s = block_sum64(acc, red);
@@ -378,70 +674,56 @@ __global__ __launch_bounds__(kThreads) void k_norm_finalize(const double* parts,
 
 // ------------------------------------------------------------------ 8-bit states
 
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_state8_pack(const float* m, const float* v,
                                                           int64_t count, uint8_t* m8, uint8_t* v8,
                                                           float* ms, float* vs, bool vec) {
+  const uint32_t l = threadIdx.x * 4;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnit; u0 < count; u0 += (int64_t)gridDim.x * kUnit) {
-    const int64_t e0 = u0 + threadIdx.x * 8;
-    float x[8], y[8];
-    get8<float>(m, e0, count, vec, x);
-    get8<float>(v, e0, count, vec, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = y[e] < 0.f ? 0.f : y[e];
-    const uint32_t em = scale_exp(block_amax(amax8(x)), 8);
-    const uint32_t ev = scale_exp(block_amax(amax8(y)), 15);
-    const float rm = exp_recip(em), rv = exp_recip(ev);
-    uint32_t cm[2], cv[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      float* xs = x + 4 * q;
-      float* ys = y + 4 * q;
-      int c = __builtin_amdgcn_cvt_pk_fp8_f32(xs[0] * rm, xs[1] * rm, 0, false);
-      cm[q] = __builtin_amdgcn_cvt_pk_fp8_f32(xs[2] * rm, xs[3] * rm, c, true);
-      c = __builtin_amdgcn_cvt_pk_bf8_f32(ys[0] * rv, ys[1] * rv, 0, false);
-      cv[q] = __builtin_amdgcn_cvt_pk_bf8_f32(ys[2] * rv, ys[3] * rv, c, true);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t sh = 8 * e, bx = __float_as_uint(xs[e]) & 0x7FFFFFFFu;
-        const uint32_t by = __float_as_uint(ys[e]) & 0x7FFFFFFFu;
-        if (bx >= kInf) cm[q] = (cm[q] & ~(0xFFu << sh)) | (0x7Fu << sh);
-        if (by >= kInf) cv[q] = (cv[q] & ~(0xFFu << sh)) | ((by == kInf ? 0x7Cu : 0x7Fu) << sh);
-        else if (by != 0u && ((cv[q] >> sh) & 0xFFu) == 0u) cv[q] |= 1u << sh;
-      }
-    }
-    put8_codes(m8, e0, count, vec, make_uint2(cm[0], cm[1]));
-    put8_codes(v8, e0, count, vec, make_uint2(cv[0], cv[1]));
-    if (e0 < count && (threadIdx.x & 31) == 0) {
-      ms[e0 / kStateBlock] = exp_value(em);
-      vs[e0 / kStateBlock] = exp_value(ev);
+    const uint32_t left = unit_left(count, u0);
+    const bool full = vec && l + 4 <= left;
+    float x[4], y[4];
+    expand4(get4<float, NT>(at<float>(m, u0), l, left, full), x);
+    expand4(get4<float, NT>(at<float>(v, u0), l, left, full), y);
+    const Codes c = encode_block<false>(x, y, nullptr);
+    put4_codes<NT>(at<uint8_t>(m8, u0), l, left, full, c.m);
+    put4_codes<NT>(at<uint8_t>(v8, u0), l, left, full, c.v);
+    if (l < left && (threadIdx.x & 63) == 0) {
+      ms[u0 / kStateBlock + (threadIdx.x >> 6)] = c.ms;
+      vs[u0 / kStateBlock + (threadIdx.x >> 6)] = c.vs;
     }
   }
 }
 
+template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_state8_unpack(const uint8_t* m8, const uint8_t* v8,
                                                             const float* ms, const float* vs,
                                                             int64_t count, float* m, float* v,
                                                             bool vec) {
+  const uint32_t l = threadIdx.x * 4;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnit; u0 < count; u0 += (int64_t)gridDim.x * kUnit) {
-    const int64_t e0 = u0 + threadIdx.x * 8;
-    if (e0 >= count) continue;
-    float x[8], y[8];
-    decode8_m(get8_codes(m8, e0, count, vec), ms[e0 / kStateBlock], x);
-    decode8_v(get8_codes(v8, e0, count, vec), vs[e0 / kStateBlock], y);
-    put8<float>(m, e0, count, vec, x);
-    put8<float>(v, e0, count, vec, y);
+    const uint32_t left = unit_left(count, u0);
+    if (l >= left) continue;
+    const bool full = vec && l + 4 <= left;
+    const int64_t blk = u0 / kStateBlock + (threadIdx.x >> 6);
+    float x[4], y[4];
+    decode4_m(get4_codes<NT>(at<uint8_t>(m8, u0), l, left, full), ms[blk], x);
+    decode4_v(get4_codes<NT>(at<uint8_t>(v8, u0), l, left, full), vs[blk], y);
+    put4<float, NT>(at<float>(m, u0), l, left, full, x);
+    put4<float, NT>(at<float>(v, u0), l, left, full, y);
   }
 }
 
+// One workgroup per unit, up to a launch's limit of 2^32 threads.
 int unit_blocks(int64_t count) {
   const int64_t n = (count + kUnit - 1) / kUnit;
-  return (int)(n < 65536 ? n : 65536);
+  return (int)(n < (1 << 23) ? n : (1 << 23));
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool state8_vec(const void* m, const void* v, const void* m8, const void* v8) {
-  return aligned(m, 16) && aligned(v, 16) && aligned(m8, 8) && aligned(v8, 8);
+  return aligned(m, 16) && aligned(v, 16) && aligned(m8, 4) && aligned(v8, 4);
 }
 
 }  // namespace
@@ -449,14 +731,12 @@ bool state8_vec(const void* m, const void* v, const void* m8, const void* v8) {
 // ------------------------------------------------------------------ launchers
 
 sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, WorkItem* items,
-                          int units, hipStream_t s) {
+                          WorkItem* norm_items, hipStream_t s) {
   int64_t most = 1;
-  for (int q = 0; q < n; ++q) {
-    const int64_t span = (int64_t)units * kUnit;
-    most = std::max<int64_t>(most, (t.e[q].count + span - 1) / span);
-  }
+  for (int q = 0; q < n; ++q)
+    most = std::max<int64_t>(most, (t.e[q].count + kStepSpan - 1) / kStepSpan);
   const dim3 grid((unsigned)std::min<int64_t>((most + kThreads - 1) / kThreads, 1024), n);
-  hipLaunchKernelGGL(k_set_fill, grid, dim3(kThreads), 0, s, t, index0, ents, items, units);
+  hipLaunchKernelGGL(k_set_fill, grid, dim3(kThreads), 0, s, t, index0, ents, items, norm_items);
   return check_launch();
 }
 
@@ -467,26 +747,24 @@ sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float
 }
 
 sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool device,
-                       const float* gscale, const float* lr_scale, bool fp8, bool stream,
-                       double bytes, hipStream_t s) {
+                       const float* gscale, const float* lr_scale, bool fp8, double bytes,
+                       hipStream_t s) {
   if (set.nitems == 0) return SM_OK;
-  (void)stream;
+  const bool stream = bytes > kStreamBytes;
+  const auto kernel = fp8 ? (stream ? k_adamw<true, true> : k_adamw<true, false>)
+                          : (stream ? k_adamw<false, true> : k_adamw<false, false>);
   prof_begin(SM_K_ADAMW, bytes, s);
-  if (fp8)
-    hipLaunchKernelGGL((k_adamw<true>), dim3(set.nitems), dim3(kThreads), 0, s, set, a, device,
-                       gscale, lr_scale);
-  else
-    hipLaunchKernelGGL((k_adamw<false>), dim3(set.nitems), dim3(kThreads), 0, s, set, a, device,
-                       gscale, lr_scale);
+  hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(kThreads), 0, s, set, a, device, gscale,
+                     lr_scale);
   prof_end(s);
   return check_launch();
 }
 
 sm_status launch_grad_sumsq(const ParamSetDev& set, double* parts, double bytes, hipStream_t s) {
-  if (set.nitems == 0) return SM_OK;
+  if (set.norm_items == 0) return SM_OK;
   prof_begin(SM_K_GRAD_NORM, bytes, s);
-  hipLaunchKernelGGL(k_grad_sumsq, dim3(norm_set_parts(set.nitems)), dim3(kThreads), 0, s, set,
-                     parts);
+  hipLaunchKernelGGL(k_grad_sumsq, dim3(norm_set_parts(set.norm_items)), dim3(kThreads), 0, s,
+                     set, parts);
   prof_end(s);
   return check_launch();
 }
@@ -502,9 +780,11 @@ sm_status launch_norm_finalize(const double* parts, int n, float scale, float ma
 
 sm_status launch_state8_pack(const float* m, const float* v, int64_t count, uint8_t* m8,
                              uint8_t* v8, float* ms, float* vs, hipStream_t s) {
-  prof_begin(SM_K_STATE8, 10.03125 * (double)count, s);
-  hipLaunchKernelGGL(k_state8_pack, dim3(unit_blocks(count)), dim3(kThreads), 0, s, m, v, count,
-                     m8, v8, ms, vs, state8_vec(m, v, m8, v8));
+  const double bytes = 10.03125 * (double)count;
+  prof_begin(SM_K_STATE8, bytes, s);
+  const auto kernel = bytes > kStreamBytes ? k_state8_pack<true> : k_state8_pack<false>;
+  hipLaunchKernelGGL(kernel, dim3(unit_blocks(count)), dim3(kThreads), 0, s, m, v, count, m8, v8,
+                     ms, vs, state8_vec(m, v, m8, v8));
   prof_end(s);
   return check_launch();
 }
@@ -512,9 +792,11 @@ sm_status launch_state8_pack(const float* m, const float* v, int64_t count, uint
 sm_status launch_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* ms,
                                const float* vs, int64_t count, float* m, float* v,
                                hipStream_t s) {
-  prof_begin(SM_K_STATE8, 10.03125 * (double)count, s);
-  hipLaunchKernelGGL(k_state8_unpack, dim3(unit_blocks(count)), dim3(kThreads), 0, s, m8, v8, ms,
-                     vs, count, m, v, state8_vec(m, v, m8, v8));
+  const double bytes = 10.03125 * (double)count;
+  prof_begin(SM_K_STATE8, bytes, s);
+  const auto kernel = bytes > kStreamBytes ? k_state8_unpack<true> : k_state8_unpack<false>;
+  hipLaunchKernelGGL(kernel, dim3(unit_blocks(count)), dim3(kThreads), 0, s, m8, v8, ms, vs,
+                     count, m, v, state8_vec(m, v, m8, v8));
   prof_end(s);
   return check_launch();
 }

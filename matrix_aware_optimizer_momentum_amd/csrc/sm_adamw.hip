@@ -30,39 +30,31 @@ bool finite(float v) { return std::isfinite(v); }
 int64_t state_blocks(int64_t count) { return (count + kStateBlock - 1) / kStateBlock; }
 bool norm_only(const sm_param& p) { return !p.w && !p.m && !p.v; }
 
-// Units per work item: sets of many entries take 4, so that a workgroup's
-// table reads are spread over 8192 entries; small ones 1, so that more
-// workgroups share the work.
-int set_units(int64_t entries) { return entries >= (int64_t(1) << 24) ? 4 : 1; }
+int64_t step_items(int64_t count) { return (count + kStepSpan - 1) / kStepSpan; }
+int64_t norm_items(int64_t count) { return (count + kNormSpan - 1) / kNormSpan; }
 
-sm_status check_sizes(const sm_param* params, int n, int64_t* entries, int64_t* items) {
+// Where a set's tables lie in its workspace.
+struct SetWs {
+  size_t scalars, ents, items, norm_items, bytes;
+  int64_t nitems, nnorm;
+};
+sm_status set_ws(const sm_param* params, int n, SetWs* w) {
   if (!params || n < 1) return SM_ERR_ARG;
   if (n > kMaxParams) return SM_ERR_SHAPE;
-  int64_t total = 0;
+  w->nitems = w->nnorm = 0;
   for (int i = 0; i < n; ++i) {
     if (params[i].count < 0 || params[i].count > kMaxCount) return SM_ERR_SHAPE;
-    total += params[i].count;   // < 2^60
+    w->nitems += step_items(params[i].count);   // < 2^51
+    w->nnorm += norm_items(params[i].count);
   }
-  const int64_t span = (int64_t)set_units(total) * kUnit;
-  int64_t ni = 0;
-  for (int i = 0; i < n; ++i) ni += (params[i].count + span - 1) / span;
-  if (ni > kMaxItems) return SM_ERR_SHAPE;
-  *entries = total;
-  *items = ni;
-  return SM_OK;
-}
-
-struct SetWs {
-  size_t scalars, ents, items, bytes;
-};
-SetWs set_ws(int n, int64_t items) {
-  SetWs w;
+  if (w->nitems > kMaxItems) return SM_ERR_SHAPE;
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
-  w.scalars = 0;
-  w.ents = up(sizeof(AdamwScalars));
-  w.items = w.ents + up((size_t)n * sizeof(ParamEnt));
-  w.bytes = w.items + up((size_t)items * sizeof(WorkItem));
-  return w;
+  w->scalars = 0;
+  w->ents = up(sizeof(AdamwScalars));
+  w->items = w->ents + up((size_t)n * sizeof(ParamEnt));
+  w->norm_items = w->items + up((size_t)w->nitems * sizeof(WorkItem));
+  w->bytes = w->norm_items + up((size_t)w->nnorm * sizeof(WorkItem));
+  return SM_OK;
 }
 
 // A range of addresses that a set reads or writes.
@@ -122,7 +114,7 @@ ParamEnt entry_of(const sm_param& p, int M) {
   e.gstride = M > 1 ? p.grad_stride : 0;
   e.lr_mult = 1.0f;
   if (p.gdt == SM_BF16) e.flags |= kPF_G16;
-  bool vec = multiple_of(p.grad, 16) && (size_t)e.gstride * gs % 16 == 0;
+  bool vec = multiple_of(p.grad, 4 * gs) && e.gstride % 4 == 0;
   if (!norm_only(p)) {
     e.w = p.w;
     e.master = p.master;
@@ -134,9 +126,9 @@ ParamEnt entry_of(const sm_param& p, int M) {
     e.lr_mult = p.lr_mult;
     if (p.wdt == SM_BF16) e.flags |= kPF_W16;
     if (p.state == SM_STATE_FP8) e.flags |= kPF_FP8;
-    const size_t sa = p.state == SM_STATE_FP8 ? 8 : 16;
-    vec = vec && multiple_of(p.w, 16) && multiple_of(p.master, 16) && multiple_of(p.m, sa) &&
-          multiple_of(p.v, sa);
+    const size_t sa = p.state == SM_STATE_FP8 ? 4 : 16;
+    vec = vec && multiple_of(p.w, 4 * dt_size(p.wdt)) && multiple_of(p.master, 16) &&
+          multiple_of(p.m, sa) && multiple_of(p.v, sa);
   }
   if (vec) e.flags |= kPF_VEC;
   return e;
@@ -151,9 +143,9 @@ extern "C" {
 
 sm_status sm_param_set_ws(const sm_param* params, int n, size_t* ws_bytes) {
   if (!ws_bytes) return SM_ERR_ARG;
-  int64_t entries, items;
-  SM_TRY(check_sizes(params, n, &entries, &items));
-  *ws_bytes = set_ws(n, items).bytes;
+  SetWs lay;
+  SM_TRY(set_ws(params, n, &lay));
+  *ws_bytes = lay.bytes;
   return SM_OK;
 }
 
@@ -161,11 +153,10 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
                               hipStream_t s, sm_param_set* out) {
   if (!out) return SM_ERR_ARG;
   *out = nullptr;
-  int64_t entries, items;
-  SM_TRY(check_sizes(params, n, &entries, &items));
+  SetWs lay;
+  SM_TRY(set_ws(params, n, &lay));
   if (M < 1 || M > 64) return SM_ERR_UNSUPPORTED;
   if (!ws || !multiple_of(ws, 256)) return SM_ERR_ARG;
-  const SetWs lay = set_ws(n, items);
   if (ws_bytes < lay.bytes) return SM_ERR_WORKSPACE;
   for (int i = 0; i < n; ++i) SM_TRY(check_param(params[i], M));
 
@@ -206,17 +197,19 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
   WorkItem* wi = reinterpret_cast<WorkItem*>(base + lay.items);
   h->dev.ents = ents;
   h->dev.items = wi;
+  WorkItem* ni = reinterpret_cast<WorkItem*>(base + lay.norm_items);
+  h->dev.norm_at = ni;
   h->dev.scalars = reinterpret_cast<AdamwScalars*>(base + lay.scalars);
-  h->dev.nitems = (int)items;
-  h->dev.units = set_units(entries);
+  h->dev.nitems = (int)lay.nitems;
+  h->dev.norm_items = (int)lay.nnorm;
   h->dev.M = M;
+  h->dev.inv_M = 1.0f / (float)M;
   h->nparam = n;
   h->update = true;
   h->fp8 = false;
   h->step_bytes = h->grad_bytes = 0.0;
 
-  const int64_t span = (int64_t)h->dev.units * kUnit;
-  int64_t first = 0;
+  int64_t first = 0, norm_first = 0;
   sm_status st = SM_OK;
   for (int i0 = 0; i0 < n && st == SM_OK; i0 += kFillMax) {
     const int k = std::min(kFillMax, n - i0);
@@ -226,7 +219,9 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
       const sm_param& p = params[i0 + q];
       t.e[q] = entry_of(p, M);
       t.first[q] = first;
-      first += (p.count + span - 1) / span;
+      t.norm_first[q] = norm_first;
+      first += step_items(p.count);
+      norm_first += norm_items(p.count);
       const double c = (double)p.count;
       h->grad_bytes += c * M * dt_size(p.gdt);
       if (norm_only(p)) {
@@ -237,7 +232,7 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
       h->step_bytes += c * (p.master ? 8.0 + dt_size(p.wdt) : 2.0 * dt_size(p.wdt)) +
                        (p.state == SM_STATE_FP8 ? 4.0 * c + 16.0 * state_blocks(p.count) : 16.0 * c);
     }
-    st = launch_set_fill(t, k, i0, ents, wi, h->dev.units, s);
+    st = launch_set_fill(t, k, i0, ents, wi, ni, s);
   }
   h->step_bytes += h->grad_bytes;
   if (st == SM_OK) {
@@ -274,7 +269,7 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
   } else {
     a = adamw_scalars(*c, t);
   }
-  return launch_adamw(set->dev, a, step != nullptr, gscale, lr_scale, set->fp8, false,
+  return launch_adamw(set->dev, a, step != nullptr, gscale, lr_scale, set->fp8,
                       set->step_bytes, s);
 }
 
@@ -300,7 +295,7 @@ sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float m
   int n = 0;
   for (int i = 0; i < nsets; ++i) {
     SM_TRY(launch_grad_sumsq(sets[i]->dev, parts + n, sets[i]->grad_bytes, s));
-    n += norm_set_parts(sets[i]->dev.nitems);
+    n += norm_set_parts(sets[i]->dev.norm_items);
   }
   return launch_norm_finalize(parts, n, scale, max_norm, out, s);
 }
