@@ -397,7 +397,7 @@ sm_status sm_graph_destroy(sm_graph g);
  *   unexpected scales or master, bad weight_decay or lr_mult, grad_stride <
  *   count with M > 1, a buffer that is written overlapping any other of the
  *   list or ws), SM_ERR_SHAPE (count < 0 or > 2^40, grad_stride > 2^40, n >
- *   2^20, or more than 2^24 - 1 work items), SM_ERR_DTYPE, SM_ERR_WORKSPACE,
+ *   2^20, or more entries than a launch holds, about 2^34), SM_ERR_DTYPE, SM_ERR_WORKSPACE,
  *   SM_ERR_UNSUPPORTED (M outside 1..64; s in graph capture), SM_ERR_HIP.
  * ---------------------------------------------------------------------- */
 typedef enum { SM_STATE_F32 = 0, SM_STATE_FP8 = 1 } sm_state;
@@ -454,8 +454,8 @@ sm_status sm_param_set_destroy(sm_param_set set);
  *   out + 1).  lr_scale: optional device float >= 0, a factor on lr (a
  *   schedule's, for captured calls).  If one of them is not finite the whole
  *   step is skipped: nothing is written and *step stays.
- * Calls on one set must be ordered by the caller (they update the same
- * tensors, and share the set's scratch).
+ * Calls on one set (steps and norms) must be ordered by the caller: they
+ * share its tensors and its scratch.
  * Errors: SM_ERR_ARG (null config or set, a set with sm_grad_norm-only
  *   parameters, t < 1 without step, t != 0 with it, misaligned pointers, lr
  *   < 0 or not finite, betas outside [0, 1), eps < 1e-15 or not finite, bad
@@ -482,16 +482,14 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
  * infinity (no clipping).  Sums of 8 squares in float32, beyond that in
  * float64, in a fixed order; a square beyond float32's range (an entry above
  * 1.8e19) makes the norm infinite.
- * sets: 1..8 sets (of any M and types).  out: 2 floats.  ws: at least
- * sm_grad_norm_ws bytes, 256-byte aligned; calls that may overlap need
- * workspaces of their own.
- * Errors: SM_ERR_ARG (null or misaligned pointers, nsets < 1, scale not
- *   finite, max_norm not > 0, out inside ws), SM_ERR_UNSUPPORTED (nsets >
- *   8), SM_ERR_WORKSPACE, SM_ERR_HIP.
+ * sets: 1..8 different sets (of any M and types), whose scratch the call
+ * uses.  out: 2 floats, outside every set's buffers.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, nsets < 1, a set twice,
+ *   scale not finite, max_norm not > 0), SM_ERR_UNSUPPORTED (nsets > 8),
+ *   SM_ERR_HIP.
  * ---------------------------------------------------------------------- */
-sm_status sm_grad_norm_ws(int nsets, size_t* ws_bytes);
 sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float max_norm,
-                       float* out, void* ws, size_t ws_bytes, hipStream_t s);
+                       float* out, hipStream_t s);
 
 /* ------------------------------------------------------------------------
  * 8-bit AdamW states from float32 ones, and back (checkpoints, and a run

@@ -104,9 +104,7 @@ SIGNATURES = {
     "sm_param_set_destroy": (c_int, [c_void_p]),
     "sm_adamw": (c_int, [P(AdamWConfig), c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                          c_void_p]),
-    "sm_grad_norm_ws": (c_int, [c_int, P(c_size_t)]),
-    "sm_grad_norm": (c_int, [P(c_void_p), c_int, c_float, c_float, c_void_p, c_void_p, c_size_t,
-                             c_void_p]),
+    "sm_grad_norm": (c_int, [P(c_void_p), c_int, c_float, c_float, c_void_p, c_void_p]),
     "sm_state8_pack": (c_int, [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                c_void_p, c_void_p]),
     "sm_state8_unpack": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,

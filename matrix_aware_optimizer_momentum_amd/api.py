@@ -6,6 +6,7 @@ status codes raise SmError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 from typing import List, Optional, Sequence
@@ -450,9 +451,16 @@ def _state_blocks(count: int) -> int:
     return (count + B.STATE8_BLOCK - 1) // B.STATE8_BLOCK
 
 
-def _stream_of(t: torch.Tensor) -> int:
-    """The current stream of t's device, whichever device is current."""
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _stream_of(index: int) -> int:
+    """The current stream of device `index`, whichever device is current."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_device(index: int):
+    """Makes device `index` current for a call; free where it is already."""
+    if torch.cuda.current_device() == index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(index)
 
 
 def _dev_all(**tensors: torch.Tensor):
@@ -579,8 +587,8 @@ class ParamSet:
     on the GPU, made once.
 
     The buffers are bound at construction and must stay in place while the
-    set, or a graph captured from its calls, lives.  Calls on one set must be
-    ordered (they update the same tensors)."""
+    set, or a graph captured from its calls, lives.  Calls on one set (steps
+    and norms) must be ordered."""
 
     def __init__(self, params: Sequence[ParamBuffers], M: int = 1,
                  ws: Optional[torch.Tensor] = None):
@@ -602,21 +610,24 @@ class ParamSet:
         if ws is not None:
             _dev(ws, "ws")
         self.ws = _ws(need.value, self.device, ws)
+        self._index = self.device.index
+        self._stream = _stream_of(self._index)   # which the tables' memory belongs to
         h = ctypes.c_void_p()
-        with torch.cuda.device(self.device):
+        with _on_device(self._index):
             code = B.lib().sm_param_set_create(arr, len(self.params), M, self.ws.data_ptr(),
                                                self.ws.numel() * self.ws.element_size(),
-                                               _stream_of(self.ws), ctypes.byref(h))
+                                               self._stream, ctypes.byref(h))
         B.check(code, "sm_param_set_create")
         self._h = h
 
-    def _use(self):
-        """The handle, for work on the device's current stream, which the
-        tables then outlive."""
+    def _use(self) -> int:
+        """The device's current stream, which the tables outlive the work on."""
         if self._h is None:
             raise RuntimeError("ParamSet: use after close()")
-        self.ws.record_stream(torch.cuda.current_stream(self.device))
-        return self._h
+        s = _stream_of(self._index)
+        if s != self._stream:
+            self.ws.record_stream(torch.cuda.current_stream(self.device))
+        return s
 
     def close(self):
         if self._h is not None:
@@ -659,38 +670,36 @@ def adamw(cfg: AdamWConfig, pset: ParamSet, t: Optional[int] = None,
     sp = _scalar(step, "step", torch.int64, dev)
     gp = _scalar(gscale, "gscale", torch.float32, dev)
     lp = _scalar(lr_scale, "lr_scale", torch.float32, dev)
-    h = pset._use()
-    with torch.cuda.device(dev):
-        code = B.lib().sm_adamw(ctypes.byref(c), h, t or 0, sp, gp, lp, _stream_of(pset.ws))
-    B.check(code, "sm_adamw")
+    s = pset._use()
+    with _on_device(pset._index):
+        code = B.lib().sm_adamw(ctypes.byref(c), pset._h, t or 0, sp, gp, lp, s)
+    if code:
+        B.check(code, "sm_adamw")
 
 
 def grad_norm(psets: Sequence[ParamSet], max_norm: float, scale: float = 1.0,
-              out: Optional[torch.Tensor] = None,
-              ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """float32 [2]: the global norm of the sets' (mean) gradients times |scale|,
     and the factor scale * min(1, max_norm / (norm + 1e-6)) for adamw's gscale
     (out[1:2]), NaN where the norm is not finite."""
     if len(psets) == 0:
         raise ValueError("grad_norm needs at least one set")
-    dev = psets[0].device
-    if any(p.device != dev for p in psets):
+    first = psets[0]
+    if any(p.device != first.device for p in psets):
         raise ValueError("all sets must be on one device")
-    need = ctypes.c_size_t(0)
-    B.check(B.lib().sm_grad_norm_ws(len(psets), ctypes.byref(need)), "sm_grad_norm_ws")
-    out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
-    _expect(out, "out", (2,), torch.float32)
-    if ws is not None:
-        _dev(ws, "ws")
-    ws = _ws(need.value, dev, ws)
-    if out.device != dev or ws.device != dev:
-        raise ValueError("out and ws must be on the sets' device")
-    arr = (ctypes.c_void_p * len(psets))(*[p._use() for p in psets])
-    with torch.cuda.device(dev):
-        code = B.lib().sm_grad_norm(arr, len(psets), scale, max_norm, out.data_ptr(),
-                                    ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    _stream_of(ws))
-    B.check(code, "sm_grad_norm")
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=first.device)
+    else:
+        _expect(out, "out", (2,), torch.float32)
+        if out.device != first.device:
+            raise ValueError("out must be on the sets' device")
+    for p in psets:
+        s = p._use()
+    arr = (ctypes.c_void_p * len(psets))(*[p._h for p in psets])
+    with _on_device(first._index):
+        code = B.lib().sm_grad_norm(arr, len(psets), scale, max_norm, out.data_ptr(), s)
+    if code:
+        B.check(code, "sm_grad_norm")
     return out
 
 
@@ -703,9 +712,10 @@ def state8_pack(m: torch.Tensor, v: torch.Tensor):
     _dev_all(m=m, v=v)
     m8, v8 = (torch.empty(m.shape, dtype=d, device=m.device) for d in STATE8_DTYPES)
     ms, vs = (torch.empty(_state_blocks(m.numel()), device=m.device) for _ in range(2))
-    with torch.cuda.device(m.device):
+    with _on_device(m.device.index):
         code = B.lib().sm_state8_pack(m.data_ptr(), v.data_ptr(), m.numel(), m8.data_ptr(),
-                                      v8.data_ptr(), ms.data_ptr(), vs.data_ptr(), _stream_of(m))
+                                      v8.data_ptr(), ms.data_ptr(), vs.data_ptr(),
+                                      _stream_of(m.device.index))
     B.check(code, "sm_state8_pack")
     return m8, v8, ms, vs
 
@@ -720,10 +730,10 @@ def state8_unpack(m8: torch.Tensor, v8: torch.Tensor, m_scale: torch.Tensor,
     _expect(v_scale, "v_scale", blocks, torch.float32, dev=False)
     _dev_all(m8=m8, v8=v8, m_scale=m_scale, v_scale=v_scale)
     m, v = (torch.empty(m8.shape, dtype=torch.float32, device=m8.device) for _ in range(2))
-    with torch.cuda.device(m8.device):
+    with _on_device(m8.device.index):
         code = B.lib().sm_state8_unpack(m8.data_ptr(), v8.data_ptr(), m_scale.data_ptr(),
                                         v_scale.data_ptr(), m8.numel(), m.data_ptr(),
-                                        v.data_ptr(), _stream_of(m8))
+                                        v.data_ptr(), _stream_of(m8.device.index))
     B.check(code, "sm_state8_unpack")
     return m, v
 

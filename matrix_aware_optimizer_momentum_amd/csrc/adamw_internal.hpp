@@ -10,8 +10,13 @@ namespace sm {
 // lane.
 constexpr int kStateBlock = SM_STATE8_BLOCK;
 static_assert(kStateBlock == 64 * 4, "a wave holds one block");
-// Entries of a work item of the step (one workgroup) and of the norm.
-constexpr int kStepSpan = 2048;
+// Threads of a workgroup of the step, with and without 8-bit states in the
+// set, and the unit of entries that it takes at a time; a work item is one
+// unit, or kUnitsFp8 (entry_of in sm_adamw.hip).
+__host__ __device__ constexpr int step_threads(bool fp8) { return fp8 ? 256 : 128; }
+__host__ __device__ constexpr int step_unit(bool fp8) { return 4 * step_threads(fp8); }
+constexpr int kUnitsFp8 = 3;
+// Entries of a work item of the norm.
 constexpr int kNormSpan = 16384;
 
 // One parameter in a set's device table.
@@ -32,10 +37,18 @@ struct ParamEnt {
   int64_t count, gstride;
   float wd, lr_mult;
   uint32_t flags;
+  int32_t span;   // entries of a work item
 };
 
-// A share of a set: `span` entries (kStepSpan or kNormSpan) of parameter
-// `tensor` from entry chunk * span on.
+__host__ __device__ inline int64_t step_items(const ParamEnt& p) {
+  return (p.count + p.span - 1) / p.span;
+}
+__host__ __device__ inline int64_t norm_items(int64_t count) {
+  return (count + kNormSpan - 1) / kNormSpan;
+}
+
+// A share of a set: `span` entries (the parameter's, or kNormSpan) of
+// parameter `tensor` from entry chunk * span on.
 struct WorkItem {
   uint32_t tensor, chunk;
 };
@@ -91,6 +104,8 @@ struct ParamSetDev {
   const WorkItem* items;      // the step's
   const WorkItem* norm_at;  // the norm's
   AdamwScalars* scalars;      // of a step with a device-side index
+  uint32_t* counter;          // of a norm's workgroups, 0 between calls
+  double* parts;              // a norm's sums of squares, one per workgroup
   int nitems, norm_items, M;
   float inv_M;
 };
@@ -104,7 +119,7 @@ struct FillTbl {
 };
 static_assert(sizeof(FillTbl) <= 3584, "the table rides in the arguments");
 sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, WorkItem* items,
-                          WorkItem* norm_items, hipStream_t s);
+                          WorkItem* norm_items, uint32_t* counter, hipStream_t s);
 
 // The scalars of a step whose index *step holds, and *step + 1 written back
 // unless the step is skipped.
@@ -117,13 +132,27 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
                        const float* gscale, const float* lr_scale, bool fp8, double bytes,
                        hipStream_t s);
 
-// Sums of squares of a set's mean gradients: one double per workgroup,
-// norm_set_parts(norm_items) of them, already divided by M^2.
-constexpr int kNormSetParts = 2048;
-inline int norm_set_parts(int items) { return items < kNormSetParts ? items : kNormSetParts; }
-sm_status launch_grad_sumsq(const ParamSetDev& set, double* parts, double bytes, hipStream_t s);
-sm_status launch_norm_finalize(const double* parts, int n, float scale, float max_norm,
-                               float* out, hipStream_t s);
+// Workgroups of a set's gradient norm, one sum of squares (over M^2) each.
+// Few, since each adds to one counter: 495 M bf16 entries of one worker take
+// 143 us with 512 workgroups, 148 with 1024, 158 with 2048.
+// Several workers' rows are read with fewer bytes in flight per lane: 270 M
+// float32 entries of four take 350 us with 1024, 556 with 512, 361 with 2048.
+constexpr int kNormParts1 = 512, kNormPartsM = 1024;
+inline int norm_set_parts(int items, int M) {
+  const int most = M == 1 ? kNormParts1 : kNormPartsM;
+  return items < 1 ? 1 : items < most ? items : most;
+}
+// What a call's last launch needs to join the sums of all its sets.
+constexpr int kNormSets = 8;
+struct NormJoin {
+  double* parts[kNormSets];
+  int n[kNormSets];
+  int nsets;       // 0: not the last launch
+  float scale, max_norm;
+  float* out;      // {norm, factor}
+};
+sm_status launch_grad_norm(const ParamSetDev& set, const NormJoin& f, double bytes,
+                           hipStream_t s);
 
 sm_status launch_state8_pack(const float* m, const float* v, int64_t count, uint8_t* m8,
                              uint8_t* v8, float* ms, float* vs, hipStream_t s);

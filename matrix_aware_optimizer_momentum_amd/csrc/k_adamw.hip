@@ -16,9 +16,7 @@ namespace sm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = kThreads * 4;          // 4 entries per thread
-constexpr int kUnits = kStepSpan / kUnit;    // of a work item
-static_assert(kUnits * kUnit == kStepSpan, "whole units");
+constexpr int kUnit = kThreads * 4;   // 4 entries per thread
 // A step that moves more than the 256 MB Infinity Cache streams with
 // non-temporal accesses; a smaller one stays cacheable.
 constexpr double kStreamBytes = 256.0 * 1024 * 1024;
@@ -63,6 +61,8 @@ template <typename T>
 __device__ __forceinline__ const SM_GLOBAL T* at(const void* p, int64_t e) {
   return (const SM_GLOBAL T*)reinterpret_cast<uintptr_t>(p) + e;
 }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16_t v) { return bf2f(v); }
 __device__ __forceinline__ void from_f32(SM_GLOBAL float* p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(SM_GLOBAL bf16_t* p, float v) { *p = f2bf(v); }
 
@@ -93,6 +93,13 @@ __device__ __forceinline__ void expand4(u32x2 a, float* v) {
   v[1] = __uint_as_float(a.x & 0xFFFF0000u);
   v[2] = __uint_as_float(a.y << 16);
   v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+}
+
+// Sixteen bytes of gradients.
+__device__ __forceinline__ void expand_all(u32x4 a, float* v, float) { expand4(a, v); }
+__device__ __forceinline__ void expand_all(u32x4 a, float* v, bf16_t) {
+  expand4(u32x2{a.x, a.y}, v);
+  expand4(u32x2{a.z, a.w}, v + 4);
 }
 
 // Four entries from p + l on, of which `left` from p on exist.  full: all of
@@ -172,33 +179,34 @@ __device__ __forceinline__ void put4_bf16(SM_GLOBAL bf16_t* p, uint32_t l, uint3
 // and since that step undoes itself the second mixing's first step leaves
 // y ^ (C ^ (C >> 16)), C = 0x9E3779B1.
 
-// y of entries e0 .. e0 + 3, e0 a multiple of 4.  The first multiplication
-// is done once: (e0 + i) ^ key differs from e0 ^ key in its two low bits,
-// which the first shift does not reach, and flipping bit b of a factor adds
-// or subtracts 2^b times the other.
+__device__ __forceinline__ void opaque(uint32_t& x) { asm("" : "+v"(x)); }
+
+// y of entries e0 .. e0 + 3, e0 a multiple of 4: (e0 + i) ^ key is e0 ^ key
+// with i in its two low bits, which the first shift does not reach.
 __device__ __forceinline__ void random4(uint32_t e0, uint32_t key, uint32_t* y) {
-  constexpr uint32_t A = 0x9E3779B1u;
   uint32_t x = e0 ^ key;
   x ^= x >> 16;
-  const uint32_t s0 = (x & 1u) ? 0u - A : A, s1 = (x & 2u) ? 0u - 2u * A : 2u * A;
-  y[0] = x * A;
-  y[1] = y[0] + s0;
-  y[2] = y[0] + s1;
-  y[3] = y[2] + s0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = (y[e] ^ (y[e] >> 15)) * 0x85A308D3u;
+  for (uint32_t e = 0; e < 4; ++e) {
+    y[e] = (x ^ e) * 0x9E3779B1u;
+    y[e] = (y[e] ^ (y[e] >> 15)) * 0x85A308D3u;
+    opaque(y[e]);   // else shifts of y become multiplications of their own
+  }
 }
 // Seeds of the hardware's stochastic conversions, which add a seed's top
 // bits below the result's last one and truncate: 16 random bits and a half
 // below them for the codes (codes' own values stay), 16 for bf16.
-__device__ __forceinline__ uint32_t seed_v(uint32_t y) { return (y & 0xFFFF0000u) | 0x8000u; }
-__device__ __forceinline__ uint32_t seed_m(uint32_t y) { return seed_v(y) ^ (y << 16); }
+__device__ __forceinline__ uint32_t seed_v(uint32_t y) {
+  uint32_t x = (y & 0xFFFF0000u) | 0x8000u;
+  opaque(x);   // one instruction, used for m as well
+  return x;
+}
+__device__ __forceinline__ uint32_t seed_m(uint32_t y, uint32_t sv) { return sv ^ (y << 16); }
 __device__ __forceinline__ uint32_t seed_w(uint32_t y) {
   uint32_t x = (y ^ (0x9E3779B1u ^ (0x9E3779B1u >> 16))) * 0x9E3779B1u;
   x = (x ^ (x >> 15)) * 0x85A308D3u;
-  // the top half: the low one of x ^ (x >> 16); as a rotation, since a shift
-  // would be drawn into one more multiplication
-  return x ^ __builtin_amdgcn_alignbit(x, x, 16);
+  opaque(x);
+  return x ^ (x << 16);   // its top half: the low one of x ^ (x >> 16)
 }
 __device__ __forceinline__ uint32_t bf16_pair_stochastic(float a, float b, uint32_t ya,
                                                          uint32_t yb) {
@@ -284,24 +292,31 @@ __device__ __forceinline__ float scale_for(uint32_t amax, int top) {
 // Four first / second moments (finite) as codes, rounded stochastically: up
 // with the probability that the dropped part is of a code's step, to 2^-17.
 // y: the entries' random bits.
-__device__ __forceinline__ uint32_t encode4_m(const float* m, float scale, const uint32_t* y) {
-  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(0u, m[0], seed_m(y[0]), scale, 0);
-  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[1], seed_m(y[1]), scale, 1);
-  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[2], seed_m(y[2]), scale, 2);
-  return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[3], seed_m(y[3]), scale, 3);
+__device__ __forceinline__ uint32_t encode4_m(const float* m, float scale, const uint32_t* y,
+                                              const uint32_t* sv) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(0u, m[0], seed_m(y[0], sv[0]), scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[1], seed_m(y[1], sv[1]), scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[2], seed_m(y[2], sv[2]), scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(c, m[3], seed_m(y[3], sv[3]), scale, 3);
 }
-// A positive v takes at least the smallest code, 2^-16 of the scale: the
-// median of v, that floor and v * 2^300 (infinite, or 0 for v = 0).
-__device__ __forceinline__ float floor_v(float v, float least) {
-  return __builtin_amdgcn_fmed3f(v, least, __builtin_amdgcn_ldexpf(v, 300));
+// A positive v takes at least the smallest code, 1: only its own code may be
+// 0 (codes are below 0x7F, so that adding 0x7F sets a byte's top bit iff it
+// is not 0).
+__device__ __forceinline__ uint32_t floor_codes(const float* v, uint32_t c) {
+  const uint32_t zeros = ~(c + 0x7F7F7F7Fu) & 0x80808080u;
+  if (__builtin_expect(__any(zeros != 0u), 0)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v[e] > 0.f) c |= (zeros >> 7) & (1u << (8 * e));
+  }
+  return c;
 }
-__device__ __forceinline__ uint32_t encode4_v(const float* v, float scale, const uint32_t* y) {
-  const float least = scale * 0x1p-16f;
-  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(0u, floor_v(v[0], least), seed_v(y[0]),
-                                                        scale, 0);
-  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[1], least), seed_v(y[1]), scale, 1);
-  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[2], least), seed_v(y[2]), scale, 2);
-  return __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, floor_v(v[3], least), seed_v(y[3]), scale, 3);
+__device__ __forceinline__ uint32_t encode4_v(const float* v, float scale, const uint32_t* sv) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(0u, v[0], sv[0], scale, 0);
+  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, v[1], sv[1], scale, 1);
+  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, v[2], sv[2], scale, 2);
+  c = __builtin_amdgcn_cvt_scalef32_sr_bf8_f32(c, v[3], sv[3], scale, 3);
+  return floor_codes(v, c);
 }
 __device__ __forceinline__ float reciprocal(float scale) {   // of 2^e, e >= -126: exact
   return __uint_as_float(0x7F000000u - __float_as_uint(scale));
@@ -313,11 +328,10 @@ __device__ __forceinline__ uint32_t encode4_m_nearest(const float* m, float scal
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2] * q, m[3] * q, c, true);
 }
 __device__ __forceinline__ uint32_t encode4_v_nearest(const float* v, float scale) {
-  const float q = reciprocal(scale), least = scale * 0x1p-16f;
-  int c = __builtin_amdgcn_cvt_pk_bf8_f32(floor_v(v[0], least) * q, floor_v(v[1], least) * q, 0,
-                                          false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(floor_v(v[2], least) * q,
-                                                   floor_v(v[3], least) * q, c, true);
+  const float q = reciprocal(scale);
+  int c = __builtin_amdgcn_cvt_pk_bf8_f32(v[0] * q, v[1] * q, 0, false);
+  c = __builtin_amdgcn_cvt_pk_bf8_f32(v[2] * q, v[3] * q, c, true);
+  return floor_codes(v, (uint32_t)c);
 }
 
 // A block with values that are not finite: those (and negative second
@@ -357,8 +371,11 @@ __device__ __forceinline__ void encode_finite(const float* m, const float* v, ui
   c.ms = scale_for(am, 8);
   c.vs = scale_for(av, 15);
   if constexpr (STOCHASTIC) {
-    c.m = encode4_m(m, c.ms, y);
-    c.v = encode4_v(v, c.vs, y);
+    uint32_t sv[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sv[e] = seed_v(y[e]);
+    c.m = encode4_m(m, c.ms, y, sv);
+    c.v = encode4_v(v, c.vs, sv);
   } else {
     c.m = encode4_m_nearest(m, c.ms);
     c.v = encode4_v_nearest(v, c.vs);
@@ -386,19 +403,22 @@ __device__ __forceinline__ Codes encode_block(float* m, float* v, const uint32_t
 // ------------------------------------------------------------------ set tables
 
 __global__ __launch_bounds__(kThreads) void k_set_fill(FillTbl t, int index0, ParamEnt* ents,
-                                                       WorkItem* items, WorkItem* norm_items) {
+                                                       WorkItem* items, WorkItem* norm_out,
+                                                       uint32_t* counter) {
   const int q = blockIdx.y;
-  const int64_t count = t.e[q].count;
-  if (blockIdx.x == 0 && threadIdx.x == 0) ents[index0 + q] = t.e[q];
-  const int64_t n = (count + kStepSpan - 1) / kStepSpan;
-  const int64_t nn = (count + kNormSpan - 1) / kNormSpan;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    ents[index0 + q] = t.e[q];
+    *counter = 0;
+  }
+  const int64_t n = step_items(t.e[q]);
+  const int64_t nn = norm_items(t.e[q].count);
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
        i += (int64_t)gridDim.x * kThreads) {
     WorkItem it;
     it.tensor = (uint32_t)(index0 + q);
     it.chunk = (uint32_t)i;
     items[t.first[q] + i] = it;
-    if (i < nn) norm_items[t.norm_first[q] + i] = it;
+    if (i < nn) norm_out[t.norm_first[q] + i] = it;   // n >= nn
   }
 }
 
@@ -452,8 +472,8 @@ __device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float 
   }
 }
 
-// What a thread holds of one unit (1024 entries of the workgroup, 256 of the
-// wave: an 8-bit state's block), as loaded: nothing waits for these loads
+// What a thread holds of one unit (4 entries, the wave's 256 one block of an 8-bit
+// state), as loaded: nothing waits for these loads
 // until finish_unit.  TS: the weights that are read; TG: the gradients, or
 // float for the sum of several workers'.
 template <typename TS, typename TG, bool FP8>
@@ -466,9 +486,10 @@ struct Held {
 };
 
 // Entries of a unit from u0 on, at most a unit.
+template <int UNIT>
 __device__ __forceinline__ uint32_t unit_left(int64_t count, int64_t u0) {
   const int64_t n = count - u0;
-  return (uint32_t)(n < kUnit ? n : kUnit);
+  return (uint32_t)(n < UNIT ? n : UNIT);
 }
 
 // full: the thread has all four entries, at addresses that take one access.
@@ -498,7 +519,7 @@ __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, 
 // TW: the weights' type.  TS float32 with bf16 weights: they have a master.
 template <typename TW, typename TS, bool FP8, bool NT, typename H>
 __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalars& a, float f,
-                                            float keep, float step, uint32_t key, int64_t u0,
+                                            float keep, float step, uint32_t key0, int64_t u0,
                                             uint32_t left, bool full, const H& h) {
   const uint32_t l = threadIdx.x * 4;
   float g[4], w[4], m[4], v[4];
@@ -516,7 +537,8 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   adamw4(a, keep, step, g, m, v, w);
   constexpr bool SR_W = sizeof(TS) == 2, MASTER = sizeof(TW) == 2 && sizeof(TS) == 4;
   uint32_t y[4];
-  if (FP8 || (SR_W && a.stochastic)) random4((uint32_t)u0 + l, key, y);
+  if (FP8 || (SR_W && a.stochastic))
+    random4((uint32_t)u0 + l, mix_key(key0, (uint32_t)((uint64_t)u0 >> 32)), y);
   SM_GLOBAL TW* wp = at<TW>(p.w, u0);
   if constexpr (SR_W) {
     if (a.stochastic)
@@ -544,9 +566,12 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   }
 }
 
+// One work item: one unit, or kUnitsFp8 of them.
 template <bool FP8, bool NT>
-__global__ __launch_bounds__(kThreads) void k_adamw(ParamSetDev set, AdamwScalars arg, bool device,
-                                                    const float* gscale, const float* lr_scale) {
+__global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
+                                                            bool device, const float* gscale,
+                                                            const float* lr_scale) {
+  constexpr int UNIT = step_unit(FP8);
   const WorkItem it = load_const(set.items + blockIdx.x);
   const ParamEnt p = load_const(set.ents + it.tensor);
   AdamwScalars a = arg;
@@ -559,38 +584,35 @@ __global__ __launch_bounds__(kThreads) void k_adamw(ParamSetDev set, AdamwScalar
   const float step = a.step * mult;
   const float f = gs * set.inv_M;
   const bool vec = p.flags & kPF_VEC;
-  const int64_t first = (int64_t)it.chunk * kStepSpan;
-  const uint32_t key = mix_key(mix_key(a.key, it.tensor), (uint32_t)((uint64_t)first >> 32));
+  const int64_t span = p.span, first = (int64_t)it.chunk * span;
+  const uint32_t key0 = mix_key(a.key, it.tensor);
   auto item = [&](auto tw, auto ts, auto tg, auto fp8) {
     typedef decltype(tw) TW;
     typedef decltype(ts) TS;
     typedef decltype(tg) TG;
     constexpr bool F8 = decltype(fp8)::value;
-    if (vec && first + kStepSpan <= p.count) {
-      if (set.M == 1) {
-        // every unit's loads are in flight before the first one is used
-        Held<TS, TG, F8> h[kUnits];
+    const bool whole = vec && first + span <= p.count;
+    if (whole && set.M == 1) {
+      constexpr int units = sizeof(TS) == 2 && F8 ? kUnitsFp8 : 1;
+      Held<TS, TG, F8> h[units];
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          load_unit<TS, TG, F8, true, NT>(p, 1, first + u * kUnit, kUnit, true, h[u]);
+      for (int u = 0; u < units; ++u)
+        load_unit<TS, TG, F8, true, NT>(p, 1, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key, first + u * kUnit, kUnit, true,
-                                      h[u]);
-      } else {
-        for (int u = 0; u < kUnits; ++u) {
-          Held<TS, float, F8> h;
-          load_unit<TS, TG, F8, false, NT>(p, set.M, first + u * kUnit, kUnit, true, h);
-          finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key, first + u * kUnit, kUnit, true, h);
-        }
-      }
+      for (int u = 0; u < units; ++u)
+        finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key0, first + u * UNIT, UNIT,
+                                    true, h[u]);
+    } else if (whole) {
+      Held<TS, float, F8> h;
+      load_unit<TS, TG, F8, false, NT>(p, set.M, first, UNIT, true, h);
+      finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key0, first, UNIT, true, h);
     } else {
-      for (int64_t u0 = first; u0 < first + kStepSpan && u0 < p.count; u0 += kUnit) {
-        const uint32_t left = unit_left(p.count, u0);
+      for (int64_t u0 = first; u0 < first + span && u0 < p.count; u0 += UNIT) {
+        const uint32_t left = unit_left<UNIT>(p.count, u0);
         const bool full = vec && threadIdx.x * 4 + 4 <= left;
         Held<TS, float, F8> h;
         load_unit<TS, TG, F8, false, false>(p, set.M, u0, left, full, h);
-        finish_unit<TW, TS, F8, false>(p, a, f, keep, step, key, u0, left, full, h);
+        finish_unit<TW, TS, F8, false>(p, a, f, keep, step, key0, u0, left, full, h);
       }
     }
   };
@@ -630,45 +652,128 @@ __device__ __forceinline__ float sumsq4(const ParamEnt& p, int M, int64_t u0, ui
   const uint32_t l = threadIdx.x * 4;
   const bool full = vec && l + 4 <= left;
   float g[4];
-  if (M == 1) expand4(get4<TG, false>(at<TG>(p.g, u0), l, left, full), g);
-  else expand4(sum_grad4<TG, false>(p, M, u0, l, left, full), g);
+  expand4(sum_grad4<TG, false>(p, M, u0, l, left, full), g);
   float s = 0.f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) s = __fmaf_rn(g[e], g[e], s);
   return s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_sumsq(ParamSetDev set, double* parts) {
+template <typename TG>
+__device__ __forceinline__ float sumsq16(u32x4 a) {
+  constexpr int E = 16 / sizeof(TG);
+  float x[E], s = 0.f;
+  expand_all(a, x, TG());
+#pragma unroll
+  for (int e = 0; e < E; ++e) s = __fmaf_rn(x[e], x[e], s);
+  return s;
+}
+
+// The thread's share of a work item (`left` entries) whose rows take 16-byte
+// loads.  One worker: kNormFlight of them in flight.
+constexpr int kNormFlight = 8;
+template <typename TG, bool NT>
+__device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, int64_t gstride,
+                                             uint32_t left) {
+  constexpr uint32_t E = 16 / sizeof(TG), STEP = kThreads * E;
+  static_assert(kNormSpan % (STEP * kNormFlight) == 0, "whole rounds");
+  const uint32_t l = threadIdx.x * E;
+  double acc = 0.0;
+  auto round = [&](uint32_t i, auto whole) {
+    u32x4 a[kNormFlight];
+#pragma unroll
+    for (uint32_t q = 0; q < kNormFlight; ++q) {
+      const bool in = decltype(whole)::value || i + q * STEP + E <= left;
+      a[q] = u32x4{0u, 0u, 0u, 0u};
+      if (in) a[q] = load_v<NT, u32x4>(g + (i + q * STEP));
+    }
+#pragma unroll
+    for (uint32_t q = 0; q < kNormFlight; ++q) acc += (double)sumsq16<TG>(a[q]);
+  };
+  if (M == 1 && left == kNormSpan) {
+    for (uint32_t i = 0; i < kNormSpan; i += STEP * kNormFlight) round(i + l, std::true_type());
+  } else if (M == 1) {
+    for (uint32_t i = l; i < left; i += STEP * kNormFlight) round(i, std::false_type());
+  } else {
+    for (uint32_t i = l; i + E <= left; i += STEP) {
+      double s[E] = {};
+#pragma unroll 8
+      for (int k = 0; k < M; ++k) {
+        float x[E];
+        expand_all(load_v<NT, u32x4>(g + k * gstride + i), x, TG());
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) s[e] += (double)x[e];
+      }
+      float q = 0.f;
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) q = __fmaf_rn((float)s[e], (float)s[e], q);
+      acc += (double)q;
+    }
+  }
+  // the last entries, fewer than a load
+  const uint32_t tail = left - left % E;
+  if (threadIdx.x < left - tail) {
+    double s = 0.0;
+    for (int k = 0; k < M; ++k) s += (double)to_f32(g[k * gstride + tail + threadIdx.x]);
+    acc += (double)((float)s * (float)s);
+  }
+  return acc;
+}
+
+// The sums of squares of a set, one per workgroup.  A call's last launch also
+// joins the sums of all its sets: its last workgroup to come adds them, in
+// their order.  The counter wraps to 0 with that one, ready for the next
+// call.  The sums are written and read by atomics at device scope, past the
+// XCDs' own L2s: a release fence in each workgroup, which writes back its
+// XCD's L2, took 90 us over 2048 workgroups.
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_grad_norm(ParamSetDev set, NormJoin f) {
   __shared__ double red[4];
+  __shared__ bool last;
   double acc = 0.0;
   for (int i = blockIdx.x; i < set.norm_items; i += gridDim.x) {
     const WorkItem it = load_const(set.norm_at + i);
     const ParamEnt p = load_const(set.ents + it.tensor);
-    const bool vec = p.flags & kPF_VEC;
+    const bool vec = p.flags & kPF_VEC, g16 = p.flags & kPF_G16;
     const int64_t first = (int64_t)it.chunk * kNormSpan;
-    for (int64_t u0 = first; u0 < first + kNormSpan && u0 < p.count; u0 += kUnit) {
-      const uint32_t left = unit_left(p.count, u0);
-      acc += (double)((p.flags & kPF_G16) ? sumsq4<bf16_t>(p, set.M, u0, left, vec)
-                                          : sumsq4<float>(p, set.M, u0, left, vec));
+    const uint32_t left = unit_left<kNormSpan>(p.count, first);
+    const uintptr_t row = (uintptr_t)p.gstride * (g16 ? 2 : 4);   // 0 for one worker
+    if (((reinterpret_cast<uintptr_t>(p.g) | row) & 15u) == 0) {
+      acc += g16 ? sumsq_item<bf16_t, NT>(at<bf16_t>(p.g, first), set.M, p.gstride, left)
+                 : sumsq_item<float, NT>(at<float>(p.g, first), set.M, p.gstride, left);
+    } else {
+      for (uint32_t u = 0; u < left; u += kUnit) {
+        const uint32_t n = left - u < kUnit ? left - u : kUnit;
+        acc += (double)(g16 ? sumsq4<bf16_t>(p, set.M, first + u, n, vec)
+                            : sumsq4<float>(p, set.M, first + u, n, vec));
+      }
     }
   }
-  const double s = block_sum64(acc, red);
-  if (threadIdx.x == 0) parts[blockIdx.x] = s / ((double)set.M * (double)set.M);
-}
-
-__global__ __launch_bounds__(kThreads) void k_norm_finalize(const double* parts, int n,
-                                                            float scale, float max_norm,
-                                                            float* out) {
-  __shared__ double red[4];
-  double acc = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) acc += parts[i];
-  const double s = block_sum64(acc, red);
+  const double s = block_sum64(acc, red) / ((double)set.M * (double)set.M);
   if (threadIdx.x == 0) {
-    const float norm = (float)(sqrt(s) * fabs((double)scale));
-    const double c = (double)max_norm / ((double)norm + 1e-6);
-    out[0] = norm;
-    out[1] = is_finite(norm) ? (float)((double)scale * (c < 1.0 ? c : 1.0))
-                             : __uint_as_float(0x7FC00000u);
+    // returns once the sum is where every XCD sees it
+    const unsigned long long was =
+        __hip_atomic_exchange(reinterpret_cast<unsigned long long*>(set.parts) + blockIdx.x,
+                              __builtin_bit_cast(unsigned long long, s), __ATOMIC_RELAXED,
+                              __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::"v"(was) : "memory");   // waits for it
+    last = f.nsets > 0 && atomicInc(set.counter, gridDim.x - 1) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  acc = 0.0;
+  for (int q = 0; q < f.nsets; ++q)
+    for (int i = threadIdx.x; i < f.n[q]; i += kThreads)
+      acc += __builtin_bit_cast(
+          double, __hip_atomic_load(reinterpret_cast<unsigned long long*>(f.parts[q]) + i,
+                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  const double total = block_sum64(acc, red);
+  if (threadIdx.x == 0) {
+    const float norm = (float)(sqrt(total) * fabs((double)f.scale));
+    const double c = (double)f.max_norm / ((double)norm + 1e-6);
+    f.out[0] = norm;
+    f.out[1] = is_finite(norm) ? (float)((double)f.scale * (c < 1.0 ? c : 1.0))
+                               : __uint_as_float(0x7FC00000u);
   }
 }
 
@@ -680,7 +785,7 @@ __global__ __launch_bounds__(kThreads) void k_state8_pack(const float* m, const 
                                                           float* ms, float* vs, bool vec) {
   const uint32_t l = threadIdx.x * 4;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnit; u0 < count; u0 += (int64_t)gridDim.x * kUnit) {
-    const uint32_t left = unit_left(count, u0);
+    const uint32_t left = unit_left<kUnit>(count, u0);
     const bool full = vec && l + 4 <= left;
     float x[4], y[4];
     expand4(get4<float, NT>(at<float>(m, u0), l, left, full), x);
@@ -702,7 +807,7 @@ __global__ __launch_bounds__(kThreads) void k_state8_unpack(const uint8_t* m8, c
                                                             bool vec) {
   const uint32_t l = threadIdx.x * 4;
   for (int64_t u0 = (int64_t)blockIdx.x * kUnit; u0 < count; u0 += (int64_t)gridDim.x * kUnit) {
-    const uint32_t left = unit_left(count, u0);
+    const uint32_t left = unit_left<kUnit>(count, u0);
     if (l >= left) continue;
     const bool full = vec && l + 4 <= left;
     const int64_t blk = u0 / kStateBlock + (threadIdx.x >> 6);
@@ -731,12 +836,13 @@ bool state8_vec(const void* m, const void* v, const void* m8, const void* v8) {
 // ------------------------------------------------------------------ launchers
 
 sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, WorkItem* items,
-                          WorkItem* norm_items, hipStream_t s) {
+                          WorkItem* norm_items, uint32_t* counter, hipStream_t s) {
   int64_t most = 1;
   for (int q = 0; q < n; ++q)
-    most = std::max<int64_t>(most, (t.e[q].count + kStepSpan - 1) / kStepSpan);
+    most = std::max<int64_t>(most, step_items(t.e[q]));
   const dim3 grid((unsigned)std::min<int64_t>((most + kThreads - 1) / kThreads, 1024), n);
-  hipLaunchKernelGGL(k_set_fill, grid, dim3(kThreads), 0, s, t, index0, ents, items, norm_items);
+  hipLaunchKernelGGL(k_set_fill, grid, dim3(kThreads), 0, s, t, index0, ents, items, norm_items,
+                     counter);
   return check_launch();
 }
 
@@ -754,26 +860,17 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
   const auto kernel = fp8 ? (stream ? k_adamw<true, true> : k_adamw<true, false>)
                           : (stream ? k_adamw<false, true> : k_adamw<false, false>);
   prof_begin(SM_K_ADAMW, bytes, s);
-  hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(kThreads), 0, s, set, a, device, gscale,
+  hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(step_threads(fp8)), 0, s, set, a, device, gscale,
                      lr_scale);
   prof_end(s);
   return check_launch();
 }
 
-sm_status launch_grad_sumsq(const ParamSetDev& set, double* parts, double bytes, hipStream_t s) {
-  if (set.norm_items == 0) return SM_OK;
+sm_status launch_grad_norm(const ParamSetDev& set, const NormJoin& f, double bytes,
+                           hipStream_t s) {
   prof_begin(SM_K_GRAD_NORM, bytes, s);
-  hipLaunchKernelGGL(k_grad_sumsq, dim3(norm_set_parts(set.norm_items)), dim3(kThreads), 0, s,
-                     set, parts);
-  prof_end(s);
-  return check_launch();
-}
-
-sm_status launch_norm_finalize(const double* parts, int n, float scale, float max_norm,
-                               float* out, hipStream_t s) {
-  prof_begin(SM_K_GRAD_NORM, 8.0 * n, s);
-  hipLaunchKernelGGL(k_norm_finalize, dim3(1), dim3(kThreads), 0, s, parts, n, scale, max_norm,
-                     out);
+  const auto kernel = bytes > kStreamBytes ? k_grad_norm<true> : k_grad_norm<false>;
+  hipLaunchKernelGGL(kernel, dim3(norm_set_parts(set.norm_items, set.M)), dim3(kThreads), 0, s, set, f);
   prof_end(s);
   return check_launch();
 }

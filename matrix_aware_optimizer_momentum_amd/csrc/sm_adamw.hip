@@ -21,8 +21,8 @@ namespace {
 
 constexpr int64_t kMaxCount = int64_t(1) << 40;
 constexpr int kMaxParams = 1 << 20;
-// a launch holds fewer than 2^32 threads
-constexpr int64_t kMaxItems = (int64_t(1) << 24) - 1;
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;
 
 bool multiple_of(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool valid_dt(int dt) { return dt == SM_F32 || dt == SM_BF16; }
@@ -30,30 +30,39 @@ bool finite(float v) { return std::isfinite(v); }
 int64_t state_blocks(int64_t count) { return (count + kStateBlock - 1) / kStateBlock; }
 bool norm_only(const sm_param& p) { return !p.w && !p.m && !p.v; }
 
-int64_t step_items(int64_t count) { return (count + kStepSpan - 1) / kStepSpan; }
-int64_t norm_items(int64_t count) { return (count + kNormSpan - 1) / kNormSpan; }
+// Some parameter of the set has 8-bit states.
+bool has_fp8(const sm_param* params, int n) {
+  for (int i = 0; i < n; ++i)
+    if (params[i].count > 0 && !norm_only(params[i]) && params[i].state == SM_STATE_FP8)
+      return true;
+  return false;
+}
 
-// Where a set's tables lie in its workspace.
+// Where a set's tables lie in its workspace, with room for work items of one
+// unit each (wider ones need less).
 struct SetWs {
-  size_t scalars, ents, items, norm_items, bytes;
-  int64_t nitems, nnorm;
+  size_t scalars, counter, parts, ents, items, norm_items, bytes;
 };
 sm_status set_ws(const sm_param* params, int n, SetWs* w) {
   if (!params || n < 1) return SM_ERR_ARG;
   if (n > kMaxParams) return SM_ERR_SHAPE;
-  w->nitems = w->nnorm = 0;
+  const bool fp8 = has_fp8(params, n);
+  const int64_t unit = step_unit(fp8);
+  int64_t nitems = 0, nnorm = 0;
   for (int i = 0; i < n; ++i) {
     if (params[i].count < 0 || params[i].count > kMaxCount) return SM_ERR_SHAPE;
-    w->nitems += step_items(params[i].count);   // < 2^51
-    w->nnorm += norm_items(params[i].count);
+    nitems += (params[i].count + unit - 1) / unit;   // < 2^52
+    nnorm += norm_items(params[i].count);
   }
-  if (w->nitems > kMaxItems) return SM_ERR_SHAPE;
+  if (nitems * step_threads(fp8) > kMaxThreads) return SM_ERR_SHAPE;
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   w->scalars = 0;
-  w->ents = up(sizeof(AdamwScalars));
+  w->counter = up(sizeof(AdamwScalars));
+  w->parts = w->counter + 256;
+  w->ents = w->parts + up(kNormPartsM * sizeof(double));
   w->items = w->ents + up((size_t)n * sizeof(ParamEnt));
-  w->norm_items = w->items + up((size_t)w->nitems * sizeof(WorkItem));
-  w->bytes = w->norm_items + up((size_t)w->nnorm * sizeof(WorkItem));
+  w->norm_items = w->items + up((size_t)nitems * sizeof(WorkItem));
+  w->bytes = w->norm_items + up((size_t)nnorm * sizeof(WorkItem));
   return SM_OK;
 }
 
@@ -105,7 +114,7 @@ sm_status check_param(const sm_param& p, int M) {
   return SM_OK;
 }
 
-ParamEnt entry_of(const sm_param& p, int M) {
+ParamEnt entry_of(const sm_param& p, int M, bool fp8) {
   ParamEnt e;
   std::memset(&e, 0, sizeof(e));
   const size_t gs = dt_size(p.gdt);
@@ -113,6 +122,7 @@ ParamEnt entry_of(const sm_param& p, int M) {
   e.count = p.count;
   e.gstride = M > 1 ? p.grad_stride : 0;
   e.lr_mult = 1.0f;
+  e.span = step_unit(fp8);
   if (p.gdt == SM_BF16) e.flags |= kPF_G16;
   bool vec = multiple_of(p.grad, 4 * gs) && e.gstride % 4 == 0;
   if (!norm_only(p)) {
@@ -125,6 +135,13 @@ ParamEnt entry_of(const sm_param& p, int M) {
     e.wd = p.weight_decay;
     e.lr_mult = p.lr_mult;
     if (p.wdt == SM_BF16) e.flags |= kPF_W16;
+    // bf16 weights alone with 8-bit states, of one worker, move the fewest
+    // bytes per entry (10): their items hold several units, whose loads are
+    // all in flight before the first one is used.  495 M entries: 0.91 ms
+    // with one unit, 0.87 with two, 0.81 with three, 0.85 with four; float32
+    // states lose by it (1.82 ms with one, 1.88 with two).
+    if (p.wdt == SM_BF16 && !p.master && M == 1 && p.state == SM_STATE_FP8)
+      e.span *= kUnitsFp8;
     if (p.state == SM_STATE_FP8) e.flags |= kPF_FP8;
     const size_t sa = p.state == SM_STATE_FP8 ? 4 : 16;
     vec = vec && multiple_of(p.w, 4 * dt_size(p.wdt)) && multiple_of(p.master, 16) &&
@@ -200,13 +217,13 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
   WorkItem* ni = reinterpret_cast<WorkItem*>(base + lay.norm_items);
   h->dev.norm_at = ni;
   h->dev.scalars = reinterpret_cast<AdamwScalars*>(base + lay.scalars);
-  h->dev.nitems = (int)lay.nitems;
-  h->dev.norm_items = (int)lay.nnorm;
+  h->dev.counter = reinterpret_cast<uint32_t*>(base + lay.counter);
+  h->dev.parts = reinterpret_cast<double*>(base + lay.parts);
   h->dev.M = M;
   h->dev.inv_M = 1.0f / (float)M;
   h->nparam = n;
   h->update = true;
-  h->fp8 = false;
+  h->fp8 = has_fp8(params, n);
   h->step_bytes = h->grad_bytes = 0.0;
 
   int64_t first = 0, norm_first = 0;
@@ -217,10 +234,10 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
     std::memset(&t, 0, sizeof(t));
     for (int q = 0; q < k; ++q) {
       const sm_param& p = params[i0 + q];
-      t.e[q] = entry_of(p, M);
+      t.e[q] = entry_of(p, M, h->fp8);
       t.first[q] = first;
       t.norm_first[q] = norm_first;
-      first += step_items(p.count);
+      first += step_items(t.e[q]);
       norm_first += norm_items(p.count);
       const double c = (double)p.count;
       h->grad_bytes += c * M * dt_size(p.gdt);
@@ -228,12 +245,13 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
         if (p.count > 0) h->update = false;
         continue;
       }
-      if (p.state == SM_STATE_FP8) h->fp8 = true;
       h->step_bytes += c * (p.master ? 8.0 + dt_size(p.wdt) : 2.0 * dt_size(p.wdt)) +
                        (p.state == SM_STATE_FP8 ? 4.0 * c + 16.0 * state_blocks(p.count) : 16.0 * c);
     }
-    st = launch_set_fill(t, k, i0, ents, wi, ni, s);
+    st = launch_set_fill(t, k, i0, ents, wi, ni, h->dev.counter, s);
   }
+  h->dev.nitems = (int)first;
+  h->dev.norm_items = (int)norm_first;
   h->step_bytes += h->grad_bytes;
   if (st == SM_OK) {
     e = hipStreamSynchronize(s);
@@ -273,31 +291,28 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
                       set->step_bytes, s);
 }
 
-sm_status sm_grad_norm_ws(int nsets, size_t* ws_bytes) {
-  if (!ws_bytes || nsets < 1) return SM_ERR_ARG;
-  if (nsets > 8) return SM_ERR_UNSUPPORTED;
-  *ws_bytes = (size_t)nsets * kNormSetParts * sizeof(double);
-  return SM_OK;
-}
-
 sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float max_norm,
-                       float* out, void* ws, size_t ws_bytes, hipStream_t s) {
-  size_t need;
-  SM_TRY(sm_grad_norm_ws(nsets, &need));
-  if (!sets || !out || !ws || !multiple_of(out, 4) || !multiple_of(ws, 256)) return SM_ERR_ARG;
-  for (int i = 0; i < nsets; ++i)
-    if (!sets[i]) return SM_ERR_ARG;
-  if (!finite(scale) || !(max_norm > 0.f)) return SM_ERR_ARG;
-  if (ws_bytes < need) return SM_ERR_WORKSPACE;
-  const uintptr_t o = reinterpret_cast<uintptr_t>(out), w = reinterpret_cast<uintptr_t>(ws);
-  if (o < w + need && w < o + 8) return SM_ERR_ARG;
-  double* parts = static_cast<double*>(ws);
-  int n = 0;
+                       float* out, hipStream_t s) {
+  if (!sets || nsets < 1 || !out || !multiple_of(out, 4)) return SM_ERR_ARG;
+  if (nsets > kNormSets) return SM_ERR_UNSUPPORTED;
   for (int i = 0; i < nsets; ++i) {
-    SM_TRY(launch_grad_sumsq(sets[i]->dev, parts + n, sets[i]->grad_bytes, s));
-    n += norm_set_parts(sets[i]->dev.norm_items);
+    if (!sets[i]) return SM_ERR_ARG;
+    for (int k = 0; k < i; ++k)
+      if (sets[k] == sets[i]) return SM_ERR_ARG;   // its scratch holds one set's sums
   }
-  return launch_norm_finalize(parts, n, scale, max_norm, out, s);
+  if (!finite(scale) || !(max_norm > 0.f)) return SM_ERR_ARG;
+  NormJoin f;
+  std::memset(&f, 0, sizeof(f));
+  f.scale = scale;
+  f.max_norm = max_norm;
+  f.out = out;
+  for (int i = 0; i < nsets; ++i) {
+    f.parts[i] = sets[i]->dev.parts;
+    f.n[i] = norm_set_parts(sets[i]->dev.norm_items, sets[i]->dev.M);
+    if (i == nsets - 1) f.nsets = nsets;
+    SM_TRY(launch_grad_norm(sets[i]->dev, f, sets[i]->grad_bytes, s));
+  }
+  return SM_OK;
 }
 
 static sm_status check_state8(const void* m, const void* v, int64_t count, const void* m8,

@@ -199,14 +199,14 @@ def test_step_and_norm_refusals_without_a_set():
     c = sm.AdamWConfig().c_struct()
     assert lib.sm_adamw(ctypes.byref(c), None, 1, None, None, None, None) == ARG
     assert lib.sm_adamw(None, None, 1, None, None, None, None) == ARG
-    need = ctypes.c_size_t(0)
-    assert lib.sm_grad_norm_ws(0, ctypes.byref(need)) == ARG
-    assert lib.sm_grad_norm_ws(9, ctypes.byref(need)) == UNSUPPORTED
-    assert lib.sm_grad_norm_ws(8, ctypes.byref(need)) == 0 and need.value > 0
-    sets = (ctypes.c_void_p * 1)(None)
+    sets = (ctypes.c_void_p * 9)()
     ok = ctypes.c_void_p(0x1000000)
-    assert lib.sm_grad_norm(sets, 1, 1.0, 1.0, ok, ok, 1 << 20, None) == ARG
-    assert lib.sm_grad_norm(None, 1, 1.0, 1.0, ok, ok, 1 << 20, None) == ARG
+    assert lib.sm_grad_norm(sets, 1, 1.0, 1.0, ok, None) == ARG
+    assert lib.sm_grad_norm(None, 1, 1.0, 1.0, ok, None) == ARG
+    assert lib.sm_grad_norm(sets, 0, 1.0, 1.0, ok, None) == ARG
+    assert lib.sm_grad_norm(sets, 1, 1.0, 1.0, None, None) == ARG
+    assert lib.sm_grad_norm(sets, 1, 1.0, 1.0, ctypes.c_void_p(0x1000002), None) == ARG
+    assert lib.sm_grad_norm(sets, 9, 1.0, 1.0, ok, None) == UNSUPPORTED
     assert lib.sm_last_hip_error() == 0
 
 

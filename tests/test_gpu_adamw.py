@@ -198,7 +198,8 @@ def run_and_check(cases, M=1, t=5, gscale=None, steps=1, rounding=sm.ROUND_NEARE
     return pset
 
 
-LENGTHS = [1, 2, 7, 8, 9, 63, 255, 256, 257, 2040, 2047, 2048, 2049, 4103, 20000, 0]
+# around the 8-bit states' blocks, a thread's, a wave's and a work item's share
+LENGTHS = [511, 512, 513, 1023, 1025, 6143, 6144, 6145, 1, 2, 7, 8, 9, 63, 255, 256, 257, 2040, 2047, 2048, 2049, 4103, 20000, 0]
 
 
 @pytest.mark.parametrize("w", ["f32", "bf16", "master"])
@@ -418,17 +419,16 @@ def test_captured_steps_replay_as_a_training_loop(gpu_lib, fp8):
     cfg = sm.AdamWConfig(lr=3e-3, rounding=sm.ROUND_STOCHASTIC, seed=17)
     se, sg = (torch.zeros(1, dtype=torch.int64, device="cuda") for _ in range(2))
     oe, og = (torch.zeros(2, device="cuda") for _ in range(2))
-    we, wg = (torch.empty(1 << 18, dtype=torch.uint8, device="cuda") for _ in range(2))
     ls = torch.ones(1, device="cuda")
 
-    def one(ps, out, ws, step):
-        sm.grad_norm([ps], 1.0, out=out, ws=ws)
+    def one(ps, out, step):
+        sm.grad_norm([ps], 1.0, out=out)
         sm.adamw(cfg, ps, step=step, gscale=out[1:], lr_scale=ls)
 
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
-        one(pg, og, wg, sg)
+        one(pg, og, sg)
     gen = torch.Generator(device="cuda")
     gen.manual_seed(4)
     side = torch.randn(256, 256, device="cuda")
@@ -441,7 +441,7 @@ def test_captured_steps_replay_as_a_training_loop(gpu_lib, fp8):
             b.grad.copy_(x)
         ls.fill_(1.0 / (k + 1))
         graph.replay()
-        one(pe, oe, we, se)
+        one(pe, oe, se)
         side = torch.tanh(side @ side.T * 1e-3)
         torch.cuda.synchronize()
         assert int(se) == int(sg) == (k + 1 if k < 3 else k)
@@ -514,10 +514,9 @@ def test_refusals_of_a_live_set(gpu_lib):
                dict(max_norm=1.0, scale=float("inf"))):
         assert code(lambda: sm.grad_norm([ps], **kw)) == 1, kw
     assert code(lambda: sm.grad_norm([ps] * 9, 1.0)) == 5
-    buf = torch.empty(1 << 18, dtype=torch.uint8, device="cuda")
-    assert code(lambda: sm.grad_norm([ps], 1.0, out=buf[:8].view(torch.float32), ws=buf)) == 1
-    with pytest.raises(ValueError, match="workspace too small"):
-        sm.grad_norm([ps], 1.0, ws=buf[:64])
+    assert code(lambda: sm.grad_norm([ps, only, ps], 1.0)) == 1
+    with pytest.raises(ValueError, match="out must have shape"):
+        sm.grad_norm([ps], 1.0, out=torch.zeros(3, device="cuda"))
     ps.close()
     with pytest.raises(RuntimeError):
         sm.adamw(ok, ps, 1)
@@ -568,10 +567,25 @@ def test_norm_that_is_not_finite_gives_no_factor(gpu_lib, bad):
 
 
 def test_norm_of_nothing(gpu_lib):
-    for n in (0, 5):
-        out = sm.grad_norm([sm.ParamSet([sm.ParamBuffers(grad=torch.zeros(n, device="cuda"))])],
-                           2.0, scale=0.5)
+    sets = [sm.ParamSet([sm.ParamBuffers(grad=torch.zeros(n, device="cuda"))]) for n in (0, 5, 0)]
+    for s in ([sets[0]], [sets[1]], sets):
+        out = sm.grad_norm(s, 2.0, scale=0.5)
         assert out.tolist() == [0.0, 0.5]
+    three = sm.ParamSet([sm.ParamBuffers(grad=torch.full((9,), 1.0, device="cuda"))])
+    assert sm.grad_norm([sets[0], three, sets[2]], float("inf")).tolist() == [3.0, 1.0]
+
+
+def test_norms_repeat_over_many_workgroups(gpu_lib):
+    """2048 workgroups and more items than that: every call gives the same
+    bits, whichever workgroup joins the sums, and leaves the counter ready."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    g = torch.randn(50_000_003, generator=gen, device="cuda")
+    ps = sm.ParamSet([sm.ParamBuffers(grad=g)])
+    outs = torch.stack([sm.grad_norm([ps], 1.0) for _ in range(50)])
+    want = float(g.double().square().sum().sqrt())
+    assert torch.equal(outs, outs[:1].expand(50, 2))
+    assert abs(float(outs[0, 0]) - want) <= 10 * 2.0 ** -24 * want
 
 
 # ---------------------------------------------------------------- 8-bit states
