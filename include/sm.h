@@ -379,7 +379,8 @@ sm_status sm_graph_destroy(sm_graph g);
  *   m, v   : [count], first and second moment, updated in place; zero them
  *            before the first step.  state SM_STATE_F32: float32.  state
  *            SM_STATE_FP8: one byte per entry (see sm_state8_pack), with
- *            m_scale, v_scale: float32 [ceil(count/256)].
+ *            m_scale, v_scale: float32 [ceil(count/256)], zero or powers of
+ *            two (as the library writes them).
  *   weight_decay >= 0, lr_mult >= 0 (a factor on the step's lr): finite.
  *   w, m and v NULL: a parameter that only sm_grad_norm takes (a Muon
  *   step's matrices enter the norm this way); wdt, state and master are
@@ -449,7 +450,7 @@ sm_status sm_param_set_destroy(sm_param_set set);
  * t: 1-based step index if step is NULL.  step: device int64, the number of
  *   steps done so far; then t must be 0, the step has index *step + 1, and
  *   *step is advanced on the device (so that a captured call replays as a
- *   training loop's next step).
+ *   training loop's next step).  A negative *step skips the step.
  * gscale: optional device float, a factor on the gradients (sm_grad_norm's
  *   out + 1).  lr_scale: optional device float >= 0, a factor on lr (a
  *   schedule's, for captured calls).  If one of them is not finite the whole

@@ -463,12 +463,19 @@ def _on_device(index: int):
     return torch.cuda.device(index)
 
 
-def _dev_all(**tensors: torch.Tensor):
-    """Contiguous GPU tensors, all on one device."""
-    for name, t in tensors.items():
+def _check_all(**wanted):
+    """Each name=(tensor, shape, dtype): a contiguous GPU tensor of that shape
+    and type, all on one device.  (The order of the checks is the messages'.)"""
+    for name, (t, shape, dtype) in wanted.items():
+        if t.dtype != dtype or t.shape != shape:
+            _expect(t, name, shape, dtype, dev=False)
+    device = None
+    for name, (t, _, _) in wanted.items():
         _dev(t, name)
-    if len({t.device for t in tensors.values()}) > 1:
-        raise ValueError(f"{', '.join(tensors)} must be on one device")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{', '.join(wanted)} must be on one device")
 
 
 @dataclass
@@ -707,34 +714,37 @@ def state8_pack(m: torch.Tensor, v: torch.Tensor):
     """(m8, v8, m_scale, v_scale): 8-bit AdamW states of float32 ones, rounded
     to nearest.  m8 is float8_e4m3fn and v8 float8_e5m2, in m's shape; the
     scales are float32, one per 256 entries."""
-    _expect(m, "m", dtype=torch.float32, dev=False)
-    _expect(v, "v", m.shape, torch.float32, dev=False)
-    _dev_all(m=m, v=v)
-    m8, v8 = (torch.empty(m.shape, dtype=d, device=m.device) for d in STATE8_DTYPES)
-    ms, vs = (torch.empty(_state_blocks(m.numel()), device=m.device) for _ in range(2))
-    with _on_device(m.device.index):
-        code = B.lib().sm_state8_pack(m.data_ptr(), v.data_ptr(), m.numel(), m8.data_ptr(),
-                                      v8.data_ptr(), ms.data_ptr(), vs.data_ptr(),
-                                      _stream_of(m.device.index))
-    B.check(code, "sm_state8_pack")
+    f32 = torch.float32
+    _check_all(m=(m, m.shape, f32), v=(v, m.shape, f32))
+    n, dev = m.numel(), m.device
+    m8 = torch.empty_like(m, dtype=STATE8_DTYPES[0])
+    v8 = torch.empty_like(m, dtype=STATE8_DTYPES[1])
+    ms = torch.empty(_state_blocks(n), dtype=f32, device=dev)
+    vs = torch.empty_like(ms)
+    with _on_device(dev.index):
+        code = B.lib().sm_state8_pack(m.data_ptr(), v.data_ptr(), n, m8.data_ptr(), v8.data_ptr(),
+                                      ms.data_ptr(), vs.data_ptr(), _stream_of(dev.index))
+    if code:
+        B.check(code, "sm_state8_pack")
     return m8, v8, ms, vs
 
 
 def state8_unpack(m8: torch.Tensor, v8: torch.Tensor, m_scale: torch.Tensor,
                   v_scale: torch.Tensor):
     """(m, v): the float32 values of 8-bit AdamW states, in m8's shape."""
-    blocks = (_state_blocks(m8.numel()),)
-    _expect(m8, "m8", dtype=STATE8_DTYPES[0], dev=False)
-    _expect(v8, "v8", m8.shape, STATE8_DTYPES[1], dev=False)
-    _expect(m_scale, "m_scale", blocks, torch.float32, dev=False)
-    _expect(v_scale, "v_scale", blocks, torch.float32, dev=False)
-    _dev_all(m8=m8, v8=v8, m_scale=m_scale, v_scale=v_scale)
-    m, v = (torch.empty(m8.shape, dtype=torch.float32, device=m8.device) for _ in range(2))
-    with _on_device(m8.device.index):
+    f32, n = torch.float32, m8.numel()
+    blocks = (_state_blocks(n),)
+    _check_all(m8=(m8, m8.shape, STATE8_DTYPES[0]), v8=(v8, m8.shape, STATE8_DTYPES[1]),
+               m_scale=(m_scale, blocks, f32), v_scale=(v_scale, blocks, f32))
+    m = torch.empty_like(m8, dtype=f32)
+    v = torch.empty_like(m)
+    index = m8.device.index
+    with _on_device(index):
         code = B.lib().sm_state8_unpack(m8.data_ptr(), v8.data_ptr(), m_scale.data_ptr(),
-                                        v_scale.data_ptr(), m8.numel(), m.data_ptr(),
-                                        v.data_ptr(), _stream_of(m8.device.index))
-    B.check(code, "sm_state8_unpack")
+                                        v_scale.data_ptr(), n, m.data_ptr(), v.data_ptr(),
+                                        _stream_of(index))
+    if code:
+        B.check(code, "sm_state8_unpack")
     return m, v
 
 

@@ -17,9 +17,17 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = kThreads * 4;   // 4 entries per thread
-// A step that moves more than the 256 MB Infinity Cache streams with
-// non-temporal accesses; a smaller one stays cacheable.
+// Where the data outgrow the 256 MB Infinity Cache, accesses are
+// non-temporal; below that they stay cacheable.  The step writes most of what
+// it reads, so that it moves twice what it holds.  Cacheable / non-temporal:
+//   step, float32 states, bf16 weights  256 MB 41 / 43 us, 512 MB 80 / 83,
+//                                       1 GB 192 / 164
+//   step, 8-bit states, masters         256 MB 41 / 45, 512 MB 88 / 87,
+//                                       1 GB 191 / 170
+//   norm    192 MB 34 / 36 us, 256 MB 43 / 45, 384 MB 70 / 64
+//   pack    192 MB 31 / 36 us, 256 MB 42 / 47, 384 MB 72 / 70
 constexpr double kStreamBytes = 256.0 * 1024 * 1024;
+constexpr double kStreamStepBytes = 512.0 * 1024 * 1024;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -431,9 +439,9 @@ __device__ __forceinline__ bool is_finite(float v) {
 __global__ void k_adamw_prep(sm_adamw_config c, int64_t* step, const float* gscale,
                              const float* lr_scale, AdamwScalars* out) {
   if (threadIdx.x != 0) return;
-  const int64_t t = *step + 1;
+  const int64_t done = *step, t = done < 0 ? 1 : done + 1;
   AdamwScalars a = adamw_scalars(c, t);
-  a.skip = (gscale && !is_finite(*gscale)) || (lr_scale && !is_finite(*lr_scale));
+  a.skip = done < 0 || (gscale && !is_finite(*gscale)) || (lr_scale && !is_finite(*lr_scale));
   *out = a;
   if (!a.skip) *step = t;
 }
@@ -566,13 +574,24 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   }
 }
 
+// The item of workgroup b: workgroups go to the 8 XCDs in turn, and of every
+// 8 * RUN items each XCD takes RUN that follow one another (the last ones,
+// fewer than that, stay in turn).  495 M entries with float32 states: 1.87
+// ms in turn, 1.84 in runs of 64, 1.81 of 256, 1.81 of 512; a 64 M-entry
+// embedding with 8-bit states and masters: 169, 164, 166 and 167 us.
+template <int RUN>
+__device__ __forceinline__ int xcd_run(int b, int items) {
+  const int in = b % (8 * RUN), first = b - in;
+  return first + 8 * RUN <= items ? first + (in % 8) * RUN + in / 8 : b;
+}
+
 // One work item: one unit, or kUnitsFp8 of them.
 template <bool FP8, bool NT>
 __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
                                                             bool device, const float* gscale,
                                                             const float* lr_scale) {
   constexpr int UNIT = step_unit(FP8);
-  const WorkItem it = load_const(set.items + blockIdx.x);
+  const WorkItem it = load_const(set.items + xcd_run<FP8 ? 64 : 256>(blockIdx.x, set.nitems));
   const ParamEnt p = load_const(set.ents + it.tensor);
   AdamwScalars a = arg;
   if (device) a = load_const(set.scalars);
@@ -856,7 +875,7 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
                        const float* gscale, const float* lr_scale, bool fp8, double bytes,
                        hipStream_t s) {
   if (set.nitems == 0) return SM_OK;
-  const bool stream = bytes > kStreamBytes;
+  const bool stream = bytes > kStreamStepBytes;
   const auto kernel = fp8 ? (stream ? k_adamw<true, true> : k_adamw<true, false>)
                           : (stream ? k_adamw<false, true> : k_adamw<false, false>);
   prof_begin(SM_K_ADAMW, bytes, s);

@@ -43,6 +43,7 @@ class Case:
     """One parameter: buffers inside larger ones (sentinels around them)."""
 
     PAD = 64
+    base = 0     # index of the first entry in its parameter
 
     def __init__(self, n, w="f32", g="f32", fp8=False, M=1, shift=0, wd=0.0, lr_mult=1.0,
                  gen=None, zero=False, gsize=1e-2, stride=None):
@@ -145,7 +146,7 @@ class Case:
             assert torch.equal(self.w, self.master.to(torch.bfloat16)), (what, "rounding")
         elif stochastic and self.w_kind == "bf16":
             # the float32 value's neighbour that the random bits choose
-            _, rw = A.random_bits(e["cfg"].seed, e["t"], e["index"], np.arange(n))
+            _, rw = A.random_bits(e["cfg"].seed, e["t"], e["index"], self.base + np.arange(n))
             ends = []
             for x in (e["w"] - e["w_off"], e["w"] + e["w_off"]):
                 # magnitudes round away by the random bits: on each end's own magnitude
@@ -159,7 +160,7 @@ class Case:
             assert np.all(np.abs(m - e["m"]) <= e["m_off"]), (what, "m")
             assert np.all(np.abs(v - e["v"]) <= e["v_off"]), (what, "v")
             return
-        r, _ = A.random_bits(e["cfg"].seed, e["t"], e["index"], np.arange(n))
+        r, _ = A.random_bits(e["cfg"].seed, e["t"], e["index"], self.base + np.arange(n))
         for kind, x, off, code, scale, bits in (
                 ("m", e["m"], e["m_off"], self.m, self.ms, r & np.uint64(0xFFFF)),
                 ("v", e["v"], e["v_off"], self.v, self.vs, r >> np.uint64(16))):
@@ -181,6 +182,24 @@ class Case:
             assert np.mean(ends[0] != ends[1]) < 1e-2 or n < 1000, (what, kind)
             big = np.abs(x) > off
             assert np.all((np.sign(got) == np.sign(x))[big & (a > 0)]), (what, kind, "sign")
+
+
+class Window(Case):
+    """A parameter's entries from a on: n of them and the rest of the last one's
+    block (the oracle takes a block's scale from all of its entries)."""
+
+    def __init__(self, p, M, a, n):
+        assert a % 256 == 0
+        n = min(-(-n // 256) * 256, p.w.numel() - a)
+        e, blocks = slice(a, a + n), slice(a // 256, -(-(a + n) // 256))
+        self.n, self.M, self.base, self.pads = n, M, a, []
+        self.wd, self.lr_mult, self.fp8 = p.weight_decay, p.lr_mult, p.m_scale is not None
+        self.w_kind = "f32" if p.w.dtype == torch.float32 else \
+            "bf16" if p.master is None else "master"
+        self.w, self.m, self.v = p.w[e], p.m[e], p.v[e]
+        self.grad = p.grad.view(M, -1)[:, e]
+        self.ms, self.vs = (None, None) if not self.fp8 else (p.m_scale[blocks], p.v_scale[blocks])
+        self.master = None if p.master is None else p.master[e]
 
 
 def run_and_check(cases, M=1, t=5, gscale=None, steps=1, rounding=sm.ROUND_NEAREST, **cfg):
@@ -310,6 +329,34 @@ def test_entries_far_beyond_32_bits(gpu_lib):
     del w, g, p
 
 
+@pytest.mark.parametrize("n,w,g,fp8,M", [
+    (30_000_001, "bf16", "bf16", False, 1), (20_000_003, "f32", "f32", False, 1),
+    (18_000_002, "f32", "f32", False, 2), (60_000_001, "bf16", "bf16", True, 1),
+    (36_000_513, "master", "f32", True, 1), (40_000_004, "master", "bf16", True, 3),
+])
+def test_sets_beyond_the_cache(gpu_lib, n, w, g, fp8, M):
+    """Steps that move more than 512 MB (non-temporal accesses, runs of items
+    per XCD), two of them; windows at both ends and in between."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n)
+    wt = (0.02 * torch.randn(n, generator=gen, device="cuda")).to(DT["f32" if w == "f32" else "bf16"])
+    grad = (1e-2 * torch.randn(M, n, generator=gen, device="cuda")).to(DT[g])
+    p = sm.ParamBuffers.with_state(wt, grad, fp8=fp8, master=w == "master", weight_decay=0.1)
+    small = Case(700, "f32", "f32", False, M=M)
+    cfg = sm.AdamWConfig(lr=1e-3, beta2=0.99, seed=n, rounding=sm.ROUND_STOCHASTIC)
+    pset = sm.ParamSet([small.buffers(), p], M=M)
+    ends = [(0, 5000), (n // 2 // 256 * 256, 7000), ((n - 4000) // 256 * 256, None)]
+    views = [Window(p, M, a, k or n - a) for a, k in ends]
+    for t in (1, 2):
+        e = [v.expect(cfg, t, 1) for v in views]
+        es = small.expect(cfg, t, 0)
+        sm.adamw(cfg, pset, t)
+        torch.cuda.synchronize()
+        for v, x in zip(views, e):
+            v.check(x, (t, v.base))
+        small.check(es, t)
+
+
 @pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
 def test_nan_and_infinite_gradients_stay_where_they_are(gpu_lib, fp8):
     """Without a clipping factor a NaN gradient spoils its own entry only, and
@@ -349,6 +396,23 @@ def test_extreme_magnitudes(gpu_lib):
         run_and_check(cs, t=1, steps=2, eps=1e-10)
 
 
+def test_small_second_moments_keep_the_smallest_code(gpu_lib):
+    """Gradients from 1 to 1e-9 in one block: second moments far below the
+    codes' range take the smallest code, zero ones stay zero, and the weights
+    move by at most a few lr (m / sqrt(v) would be huge with v lost)."""
+    c = Case(1024, "f32", "f32", True, zero=True)
+    c.grad[0] = torch.tensor([10.0 ** -(i % 10) for i in range(1024)]).cuda()
+    c.grad[0, 512:768:7] = 0.0
+    pset = run_and_check([c], t=1, steps=4)
+    code = c.v.view(torch.uint8).cpu().numpy()
+    g = c.grad[0].cpu().numpy()
+    assert np.all(code[g > 0] >= 1) and np.any(code[g > 0] == 1) and np.all(code[g == 0] == 0)
+    before = np64(c.w)
+    for t in range(5, 25):
+        sm.adamw(sm.AdamWConfig(lr=1e-3, beta2=0.99, seed=t), pset, t)
+    assert np.all(np.abs(np64(c.w) - before) <= 20 * 1e-3 * 4)
+
+
 # ---------------------------------------------------------------- skipping, device-side index
 
 def _snapshot(cases):
@@ -369,6 +433,13 @@ def test_a_factor_that_is_not_finite_skips_the_step(gpu_lib, which, value):
     assert int(step) == 41
     for x, y in zip(before, _snapshot(cases)):
         assert all(np.array_equal(p, q) for p, q in zip(x, y))
+    step.fill_(-7)                     # not a number of steps: skipped as well
+    sm.adamw(sm.AdamWConfig(), pset, step=step)
+    torch.cuda.synchronize()
+    assert int(step) == -7
+    for x, y in zip(before, _snapshot(cases)):
+        assert all(np.array_equal(p, q) for p, q in zip(x, y))
+    step.fill_(41)
     sm.adamw(sm.AdamWConfig(), pset, step=step)
     torch.cuda.synchronize()
     assert int(step) == 42
