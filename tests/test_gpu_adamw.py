@@ -119,8 +119,10 @@ class Case:
         grads = self.grads64()
         g, m1, v1 = A.moments(grads, m, v, c, gscale)
         b1, b2 = A.f32(cfg.beta1), A.f32(cfg.beta2)
-        m_off = 2.0 ** -21 * (np.abs(b1 * m) + np.abs((1 - b1) * g)) + 2.0 ** -149
-        v_off = 2.0 ** -20 * v1 + 2.0 ** -149
+        # ... and a denormal's step, but nothing where all terms are zero
+        terms = np.abs(b1 * m) + np.abs((1 - b1) * g)
+        m_off = 2.0 ** -21 * terms + np.where(terms > 0, 2.0 ** -149, 0.0)
+        v_off = 2.0 ** -20 * v1 + np.where(v1 > 0, 2.0 ** -149, 0.0)
         w1, d = A.weights(w, m1, v1, t, c, self.wd, self.lr_mult, lr_scale)
         lr = cfg.lr * self.lr_mult * lr_scale
         den = np.sqrt(v1 / (1 - b2 ** t)) + cfg.eps
