@@ -385,8 +385,7 @@ sm_status sm_graph_destroy(sm_graph g);
  *   w, m and v NULL: a parameter that only sm_grad_norm takes (a Muon
  *   step's matrices enter the norm this way); wdt, state and master are
  *   ignored.
- * Pointers are aligned to their elements; a parameter whose pointers (and
- * worker rows) all are aligned to four elements takes the vector path.
+ * Pointers are aligned to their elements.
  *
  * sm_param_set_create validates the list and writes its tables into ws (at
  * least sm_param_set_ws bytes, 256-byte aligned).  It is the set-up call:
@@ -505,8 +504,7 @@ sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float m
  * code, since v = 0 under a nonzero m would divide by eps alone; a negative
  * v counts as 0.  A NaN or infinite m is stored as NaN, a NaN v as NaN, an
  * infinite v as infinity; none of them touches its block's scale.
- * m, v: float32 [count] (16-byte alignment takes the vector path).  m8, v8:
- * [count] bytes (any alignment; 4-byte alignment takes it).  m_scale, v_scale: float32
+ * m, v: float32 [count].  m8, v8: [count] bytes (any alignment).  m_scale, v_scale: float32
  * [ceil(count/256)].  count == 0 is a no-op.
  * Errors: SM_ERR_ARG (null or misaligned pointers, an output overlapping
  *   another buffer), SM_ERR_SHAPE (count < 0 or > 2^40), SM_ERR_HIP.

@@ -24,7 +24,6 @@ enum : uint32_t {
   kPF_W16 = 1,     // bf16 weights
   kPF_G16 = 2,     // bf16 gradients
   kPF_FP8 = 4,     // 8-bit states
-  kPF_VEC = 8,     // every pointer and worker row is aligned to 4 of its entries
 };
 struct ParamEnt {
   void* w;

@@ -117,14 +117,12 @@ sm_status check_param(const sm_param& p, int M) {
 ParamEnt entry_of(const sm_param& p, int M, bool fp8) {
   ParamEnt e;
   std::memset(&e, 0, sizeof(e));
-  const size_t gs = dt_size(p.gdt);
   e.g = p.grad;
   e.count = p.count;
   e.gstride = M > 1 ? p.grad_stride : 0;
   e.lr_mult = 1.0f;
   e.span = step_unit(fp8);
   if (p.gdt == SM_BF16) e.flags |= kPF_G16;
-  bool vec = multiple_of(p.grad, 4 * gs) && e.gstride % 4 == 0;
   if (!norm_only(p)) {
     e.w = p.w;
     e.master = p.master;
@@ -143,11 +141,7 @@ ParamEnt entry_of(const sm_param& p, int M, bool fp8) {
     if (p.wdt == SM_BF16 && !p.master && M == 1 && p.state == SM_STATE_FP8)
       e.span *= kUnitsFp8;
     if (p.state == SM_STATE_FP8) e.flags |= kPF_FP8;
-    const size_t sa = p.state == SM_STATE_FP8 ? 4 : 16;
-    vec = vec && multiple_of(p.w, 4 * dt_size(p.wdt)) && multiple_of(p.master, 16) &&
-          multiple_of(p.m, sa) && multiple_of(p.v, sa);
   }
-  if (vec) e.flags |= kPF_VEC;
   return e;
 }
 
