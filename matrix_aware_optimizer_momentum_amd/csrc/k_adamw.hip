@@ -17,17 +17,20 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnit = kThreads * 4;   // 4 entries per thread
-// Where the data outgrow the 256 MB Infinity Cache, accesses are
-// non-temporal; below that they stay cacheable.  The step writes most of what
-// it reads, so that it moves twice what it holds.  Cacheable / non-temporal:
-//   step, float32 states, bf16 weights  256 MB 41 / 43 us, 512 MB 80 / 83,
-//                                       1 GB 192 / 164
-//   step, 8-bit states, masters         256 MB 41 / 45, 512 MB 88 / 87,
-//                                       1 GB 191 / 170
-//   norm    192 MB 34 / 36 us, 256 MB 43 / 45, 384 MB 70 / 64
-//   pack    192 MB 31 / 36 us, 256 MB 42 / 47, 384 MB 72 / 70
+// The step's accesses are non-temporal: between two steps a forward and a
+// backward pass go through the caches, so that nothing of a set is left in
+// them.  On data that other sets have pushed out, cacheable / non-temporal,
+// by the bytes that a step moves:
+//   float32 states, bf16 weights   16 MB 7.0 / 6.9 us, 64 MB 16.5 / 13.8,
+//                                  256 MB 52 / 45, 512 MB 100 / 84
+//   8-bit states, masters          16 MB 7.3 / 6.9 us, 64 MB 18.2 / 14.7,
+//                                  256 MB 53 / 46, 512 MB 100 / 89
+// (On a set of 256 MB that is still cached, 41 / 43.)  The norm, whose
+// gradients the step reads next, and the states' conversion stay cacheable
+// up to the 256 MB of the Infinity Cache:
+//   norm   256 MB 48 / 46 us, 400 MB 72 / 67, 512 MB 90 / 84
+//   pack   192 MB 35 / 36 us, 256 MB 46 / 46, 400 MB 76 / 70
 constexpr double kStreamBytes = 256.0 * 1024 * 1024;
-constexpr double kStreamStepBytes = 512.0 * 1024 * 1024;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -453,7 +456,7 @@ __global__ void k_adamw_prep(sm_adamw_config c, int64_t* step, const float* gsca
 
 // Sum of the workers' gradients of four entries, in float64: it does not
 // depend on their order, and is rounded once.
-template <typename TG, bool NT>
+template <typename TG>
 __device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0, uint32_t l,
                                            uint32_t left, bool full) {
   const SM_GLOBAL TG* gp = at<TG>(p.g, u0);
@@ -461,7 +464,7 @@ __device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0,
 #pragma unroll 4
   for (int k = 0; k < M; ++k) {
     float x[4];
-    expand4(get4<TG, NT>(gp + k * p.gstride, l, left, full), x);
+    expand4(get4<TG, true>(gp + k * p.gstride, l, left, full), x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += (double)x[e];
   }
@@ -506,7 +509,7 @@ __device__ __forceinline__ uint32_t unit_left(int64_t count, int64_t u0) {
 }
 
 // full: the thread has all four entries.  ONE: a single worker.
-template <typename TS, typename TG, bool FP8, bool ONE, bool NT, typename H>
+template <typename TS, typename TG, bool FP8, bool ONE, typename H>
 __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, uint32_t left,
                                           bool full, H& h) {
   const uint32_t l = threadIdx.x * 4;
@@ -515,21 +518,21 @@ __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, 
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t blk = u0 / kStateBlock + wave;
     const bool inside = wave * kStateBlock < left;
-    h.mc = get4_codes<NT>(at<uint8_t>(p.m, u0), l, left, full);
-    h.vc = get4_codes<NT>(at<uint8_t>(p.v, u0), l, left, full);
+    h.mc = get4_codes<true>(at<uint8_t>(p.m, u0), l, left, full);
+    h.vc = get4_codes<true>(at<uint8_t>(p.v, u0), l, left, full);
     h.ms = inside ? *at<float>(p.ms, blk) : 1.0f;
     h.vs = inside ? *at<float>(p.vs, blk) : 1.0f;
   } else {
-    h.m = get4<float, NT>(at<float>(p.m, u0), l, left, full);
-    h.v = get4<float, NT>(at<float>(p.v, u0), l, left, full);
+    h.m = get4<float, true>(at<float>(p.m, u0), l, left, full);
+    h.v = get4<float, true>(at<float>(p.v, u0), l, left, full);
   }
-  h.w = get4<TS, NT>(at<TS>(sizeof(TS) == 4 && p.master ? p.master : p.w, u0), l, left, full);
-  if constexpr (ONE) h.g = get4<TG, NT>(at<TG>(p.g, u0), l, left, full);
-  else h.g = sum_grad4<TG, NT>(p, M, u0, l, left, full);
+  h.w = get4<TS, true>(at<TS>(sizeof(TS) == 4 && p.master ? p.master : p.w, u0), l, left, full);
+  if constexpr (ONE) h.g = get4<TG, true>(at<TG>(p.g, u0), l, left, full);
+  else h.g = sum_grad4<TG>(p, M, u0, l, left, full);
 }
 
 // TW: the weights' type.  TS float32 with bf16 weights: they have a master.
-template <typename TW, typename TS, bool FP8, bool NT, typename H>
+template <typename TW, typename TS, bool FP8, typename H>
 __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalars& a, float f,
                                             float keep, float step, uint32_t key0, int64_t u0,
                                             uint32_t left, bool full, const H& h) {
@@ -554,27 +557,27 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   SM_GLOBAL TW* wp = at<TW>(p.w, u0);
   if constexpr (SR_W) {
     if (a.stochastic)
-      put4_bf16<NT>(wp, l, left, full, bf16_pair_stochastic(w[0], w[1], y[0], y[1]),
+      put4_bf16<true>(wp, l, left, full, bf16_pair_stochastic(w[0], w[1], y[0], y[1]),
                     bf16_pair_stochastic(w[2], w[3], y[2], y[3]));
     else
-      put4<TW, NT>(wp, l, left, full, w);
+      put4<TW, true>(wp, l, left, full, w);
   } else {
-    put4<TW, NT>(wp, l, left, full, w);
+    put4<TW, true>(wp, l, left, full, w);
   }
-  if constexpr (MASTER) put4<float, NT>(at<float>(p.master, u0), l, left, full, w);
+  if constexpr (MASTER) put4<float, true>(at<float>(p.master, u0), l, left, full, w);
   if constexpr (FP8) {
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t blk = u0 / kStateBlock + wave;
     const Codes c = encode_block<true>(m, v, y);
-    put4_codes<NT>(at<uint8_t>(p.m, u0), l, left, full, c.m);
-    put4_codes<NT>(at<uint8_t>(p.v, u0), l, left, full, c.v);
+    put4_codes<true>(at<uint8_t>(p.m, u0), l, left, full, c.m);
+    put4_codes<true>(at<uint8_t>(p.v, u0), l, left, full, c.v);
     if (wave * kStateBlock < left && (threadIdx.x & 63) == 0) {
       *at<float>(p.ms, blk) = c.ms;
       *at<float>(p.vs, blk) = c.vs;
     }
   } else {
-    put4<float, NT>(at<float>(p.m, u0), l, left, full, m);
-    put4<float, NT>(at<float>(p.v, u0), l, left, full, v);
+    put4<float, true>(at<float>(p.m, u0), l, left, full, m);
+    put4<float, true>(at<float>(p.v, u0), l, left, full, v);
   }
 }
 
@@ -590,7 +593,7 @@ __device__ __forceinline__ int xcd_run(int b, int items) {
 }
 
 // One work item: one unit, or kUnitsFp8 of them.
-template <bool FP8, bool NT>
+template <bool FP8>
 __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
                                                             bool device, const float* gscale,
                                                             const float* lr_scale) {
@@ -619,22 +622,22 @@ __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, Ad
       Held<TS, TG, F8> h[units];
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        load_unit<TS, TG, F8, true, NT>(p, 1, first + u * UNIT, UNIT, true, h[u]);
+        load_unit<TS, TG, F8, true>(p, 1, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key0, first + u * UNIT, UNIT,
+        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first + u * UNIT, UNIT,
                                     true, h[u]);
     } else if (whole) {
       Held<TS, float, F8> h;
-      load_unit<TS, TG, F8, false, NT>(p, set.M, first, UNIT, true, h);
-      finish_unit<TW, TS, F8, NT>(p, a, f, keep, step, key0, first, UNIT, true, h);
+      load_unit<TS, TG, F8, false>(p, set.M, first, UNIT, true, h);
+      finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first, UNIT, true, h);
     } else {
       for (int64_t u0 = first; u0 < first + span && u0 < p.count; u0 += UNIT) {
         const uint32_t left = unit_left<UNIT>(p.count, u0);
         const bool full = threadIdx.x * 4 + 4 <= left;
         Held<TS, float, F8> h;
-        load_unit<TS, TG, F8, false, false>(p, set.M, u0, left, full, h);
-        finish_unit<TW, TS, F8, false>(p, a, f, keep, step, key0, u0, left, full, h);
+        load_unit<TS, TG, F8, false>(p, set.M, u0, left, full, h);
+        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, u0, left, full, h);
       }
     }
   };
@@ -848,9 +851,7 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
                        const float* gscale, const float* lr_scale, bool fp8, double bytes,
                        hipStream_t s) {
   if (set.nitems == 0) return SM_OK;
-  const bool stream = bytes > kStreamStepBytes;
-  const auto kernel = fp8 ? (stream ? k_adamw<true, true> : k_adamw<true, false>)
-                          : (stream ? k_adamw<false, true> : k_adamw<false, false>);
+  const auto kernel = fp8 ? k_adamw<true> : k_adamw<false>;
   prof_begin(SM_K_ADAMW, bytes, s);
   hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(step_threads(fp8)), 0, s, set, a, device, gscale,
                      lr_scale);

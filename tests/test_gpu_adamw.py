@@ -337,8 +337,8 @@ def test_entries_far_beyond_32_bits(gpu_lib):
     (36_000_513, "master", "f32", True, 1), (40_000_004, "master", "bf16", True, 3),
 ])
 def test_sets_beyond_the_cache(gpu_lib, n, w, g, fp8, M):
-    """Steps that move more than 512 MB (non-temporal accesses, runs of items
-    per XCD), two of them; windows at both ends and in between."""
+    """Steps that move more than 512 MB (runs of items per XCD), two of them;
+    windows at both ends and in between."""
     gen = torch.Generator(device="cuda")
     gen.manual_seed(n)
     wt = (0.02 * torch.randn(n, generator=gen, device="cuda")).to(DT["f32" if w == "f32" else "bf16"])
