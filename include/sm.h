@@ -1,5 +1,8 @@
 /*
  * sm.h - C ABI of the MI355X (gfx950) Muon-family optimizer step library.
+ * Beside the Muon steps of weight matrices it has the AdamW step of a
+ * model's other parameters (sm_param_set, sm_adamw, sm_grad_norm,
+ * sm_state8_pack / sm_state8_unpack).
  *
  * One optimizer step of Sign-Muon, CacheMuon or LionMuon on a set of weight
  * matrices, with M data-parallel workers simulated on one GPU as M gradient

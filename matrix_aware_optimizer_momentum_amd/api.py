@@ -616,6 +616,8 @@ class ParamSet:
                 "sm_param_set_ws")
         if ws is not None:
             _dev(ws, "ws")
+            if ws.device != self.device:
+                raise ValueError("ws must be on the tensors' device")
         self.ws = _ws(need.value, self.device, ws)
         self._index = self.device.index
         self._stream = _stream_of(self._index)   # which the tables' memory belongs to

@@ -101,7 +101,7 @@ __host__ __device__ inline AdamwScalars adamw_scalars(const sm_adamw_config& c, 
 struct ParamSetDev {
   const ParamEnt* ents;
   const WorkItem* items;      // the step's
-  const WorkItem* norm_at;  // the norm's
+  const WorkItem* norm_at;    // the norm's
   AdamwScalars* scalars;      // of a step with a device-side index
   uint32_t* counter;          // of a norm's workgroups, 0 between calls
   double* parts;              // a norm's sums of squares, one per workgroup

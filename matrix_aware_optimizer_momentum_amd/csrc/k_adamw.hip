@@ -120,8 +120,9 @@ __device__ __forceinline__ void expand_all(u32x4 a, float* v, bf16_t) {
 }
 
 // Four entries from p + l on, of which `left` from p on exist.  full: all of
-// them do; otherwise missing ones read as 0 and are not written.  p is uniform and l the lane's offset, so that the
-// addresses are a scalar base and a 32-bit offset.
+// them do; otherwise missing ones read as 0 and are not written.  p is
+// uniform and l the lane's offset, so that the addresses are a scalar base
+// and a 32-bit offset.
 template <typename T, bool NT>
 __device__ __forceinline__ typename Raw4<T>::type get4(const SM_GLOBAL T* p, uint32_t l,
                                                        uint32_t left, bool full) {
@@ -488,10 +489,10 @@ __device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float 
   }
 }
 
-// What a thread holds of one unit (4 entries, the wave's 256 one block of an 8-bit
-// state), as loaded: nothing waits for these loads
-// until finish_unit.  TS: the weights that are read; TG: the gradients, or
-// float for the sum of several workers'.
+// What a thread holds of one unit (4 entries, the wave's 256 one block of an
+// 8-bit state), as loaded: nothing waits for these loads until finish_unit.
+// TS: the weights that are read; TG: the gradients, or float for the sum of
+// several workers'.
 template <typename TS, typename TG, bool FP8>
 struct Held {
   typename Raw4<TG>::type g;
@@ -558,7 +559,7 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   if constexpr (SR_W) {
     if (a.stochastic)
       put4_bf16<true>(wp, l, left, full, bf16_pair_stochastic(w[0], w[1], y[0], y[1]),
-                    bf16_pair_stochastic(w[2], w[3], y[2], y[3]));
+                      bf16_pair_stochastic(w[2], w[3], y[2], y[3]));
     else
       put4<TW, true>(wp, l, left, full, w);
   } else {
@@ -592,7 +593,12 @@ __device__ __forceinline__ int xcd_run(int b, int items) {
   return first + 8 * RUN <= items ? first + (in % 8) * RUN + in / 8 : b;
 }
 
-// One work item: one unit, or kUnitsFp8 of them.
+// One work item: one unit, or kUnitsFp8 of them.  HBM bounds it: 1.81-1.85
+// ms for 495 M bf16 entries with float32 states (22 bytes each, 5.9-6.0
+// TB/s), 164 us for a 64 M-entry embedding with 8-bit states and masters (16
+// bytes, 6.3 TB/s).  With 8-bit states and stochastic weights (10 bytes, 0.82
+// ms, 6.1 TB/s) the vector units are busy throughout as well, at 51
+// instructions an entry, half of them for the random bits.
 template <bool FP8>
 __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
                                                             bool device, const float* gscale,
@@ -625,8 +631,7 @@ __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, Ad
         load_unit<TS, TG, F8, true>(p, 1, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first + u * UNIT, UNIT,
-                                    true, h[u]);
+        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first + u * UNIT, UNIT, true, h[u]);
     } else if (whole) {
       Held<TS, float, F8> h;
       load_unit<TS, TG, F8, false>(p, set.M, first, UNIT, true, h);
@@ -731,12 +736,14 @@ __device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, int64
   return acc;
 }
 
-// The sums of squares of a set, one per workgroup.  A call's last launch also
-// joins the sums of all its sets: its last workgroup to come adds them, in
-// their order.  The counter wraps to 0 with that one, ready for the next
-// call.  The sums are written and read by atomics at device scope, past the
-// XCDs' own L2s: a release fence in each workgroup, which writes back its
-// XCD's L2, took 90 us over 2048 workgroups.
+// The sums of squares of a set, one per workgroup (495 M bf16 entries in
+// 143-148 us, 6.7-6.9 TB/s).  A call's last launch also joins the sums of all
+// its sets: its last workgroup to come adds them, in their order.  The
+// counter wraps to 0 with that one, ready for the next call.  The sums are
+// written and read by atomics at device scope, past the XCDs' own L2s: a
+// release fence in each workgroup, which writes back its XCD's L2, took 90
+// us over 2048 workgroups.  A second launch for the joining took a small set
+// (290 vectors) from 8.7 to 11 us.
 template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_grad_norm(ParamSetDev set, NormJoin f) {
   __shared__ double red[4];
@@ -781,6 +788,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(ParamSetDev set, NormJoi
 
 // ------------------------------------------------------------------ 8-bit states
 
+// A wave per block, 4 entries per lane (64 M entries: 102-106 us each way,
+// 6.1-6.3 TB/s).
 template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_state8_pack(const float* m, const float* v,
                                                           int64_t count, uint8_t* m8, uint8_t* v8,
@@ -853,8 +862,8 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
   if (set.nitems == 0) return SM_OK;
   const auto kernel = fp8 ? k_adamw<true> : k_adamw<false>;
   prof_begin(SM_K_ADAMW, bytes, s);
-  hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(step_threads(fp8)), 0, s, set, a, device, gscale,
-                     lr_scale);
+  hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(step_threads(fp8)), 0, s, set, a, device,
+                     gscale, lr_scale);
   prof_end(s);
   return check_launch();
 }
@@ -863,7 +872,8 @@ sm_status launch_grad_norm(const ParamSetDev& set, const NormJoin& f, double byt
                            hipStream_t s) {
   prof_begin(SM_K_GRAD_NORM, bytes, s);
   const auto kernel = bytes > kStreamBytes ? k_grad_norm<true> : k_grad_norm<false>;
-  hipLaunchKernelGGL(kernel, dim3(norm_set_parts(set.norm_items, set.M)), dim3(kThreads), 0, s, set, f);
+  hipLaunchKernelGGL(kernel, dim3(norm_set_parts(set.norm_items, set.M)), dim3(kThreads), 0, s,
+                     set, f);
   prof_end(s);
   return check_launch();
 }

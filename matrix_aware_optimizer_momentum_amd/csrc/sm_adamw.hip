@@ -239,8 +239,8 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
         if (p.count > 0) h->update = false;
         continue;
       }
-      h->step_bytes += c * (p.master ? 8.0 + dt_size(p.wdt) : 2.0 * dt_size(p.wdt)) +
-                       (p.state == SM_STATE_FP8 ? 4.0 * c + 16.0 * state_blocks(p.count) : 16.0 * c);
+      h->step_bytes += c * (p.master ? 8.0 + dt_size(p.wdt) : 2.0 * dt_size(p.wdt));
+      h->step_bytes += p.state == SM_STATE_FP8 ? 4.0 * c + 16.0 * state_blocks(p.count) : 16.0 * c;
     }
     st = launch_set_fill(t, k, i0, ents, wi, ni, h->dev.counter, s);
   }
