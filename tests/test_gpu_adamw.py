@@ -555,6 +555,114 @@ def test_other_streams(gpu_lib):
         assert np.array_equal(raw(x), raw(y))
 
 
+def test_shapes_rows_and_shared_gradients(gpu_lib):
+    """Weights of any rank, gradients with and without the leading 1, two
+    parameters on one gradient, a workspace of the caller's: all as flat ones."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    g = 0.01 * torch.randn(6, 5, 41, generator=gen, device="cuda")
+
+    def params(shapes):
+        out = []
+        for k, (ws, gs) in enumerate(shapes):
+            p = sm.ParamBuffers.with_state(torch.full(ws, 0.5, device="cuda"), g.view(gs),
+                                           fp8=k % 2 == 1)
+            out.append(p)
+        return out
+
+    n = g.numel()
+    cfg = sm.AdamWConfig(seed=4)
+    results = []
+    for shapes in ([((6, 5, 41), (6, 5, 41)), ((6, 205), (1, 6, 205)), ((n,), (1, n))],
+                   [((n,), (n,))] * 3):
+        ps = params(shapes)
+        ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+        pset = sm.ParamSet(ps, ws=ws)
+        for t in (1, 2):
+            sm.adamw(cfg, pset, t)
+        norm = sm.grad_norm([pset], 1.0)
+        torch.cuda.synchronize()
+        results.append([raw(x) for p in ps for x in (p.w, p.m, p.v)] + [raw(norm)])
+    assert all(np.array_equal(a, b) for a, b in zip(*results))
+    assert abs(float(norm[0]) - float((3 * g.double().square().sum()).sqrt())) < 1e-5
+
+
+def test_hyper_parameters_at_their_ends(gpu_lib):
+    """No averaging, no decay, no schedule, eps from 1e-15 to large, far steps."""
+    for kw in (dict(beta1=0.0), dict(beta2=0.0), dict(beta1=0.0, beta2=0.0), dict(eps=1e-15),
+               dict(eps=10.0), dict(beta1=0.999, beta2=0.99999), dict(lr=0.0)):
+        run_and_check([Case(n, w, "bf16", f, wd=0.01) for n in (70, 1500) for w in ("f32", "bf16")
+                       for f in (False, True)], **kw)
+    run_and_check([Case(900, "f32", "f32", f) for f in (False, True)], t=(1 << 40) + 3,
+                  seed=(1 << 64) - 1)
+
+
+def test_schedule_factor_with_a_host_index(gpu_lib):
+    a, b = ([Case(n, "f32", "f32", f, wd=0.3) for n in (90, 3000) for f in (False, True)]
+            for _ in range(2))
+    sm.adamw(sm.AdamWConfig(lr=1e-2), sm.ParamSet([c.buffers() for c in a]), 4,
+             lr_scale=torch.tensor(0.25, device="cuda"))
+    sm.adamw(sm.AdamWConfig(lr=2.5e-3), sm.ParamSet([c.buffers() for c in b]), 4)
+    torch.cuda.synchronize()
+    # 0.25 * float32(1e-2) is float32(2.5e-3)
+    for x, y in zip(_snapshot(a), _snapshot(b)):
+        assert all(np.array_equal(p, q) for p, q in zip(x, y))
+
+
+def test_two_graphs_of_one_set(gpu_lib):
+    """The norm and the step captured apart, replayed in turn, with another set's
+    norm joined; equal to the eager calls."""
+    def make():
+        a, b = Case(5000, "bf16", "bf16", True), Case(40000, "f32", "f32")
+        return [a, b], sm.ParamSet([a.buffers()]), sm.ParamSet([b.grad_only()])
+    cs, p1, p2 = make()
+    ce, q1, q2 = make()
+    out = torch.zeros(2, device="cuda")
+    step, step_e = (torch.zeros(1, dtype=torch.int64, device="cuda") for _ in range(2))
+    cfg = sm.AdamWConfig(seed=21, rounding=sm.ROUND_STOCHASTIC)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        sm.grad_norm([p1, p2], 0.3, scale=0.5, out=out)
+    with torch.cuda.graph(g2):
+        sm.adamw(cfg, p1, step=step, gscale=out[1:])
+    for k in range(5):
+        for a, b in zip(cs, ce):
+            x = torch.randn_like(a.grad.float()) * 0.01
+            a.grad.copy_(x)
+            b.grad.copy_(x)
+        g1.replay()
+        g2.replay()
+        o = sm.grad_norm([q1, q2], 0.3, scale=0.5)
+        sm.adamw(cfg, q1, step=step_e, gscale=o[1:])
+        torch.cuda.synchronize()
+        assert torch.equal(o, out) and int(step) == k + 1
+        assert all(np.array_equal(p, q) for p, q in zip(_snapshot(cs)[0], _snapshot(ce)[0]))
+
+
+def test_a_set_made_and_dropped_on_side_streams(gpu_lib):
+    """Sets whose tables belong to one stream, used on another and dropped at
+    once, while the first stream allocates over what it gets back."""
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = Case(200000, "bf16", "bf16", True), Case(200000, "bf16", "bf16", True)
+    torch.cuda.synchronize()
+    cfg = sm.AdamWConfig(seed=1)
+    pb = sm.ParamSet([b.buffers()])
+    for t in range(1, 9):
+        with torch.cuda.stream(s1):
+            ps = sm.ParamSet([a.buffers()])
+        with torch.cuda.stream(s2):
+            sm.adamw(cfg, ps, t)
+        del ps
+        with torch.cuda.stream(s1):
+            for _ in range(4):
+                torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda")
+        sm.adamw(cfg, pb, t)
+    torch.cuda.synchronize()
+    for x, y in zip(a.written(), b.written()):
+        assert np.array_equal(raw(x), raw(y))
+
+
 def test_refusals_of_a_live_set(gpu_lib):
     c = Case(64)
     ps = sm.ParamSet([c.buffers()])
