@@ -394,8 +394,11 @@ sm_status sm_graph_destroy(sm_graph g);
  * least sm_param_set_ws bytes, 256-byte aligned).  It is the set-up call:
  * it waits for the tables to be written, so that the set may be used on any
  * stream of the device afterwards.  The buffers that the list names, and
- * ws, must stay allocated, in place, until sm_param_set_destroy, which does
- * not wait: call it once the work enqueued with the set has finished.
+ * ws (which belongs to this set alone), must stay allocated, in place, until
+ * sm_param_set_destroy, which does not wait: call it once the work enqueued
+ * with the set has finished.  A graph captured from calls on the set holds
+ * the addresses of the buffers and of ws: none of them may be freed or used
+ * for anything else before the graph's last replay has finished.
  * Errors: SM_ERR_ARG (n < 1, null or misaligned pointers, missing or
  *   unexpected scales or master, bad weight_decay or lr_mult, grad_stride <
  *   count with M > 1, a buffer that is written overlapping any other of the

@@ -617,13 +617,28 @@ def _plain(p: ParamBuffers, M: int, device) -> bool:
             v.device == device)
 
 
+# Sets whose calls some graph has captured.  A graph holds the addresses of a
+# set's tables and buffers, and no references: the set stays until its close().
+_captured_sets = set()
+
+
+def _capturing(index: int) -> bool:
+    """Device `index`'s current stream is being captured into a graph."""
+    if torch._C._cuda_getDevice() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class ParamSet:
     """A list of parameters that one call works on (sm_param_set): its tables
     on the GPU, made once.
 
     The buffers are bound at construction and must stay in place while the
-    set, or a graph captured from its calls, lives.  Calls on one set (steps
-    and norms) must be ordered."""
+    set, or a graph captured from its calls, lives.  A set whose calls were
+    captured is kept, with its buffers and workspace, until its close() is
+    called, which has to wait until those graphs are replayed no more.  Calls
+    on one set (steps and norms) must be ordered."""
 
     def __init__(self, params: Sequence[ParamBuffers], M: int = 1,
                  ws: Optional[torch.Tensor] = None):
@@ -662,9 +677,13 @@ class ParamSet:
         s = _stream_of(self._index)
         if s != self._stream:
             self.ws.record_stream(torch.cuda.current_stream(self.device))
+        if s and _capturing(self._index):   # the null stream cannot be captured
+            _captured_sets.add(self)
         return s
 
     def close(self):
+        """Ends the set, once no graph captured from its calls is replayed any more."""
+        _captured_sets.discard(self)
         if self._h is not None:
             h, self._h = self._h, None
             B.lib().sm_param_set_destroy(h)

@@ -3,8 +3,10 @@ implementations (torch.optim.AdamW in float64, torch's float8 conversions),
 the struct layouts, and every refusal of the C ABI and the Python front end
 (all on the host, before any HIP call)."""
 import ctypes
+import gc
 import os
 import subprocess
+import weakref
 
 import numpy as np
 import pytest
@@ -305,3 +307,47 @@ def test_with_state_makes_empty_states():
     assert p.m.shape == p.v.shape == w.shape and p.m_scale.shape == p.v_scale.shape == (3,)
     assert not p.m.view(torch.uint8).any() and not p.v.view(torch.uint8).any()
     assert torch.equal(p.master, w.float())
+
+
+# ---------------------------------------------------------------- what a set keeps alive
+
+@pytest.fixture
+def host_sets(monkeypatch):
+    """ParamSet over CPU tensors: the whole front end but the GPU calls.
+    capturing[0]: whether the current stream is being captured."""
+    from matrix_aware_optimizer_momentum_amd import api
+    capturing = [False]
+    monkeypatch.setattr(api, "_check_param", lambda *a: None)
+    monkeypatch.setattr(api, "_stream_of", lambda index: 0x1000)
+    monkeypatch.setattr(api, "_call_on", lambda index, name, *a: None)
+    monkeypatch.setattr(api, "_capturing", lambda index: capturing[0], raising=False)
+    return capturing
+
+
+@pytest.mark.parametrize("call", [lambda ps: sm.adamw(sm.AdamWConfig(), ps, 1),
+                                  lambda ps: sm.grad_norm([ps], 1.0)], ids=["step", "norm"])
+def test_a_set_of_captured_calls_is_kept_until_it_is_closed(host_sets, call):
+    """A graph replays on the set's tables and buffers: they stay after the
+    caller's last reference to the set, and go with close()."""
+    ps = sm.ParamSet([_bufs()])
+    ws, state = weakref.ref(ps.ws), weakref.ref(ps.params[0].m)
+    host_sets[0] = True
+    call(ps)
+    host_sets[0] = False
+    alive = weakref.ref(ps)
+    del ps
+    gc.collect()
+    assert alive() is not None and ws() is not None and state() is not None
+    alive().close()
+    gc.collect()
+    assert alive() is None and ws() is None and state() is None
+
+
+def test_a_set_of_eager_calls_goes_with_its_last_reference(host_sets):
+    ps = sm.ParamSet([_bufs()])
+    sm.adamw(sm.AdamWConfig(), ps, 1)
+    sm.grad_norm([ps], 1.0)
+    alive = weakref.ref(ps)
+    del ps
+    gc.collect()
+    assert alive() is None

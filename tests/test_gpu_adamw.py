@@ -17,6 +17,9 @@ k roundings is off by at most k * 2^-24 of its terms (half a step each):
 be between the two ends (in almost all cases they agree), and its block's
 scale one that the interval of its largest entry allows.
 """
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -906,3 +909,47 @@ def test_kernel_times_are_accounted(gpu_lib):
             assert n >= 1 and ms > 0 and work >= least
     finally:
         sm.profile_enable(False)
+
+
+# ---------------------------------------------------------------- what graphs hold
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+def test_a_graph_outlives_the_references_to_its_set(gpu_lib, fp8):
+    """Norm and step captured, the set's last reference dropped and memory of
+    its tables' size written over and over: the replays equal the eager loop's
+    steps; close() lets the set go."""
+    def make():
+        cs = [Case(n, "bf16", "bf16", fp8) for n in (33, 2048, 7000)]
+        return cs, sm.ParamSet([c.buffers() for c in cs])
+    eager, pe = make()
+    graphed, pg = make()
+    cfg = sm.AdamWConfig(lr=3e-3, rounding=sm.ROUND_STOCHASTIC, seed=23)
+    se, sg = (torch.zeros(1, dtype=torch.int64, device="cuda") for _ in range(2))
+    out = torch.zeros(2, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        sm.grad_norm([pg], 1.0, out=out)
+        sm.adamw(cfg, pg, step=sg, gscale=out[1:])
+    size, alive = pg.ws.numel(), weakref.ref(pg)
+    del pg
+    gc.collect()
+    assert alive() is not None      # else a replay would run on freed tables
+    for k in range(4):
+        for _ in range(4):
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        for a, b in zip(eager, graphed):
+            x = 0.03 * torch.randn_like(a.grad.float())
+            a.grad.copy_(x)
+            b.grad.copy_(x)
+        graph.replay()
+        o = sm.grad_norm([pe], 1.0)
+        sm.adamw(cfg, pe, step=se, gscale=o[1:])
+        torch.cuda.synchronize()
+        assert int(se) == int(sg) == k + 1 and torch.equal(o, out)
+        for x, y in zip(_snapshot(eager), _snapshot(graphed)):
+            assert all(np.array_equal(p, q) for p, q in zip(x, y)), k
+    del graph
+    alive().close()
+    gc.collect()
+    assert alive() is None
