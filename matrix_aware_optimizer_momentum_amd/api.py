@@ -634,8 +634,9 @@ class ParamSet:
     """A list of parameters that one call works on (sm_param_set): its tables
     on the GPU, made once.
 
-    The buffers are bound at construction and must stay in place while the
-    set, or a graph captured from its calls, lives.  A set whose calls were
+    The buffers are bound at construction (a ParamBuffers changed afterwards
+    changes nothing in the set) and must stay in place while the set, or a
+    graph captured from its calls, lives.  A set whose calls were
     captured is kept, with its buffers and workspace, until its close() is
     called, which has to wait until those graphs are replayed no more.  Calls
     on one set (steps and norms) must be ordered."""
@@ -648,6 +649,9 @@ class ParamSet:
         if M < 1:
             raise ValueError("M must be at least 1")
         self.params = list(params)
+        # the tensors themselves: a field of a ParamBuffers may be set anew
+        self._tensors = [(p.grad, p.w, p.m, p.v, p.m_scale, p.v_scale, p.master)
+                         for p in self.params]
         self.M = M
         self.device = self.params[0].grad.device
         for j, p in enumerate(self.params):

@@ -351,3 +351,19 @@ def test_a_set_of_eager_calls_goes_with_its_last_reference(host_sets):
     del ps
     gc.collect()
     assert alive() is None
+
+
+def test_a_set_keeps_the_tensors_that_it_was_made_of(host_sets):
+    """Its tables hold their addresses, also after a field of a ParamBuffers
+    has been set anew."""
+    p = _bufs(wdt=torch.bfloat16, fp8=True, master=True)
+    names = ("grad", "w", "m", "v", "m_scale", "v_scale", "master")
+    held = [weakref.ref(getattr(p, name)) for name in names]
+    ps = sm.ParamSet([p])
+    for name in names:
+        setattr(p, name, getattr(p, name).clone())
+    gc.collect()
+    assert all(t() is not None for t in held)
+    del ps
+    gc.collect()
+    assert all(t() is None for t in held)
