@@ -98,6 +98,15 @@ __host__ __device__ inline AdamwScalars adamw_scalars(const sm_adamw_config& c, 
   return a;
 }
 
+// The hardware's square root takes values below 2^-126 as 0, and its
+// reciprocal is 0 above 2^126.  The first moves the denominator, at least eps,
+// by up to 2^-63 / sqrt(1 - b2^t), most at t = 1: by 2^-22 of it or less
+// unless eps is tiny (at b2 = 0.999 below 1.4e-11).  The second needs a huge
+// eps.  For such an eps the step scales both.
+inline bool scaled_roots(const sm_adamw_config& c) {
+  return 0x1p-41f / sqrtf(1.0f - c.beta2) > c.eps || c.eps > 0x1p100f;
+}
+
 struct ParamSetDev {
   const ParamEnt* ents;
   const WorkItem* items;      // the step's
@@ -125,11 +134,11 @@ sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, W
 sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float* gscale,
                             const float* lr_scale, AdamwScalars* out, hipStream_t s);
 // The step itself: scalars from the arguments, or from set.scalars if
-// `device`.  fp8: some parameter has 8-bit states.  bytes: what the step
-// reads and writes.
+// `device`.  fp8: some parameter has 8-bit states.  scaled: scaled_roots.
+// bytes: what the step reads and writes.
 sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool device,
-                       const float* gscale, const float* lr_scale, bool fp8, double bytes,
-                       hipStream_t s);
+                       const float* gscale, const float* lr_scale, bool fp8, bool scaled,
+                       double bytes, hipStream_t s);
 
 // Workgroups of a set's gradient norm, one sum of squares (over M^2) each.
 // Few, since each adds to one counter: 495 M bf16 entries of one worker take

@@ -477,15 +477,25 @@ __device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0,
 
 // The moments' averages and the weights' change, the same for both kinds of
 // states.  sqrt and the reciprocal are the hardware's (each within an ulp):
-// their error is relative to one step's change, not to the weight.
+// their error is relative to one step's change, not to the weight.  SCALED:
+// powers of two keep their arguments and results normal (scaled_roots).
+template <bool SCALED>
 __device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float step,
                                        const float* g, float* m, float* v, float* w) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     m[e] = a.b1 * m[e] + a.a1 * g[e];
     v[e] = a.b2 * v[e] + a.a2 * (g[e] * g[e]);
-    const float den = __fmaf_rn(__builtin_amdgcn_sqrtf(v[e]), a.root, a.eps);
-    w[e] = __fmaf_rn(-step, m[e] * __builtin_amdgcn_rcpf(den), w[e] * keep);
+    float d;
+    if constexpr (SCALED) {
+      const bool low = v[e] < 0x1p-126f;
+      const float root = __builtin_amdgcn_sqrtf(low ? v[e] * 0x1p64f : v[e]);
+      const float den = __fmaf_rn(low ? root * 0x1p-32f : root, a.root, a.eps);
+      d = m[e] * __builtin_amdgcn_rcpf(den * 0x1p-32f) * 0x1p-32f;
+    } else {
+      d = m[e] * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_sqrtf(v[e]), a.root, a.eps));
+    }
+    w[e] = __fmaf_rn(-step, d, w[e] * keep);
   }
 }
 
@@ -533,7 +543,7 @@ __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, 
 }
 
 // TW: the weights' type.  TS float32 with bf16 weights: they have a master.
-template <typename TW, typename TS, bool FP8, typename H>
+template <typename TW, typename TS, bool FP8, bool SCALED, typename H>
 __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalars& a, float f,
                                             float keep, float step, uint32_t key0, int64_t u0,
                                             uint32_t left, bool full, const H& h) {
@@ -550,7 +560,7 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) g[e] = g[e] * f;
-  adamw4(a, keep, step, g, m, v, w);
+  adamw4<SCALED>(a, keep, step, g, m, v, w);
   constexpr bool SR_W = sizeof(TS) == 2, MASTER = sizeof(TW) == 2 && sizeof(TS) == 4;
   uint32_t y[4];
   if (FP8 || (SR_W && a.stochastic))
@@ -599,10 +609,10 @@ __device__ __forceinline__ int xcd_run(int b, int items) {
 // bytes, 6.3 TB/s).  With 8-bit states and stochastic weights (10 bytes, 0.82
 // ms, 6.1 TB/s) the vector units are busy throughout as well, at 51
 // instructions an entry, half of them for the random bits.
-template <bool FP8>
-__global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
-                                                            bool device, const float* gscale,
-                                                            const float* lr_scale) {
+template <bool FP8, bool SCALED>
+__device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwScalars& arg,
+                                           bool device, const float* gscale,
+                                           const float* lr_scale) {
   constexpr int UNIT = step_unit(FP8);
   const WorkItem it = load_const(set.items + xcd_run<FP8 ? 64 : 256>(blockIdx.x, set.nitems));
   const ParamEnt p = load_const(set.ents + it.tensor);
@@ -631,18 +641,18 @@ __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, Ad
         load_unit<TS, TG, F8, true>(p, 1, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first + u * UNIT, UNIT, true, h[u]);
+        finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first + u * UNIT, UNIT, true, h[u]);
     } else if (whole) {
       Held<TS, float, F8> h;
       load_unit<TS, TG, F8, false>(p, set.M, first, UNIT, true, h);
-      finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, first, UNIT, true, h);
+      finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first, UNIT, true, h);
     } else {
       for (int64_t u0 = first; u0 < first + span && u0 < p.count; u0 += UNIT) {
         const uint32_t left = unit_left<UNIT>(p.count, u0);
         const bool full = threadIdx.x * 4 + 4 <= left;
         Held<TS, float, F8> h;
         load_unit<TS, TG, F8, false>(p, set.M, u0, left, full, h);
-        finish_unit<TW, TS, F8>(p, a, f, keep, step, key0, u0, left, full, h);
+        finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, u0, left, full, h);
       }
     }
   };
@@ -662,6 +672,20 @@ __global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, Ad
     }
   }
   weights(std::false_type());
+}
+template <bool FP8>
+__global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
+                                                            bool device, const float* gscale,
+                                                            const float* lr_scale) {
+  adamw_item<FP8, false>(set, arg, device, gscale, lr_scale);
+}
+// A kernel of its own: behind a uniform branch of the one above the scaling
+// costs every step 73 registers, where seven waves per SIMD leave 72, and 30
+// spilled scalars.
+template <bool FP8>
+__global__ __launch_bounds__(step_threads(FP8)) void k_adamw_scaled(
+    ParamSetDev set, AdamwScalars arg, bool device, const float* gscale, const float* lr_scale) {
+  adamw_item<FP8, true>(set, arg, device, gscale, lr_scale);
 }
 
 // ------------------------------------------------------------------ gradient norm
@@ -857,10 +881,11 @@ sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float
 }
 
 sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool device,
-                       const float* gscale, const float* lr_scale, bool fp8, double bytes,
-                       hipStream_t s) {
+                       const float* gscale, const float* lr_scale, bool fp8, bool scaled,
+                       double bytes, hipStream_t s) {
   if (set.nitems == 0) return SM_OK;
-  const auto kernel = fp8 ? k_adamw<true> : k_adamw<false>;
+  const auto kernel = scaled ? (fp8 ? k_adamw_scaled<true> : k_adamw_scaled<false>)
+                             : (fp8 ? k_adamw<true> : k_adamw<false>);
   prof_begin(SM_K_ADAMW, bytes, s);
   hipLaunchKernelGGL(kernel, dim3(set.nitems), dim3(step_threads(fp8)), 0, s, set, a, device,
                      gscale, lr_scale);

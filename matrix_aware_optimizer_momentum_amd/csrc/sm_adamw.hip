@@ -282,7 +282,7 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
     a = adamw_scalars(*c, t);
   }
   return launch_adamw(set->dev, a, step != nullptr, gscale, lr_scale, set->fp8,
-                      set->step_bytes, s);
+                      scaled_roots(*c), set->step_bytes, s);
 }
 
 sm_status sm_grad_norm(const sm_param_set* sets, int nsets, float scale, float max_norm,

@@ -953,3 +953,25 @@ def test_a_graph_outlives_the_references_to_its_set(gpu_lib, fp8):
     alive().close()
     gc.collect()
     assert alive() is None
+
+
+# ---------------------------------------------------------------- tiny and huge eps
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+def test_second_moments_below_the_normal_range_count_beside_a_tiny_eps(gpu_lib, fp8):
+    """beta2 = 0.99999 and t = 1: v = 1e-5 g^2 from 9e-41 to 1e-37, across
+    2^-126, whose root times 316 is up to a tenth of eps = 1e-15.  v is held
+    to 2^-149 / 9e-41 = 2^-16 of itself at worst, half of that in the root,
+    which is 0.3 % of the denominator there: 2^-26 of the change."""
+    c = Case(600, "f32", "f32", fp8, zero=True)
+    c.grad[0] = torch.from_numpy(np.geomspace(3e-18, 1e-16, 600).astype(np.float32)).cuda()
+    run_and_check([c], t=1, lr=0.1, beta2=0.99999, eps=1e-15)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+def test_the_change_under_a_huge_eps(gpu_lib, fp8):
+    """eps beyond 2^126, whose reciprocal is below the normal range: the change
+    is m / eps all the same (weights of 0 show it)."""
+    c = Case(600, "f32", "f32", fp8, zero=True, gsize=1e18)
+    c.w.zero_()
+    run_and_check([c], t=1, lr=1.0, eps=2e38)
