@@ -485,9 +485,10 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
  *            sm_adamw takes as gscale; NaN if out[0] is not finite, so that
  *            the step is skipped.
  * scale undoes a loss scaling (1 if there is none); max_norm may be
- * infinity (no clipping).  Sums of up to 8 squares in float32, beyond that in
- * float64, in a fixed order; a square beyond float32's range (an entry above
- * 1.8e19) makes the norm infinite.
+ * infinity (no clipping).  The workers' sum in float64, sums of up to 8
+ * squares in float32, beyond that in float64, in a fixed order.  A square
+ * beyond float32's range (an entry of the mean above 1.8e19) makes the norm
+ * infinite; entries below 1e-19 lose bits of theirs, and below 1e-23 count as 0.
  * sets: 1..8 different sets (of any M and types), whose scratch the call
  * uses.  out: 2 floats, outside every set's buffers.
  * Errors: SM_ERR_ARG (null or misaligned pointers, nsets < 1, a set twice,

@@ -115,7 +115,10 @@ struct ParamSetDev {
   uint32_t* counter;          // of a norm's workgroups, 0 between calls
   double* parts;              // a norm's sums of squares, one per workgroup
   int nitems, norm_items, M;
-  float inv_M;
+  // The workers' sum is rounded to float32 after a division by P, the power
+  // of two from M on: it is in the mean's range then.  The rest is P / M.
+  double inv_P;
+  float P_over_M;
 };
 
 // Tables of up to kFillMax parameters written per launch (they ride in the
@@ -140,7 +143,7 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
                        const float* gscale, const float* lr_scale, bool fp8, bool scaled,
                        double bytes, hipStream_t s);
 
-// Workgroups of a set's gradient norm, one sum of squares (over M^2) each.
+// Workgroups of a set's gradient norm, one sum of squares of the mean each.
 // Few, since each adds to one counter: 495 M bf16 entries of one worker take
 // 143 us with 512 workgroups, 148 with 1024, 158 with 2048.
 // Several workers' rows are read with fewer bytes in flight per lane: 270 M

@@ -455,11 +455,12 @@ __global__ void k_adamw_prep(sm_adamw_config c, int64_t* step, const float* gsca
   if (!a.skip) *step = t;
 }
 
-// Sum of the workers' gradients of four entries, in float64: it does not
-// depend on their order, and is rounded once.
+// Sum of the workers' gradients of four entries over P (ParamSetDev), in
+// float64 and rounded once.  (Gradients of one entry less than 2^23 apart are
+// summed exactly, whatever M.)
 template <typename TG>
-__device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0, uint32_t l,
-                                           uint32_t left, bool full) {
+__device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, double inv_P, int64_t u0,
+                                           uint32_t l, uint32_t left, bool full) {
   const SM_GLOBAL TG* gp = at<TG>(p.g, u0);
   double s[4] = {};
 #pragma unroll 4
@@ -471,7 +472,7 @@ __device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, int64_t u0,
   }
   u32x4 g;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) g[e] = __float_as_uint((float)s[e]);
+  for (int e = 0; e < 4; ++e) g[e] = __float_as_uint((float)(s[e] * inv_P));
   return g;
 }
 
@@ -521,8 +522,8 @@ __device__ __forceinline__ uint32_t unit_left(int64_t count, int64_t u0) {
 
 // full: the thread has all four entries.  ONE: a single worker.
 template <typename TS, typename TG, bool FP8, bool ONE, typename H>
-__device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, uint32_t left,
-                                          bool full, H& h) {
+__device__ __forceinline__ void load_unit(const ParamEnt& p, int M, double inv_P, int64_t u0,
+                                          uint32_t left, bool full, H& h) {
   const uint32_t l = threadIdx.x * 4;
   if constexpr (FP8) {
     // the wave's block, uniform
@@ -539,7 +540,7 @@ __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, int64_t u0, 
   }
   h.w = get4<TS, true>(at<TS>(sizeof(TS) == 4 && p.master ? p.master : p.w, u0), l, left, full);
   if constexpr (ONE) h.g = get4<TG, true>(at<TG>(p.g, u0), l, left, full);
-  else h.g = sum_grad4<TG>(p, M, u0, l, left, full);
+  else h.g = sum_grad4<TG>(p, M, inv_P, u0, l, left, full);
 }
 
 // TW: the weights' type.  TS float32 with bf16 weights: they have a master.
@@ -624,7 +625,7 @@ __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwSc
   const float mult = ls * p.lr_mult;
   const float keep = (float)(1.0 - (double)(a.lr * mult) * (double)p.wd);
   const float step = a.step * mult;
-  const float f = gs * set.inv_M;
+  const float f = gs * set.P_over_M;
   const int64_t span = p.span, first = (int64_t)it.chunk * span;
   const uint32_t key0 = mix_key(a.key, it.tensor);
   auto item = [&](auto tw, auto ts, auto tg, auto fp8) {
@@ -638,20 +639,20 @@ __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwSc
       Held<TS, TG, F8> h[units];
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        load_unit<TS, TG, F8, true>(p, 1, first + u * UNIT, UNIT, true, h[u]);
+        load_unit<TS, TG, F8, true>(p, 1, 1.0, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
       for (int u = 0; u < units; ++u)
         finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first + u * UNIT, UNIT, true, h[u]);
     } else if (whole) {
       Held<TS, float, F8> h;
-      load_unit<TS, TG, F8, false>(p, set.M, first, UNIT, true, h);
+      load_unit<TS, TG, F8, false>(p, set.M, set.inv_P, first, UNIT, true, h);
       finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first, UNIT, true, h);
     } else {
       for (int64_t u0 = first; u0 < first + span && u0 < p.count; u0 += UNIT) {
         const uint32_t left = unit_left<UNIT>(p.count, u0);
         const bool full = threadIdx.x * 4 + 4 <= left;
         Held<TS, float, F8> h;
-        load_unit<TS, TG, F8, false>(p, set.M, u0, left, full, h);
+        load_unit<TS, TG, F8, false>(p, set.M, set.inv_P, u0, left, full, h);
         finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, u0, left, full, h);
       }
     }
@@ -713,8 +714,8 @@ __device__ __forceinline__ float sumsq16(u32x4 a) {
 // 16-byte loads in flight.
 constexpr int kNormFlight = 8;
 template <typename TG, bool NT>
-__device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, int64_t gstride,
-                                             uint32_t left) {
+__device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, double inv_P,
+                                             int64_t gstride, uint32_t left) {
   constexpr uint32_t E = 16 / sizeof(TG), STEP = kThreads * E;
   static_assert(kNormSpan % (STEP * kNormFlight) == 0, "whole rounds");
   const uint32_t l = threadIdx.x * E;
@@ -746,7 +747,10 @@ __device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, int64
       }
       float q = 0.f;
 #pragma unroll
-      for (uint32_t e = 0; e < E; ++e) q = __fmaf_rn((float)s[e], (float)s[e], q);
+      for (uint32_t e = 0; e < E; ++e) {
+        const float x = (float)(s[e] * inv_P);
+        q = __fmaf_rn(x, x, q);
+      }
       acc += (double)q;
     }
   }
@@ -755,7 +759,8 @@ __device__ __forceinline__ double sumsq_item(const SM_GLOBAL TG* g, int M, int64
   if (threadIdx.x < left - tail) {
     double s = 0.0;
     for (int k = 0; k < M; ++k) s += (double)to_f32(g[k * gstride + tail + threadIdx.x]);
-    acc += (double)((float)s * (float)s);
+    const float x = (float)(s * inv_P);
+    acc += (double)(x * x);
   }
   return acc;
 }
@@ -779,10 +784,11 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(ParamSetDev set, NormJoi
     const int64_t first = (int64_t)it.chunk * kNormSpan;
     const uint32_t left = unit_left<kNormSpan>(p.count, first);
     acc += (p.flags & kPF_G16)
-               ? sumsq_item<bf16_t, NT>(at<bf16_t>(p.g, first), set.M, p.gstride, left)
-               : sumsq_item<float, NT>(at<float>(p.g, first), set.M, p.gstride, left);
+               ? sumsq_item<bf16_t, NT>(at<bf16_t>(p.g, first), set.M, set.inv_P, p.gstride, left)
+               : sumsq_item<float, NT>(at<float>(p.g, first), set.M, set.inv_P, p.gstride, left);
   }
-  const double s = block_sum64(acc, red) / ((double)set.M * (double)set.M);
+  const double P_over_M = 1.0 / (set.inv_P * (double)set.M);
+  const double s = block_sum64(acc, red) * (P_over_M * P_over_M);
   if (threadIdx.x == 0) {
     // returns once the sum is where every XCD sees it
     const unsigned long long was =

@@ -214,7 +214,10 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
   h->dev.counter = reinterpret_cast<uint32_t*>(base + lay.counter);
   h->dev.parts = reinterpret_cast<double*>(base + lay.parts);
   h->dev.M = M;
-  h->dev.inv_M = 1.0f / (float)M;
+  int P = 1;
+  while (P < M) P *= 2;
+  h->dev.inv_P = 1.0 / P;
+  h->dev.P_over_M = (float)P / (float)M;
   h->nparam = n;
   h->update = true;
   h->fp8 = has_fp8(params, n);

@@ -975,3 +975,32 @@ def test_the_change_under_a_huge_eps(gpu_lib, fp8):
     c = Case(600, "f32", "f32", fp8, zero=True, gsize=1e18)
     c.w.zero_()
     run_and_check([c], t=1, lr=1.0, eps=2e38)
+
+
+# ---------------------------------------------------------------- large sums of workers
+
+@pytest.mark.parametrize("M", [2, 3, 64])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+def test_step_on_a_mean_whose_sum_leaves_float32(gpu_lib, M, g):
+    """Gradients of 1e38 to 3e38 of one sign: their sum is beyond float32, the
+    mean, and gscale times it, are not.  The roundings are the usual ones."""
+    cases = []
+    for i, (n, fp8) in enumerate((n, f) for n in (7, 1030) for f in (False, True)):
+        c = Case(n, "f32", g, fp8, M=M)
+        x = np.random.default_rng(i).uniform(1e38, 3e38, (M, n)) * np.where(np.arange(n) % 3, 1, -1)
+        c.grad.copy_(torch.from_numpy(x.astype(np.float32)))
+        cases.append(c)
+    run_and_check(cases, M=M, gscale=1e-38 * 2.0)
+
+
+@pytest.mark.parametrize("M", [2, 3, 64])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+def test_norm_of_a_mean_whose_sum_squared_leaves_float32(gpu_lib, M, g):
+    """Entries up to 1.2e19: the mean's squares stay below 3.4e38, the sum's do
+    not (M = 2: 5.8e38).  8 of them may not be added in float32 either, so
+    that large entries stand alone among small ones."""
+    n = 5003
+    c = Case(n, "f32", g, M=M, gsize=1e12)
+    c.grad[:, ::64] = 1.2e19
+    out = sm.grad_norm([sm.ParamSet([c.grad_only()], M=M)], float("inf"), scale=2.0 ** -60)
+    _norm_ok(out, [(M, [c.grads64()])], 2.0 ** -60, float("inf"))
