@@ -476,12 +476,25 @@ __device__ __forceinline__ u32x4 sum_grad4(const ParamEnt& p, int M, double inv_
   return g;
 }
 
+// An infinite value as the largest finite one: under a decay it would be taken
+// from itself.  (Two instructions with their constants inside them: a med3
+// would hold its own in registers, of which the step has none left.)
+__device__ __forceinline__ float clamp_finite(float w) {
+  float r;
+  asm("v_min_f32 %0, 0x7f7fffff, %1" : "=v"(r) : "v"(w));
+  asm("v_max_f32 %0, 0xff7fffff, %0" : "+v"(r));
+  return r;
+}
+
 // The moments' averages and the weights' change, the same for both kinds of
 // states.  sqrt and the reciprocal are the hardware's (each within an ulp):
 // their error is relative to one step's change, not to the weight.  SCALED:
-// powers of two keep their arguments and results normal (scaled_roots).
+// powers of two keep their arguments and results normal (scaled_roots).  The
+// decay and the change are one term, so that a weight is rounded once: a
+// factor 1 - lr wd in float32 would be off by 3 % of a decay of 1e-6 and leave
+// out one below 3e-8, the same way at every step.
 template <bool SCALED>
-__device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float step,
+__device__ __forceinline__ void adamw4(const AdamwScalars& a, float decay, float step,
                                        const float* g, float* m, float* v, float* w) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -496,7 +509,7 @@ __device__ __forceinline__ void adamw4(const AdamwScalars& a, float keep, float 
     } else {
       d = m[e] * __builtin_amdgcn_rcpf(__fmaf_rn(__builtin_amdgcn_sqrtf(v[e]), a.root, a.eps));
     }
-    w[e] = __fmaf_rn(-step, d, w[e] * keep);
+    w[e] = w[e] - __fmaf_rn(step, d, decay * clamp_finite(w[e]));
   }
 }
 
@@ -546,7 +559,7 @@ __device__ __forceinline__ void load_unit(const ParamEnt& p, int M, double inv_P
 // TW: the weights' type.  TS float32 with bf16 weights: they have a master.
 template <typename TW, typename TS, bool FP8, bool SCALED, typename H>
 __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalars& a, float f,
-                                            float keep, float step, uint32_t key0, int64_t u0,
+                                            float decay, float step, uint32_t key0, int64_t u0,
                                             uint32_t left, bool full, const H& h) {
   const uint32_t l = threadIdx.x * 4;
   float g[4], w[4], m[4], v[4];
@@ -561,7 +574,7 @@ __device__ __forceinline__ void finish_unit(const ParamEnt& p, const AdamwScalar
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) g[e] = g[e] * f;
-  adamw4<SCALED>(a, keep, step, g, m, v, w);
+  adamw4<SCALED>(a, decay, step, g, m, v, w);
   constexpr bool SR_W = sizeof(TS) == 2, MASTER = sizeof(TW) == 2 && sizeof(TS) == 4;
   uint32_t y[4];
   if (FP8 || (SR_W && a.stochastic))
@@ -623,7 +636,7 @@ __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwSc
   const float ls = lr_scale ? load_const(lr_scale) : 1.0f;
   if (a.skip || !is_finite(gs) || !is_finite(ls)) return;
   const float mult = ls * p.lr_mult;
-  const float keep = (float)(1.0 - (double)(a.lr * mult) * (double)p.wd);
+  const float decay = a.lr * mult * p.wd;
   const float step = a.step * mult;
   const float f = gs * set.P_over_M;
   const int64_t span = p.span, first = (int64_t)it.chunk * span;
@@ -642,18 +655,19 @@ __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwSc
         load_unit<TS, TG, F8, true>(p, 1, 1.0, first + u * UNIT, UNIT, true, h[u]);
 #pragma unroll
       for (int u = 0; u < units; ++u)
-        finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first + u * UNIT, UNIT, true, h[u]);
+        finish_unit<TW, TS, F8, SCALED>(p, a, f, decay, step, key0, first + u * UNIT, UNIT, true,
+                                        h[u]);
     } else if (whole) {
       Held<TS, float, F8> h;
       load_unit<TS, TG, F8, false>(p, set.M, set.inv_P, first, UNIT, true, h);
-      finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, first, UNIT, true, h);
+      finish_unit<TW, TS, F8, SCALED>(p, a, f, decay, step, key0, first, UNIT, true, h);
     } else {
       for (int64_t u0 = first; u0 < first + span && u0 < p.count; u0 += UNIT) {
         const uint32_t left = unit_left<UNIT>(p.count, u0);
         const bool full = threadIdx.x * 4 + 4 <= left;
         Held<TS, float, F8> h;
         load_unit<TS, TG, F8, false>(p, set.M, set.inv_P, u0, left, full, h);
-        finish_unit<TW, TS, F8, SCALED>(p, a, f, keep, step, key0, u0, left, full, h);
+        finish_unit<TW, TS, F8, SCALED>(p, a, f, decay, step, key0, u0, left, full, h);
       }
     }
   };
@@ -674,10 +688,10 @@ __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwSc
   }
   weights(std::false_type());
 }
+// 72 registers: seven waves per SIMD.
 template <bool FP8>
-__global__ __launch_bounds__(step_threads(FP8)) void k_adamw(ParamSetDev set, AdamwScalars arg,
-                                                            bool device, const float* gscale,
-                                                            const float* lr_scale) {
+__global__ __launch_bounds__(step_threads(FP8)) __attribute__((amdgpu_num_vgpr(72))) void k_adamw(
+    ParamSetDev set, AdamwScalars arg, bool device, const float* gscale, const float* lr_scale) {
   adamw_item<FP8, false>(set, arg, device, gscale, lr_scale);
 }
 // A kernel of its own: behind a uniform branch of the one above the scaling

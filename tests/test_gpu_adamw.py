@@ -1004,3 +1004,40 @@ def test_norm_of_a_mean_whose_sum_squared_leaves_float32(gpu_lib, M, g):
     c.grad[:, ::64] = 1.2e19
     out = sm.grad_norm([sm.ParamSet([c.grad_only()], M=M)], float("inf"), scale=2.0 ** -60)
     _norm_ok(out, [(M, [c.grads64()])], 2.0 ** -60, float("inf"))
+
+
+# ---------------------------------------------------------------- small decays
+
+@pytest.mark.parametrize("lr,wd", [(1e-6, 0.1), (3e-7, 0.2), (1e-4, 0.01)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+@pytest.mark.parametrize("w", ["f32", "master"])
+def test_a_small_decay_is_rounded_with_the_weight_alone(gpu_lib, lr, wd, fp8, w):
+    """No gradient and no moments: a weight is w (1 - lr wd), rounded once, at
+    most half a float32 step of w (and the product's own rounding, 2^-22 of
+    the decay) off."""
+    c = Case(2500, w, "f32", fp8, zero=True, wd=wd)
+    c.grad.zero_()
+    kept = c.w if c.master is None else c.master
+    before = np64(kept)
+    sm.adamw(sm.AdamWConfig(lr=lr), sm.ParamSet([c.buffers()]), 3)
+    torch.cuda.synchronize()
+    decay = A.f32(lr) * A.f32(wd)
+    half = np.spacing(np.abs(before).astype(np.float32)).astype(float) / 2
+    off = np.abs(np64(kept) - before * (1 - decay))
+    assert np.all(off <= half + 2.0 ** -22 * decay * np.abs(before))
+
+
+@pytest.mark.parametrize("wd", [0.0, 0.1])
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+@pytest.mark.parametrize("w", ["f32", "bf16", "master"])
+def test_an_infinite_weight_stays_one(gpu_lib, w, fp8, wd):
+    c = Case(900, w, "bf16", fp8, wd=wd)
+    for t in (c.w, c.master):
+        if t is not None:
+            t[5], t[700] = float("inf"), float("-inf")
+    sm.adamw(sm.AdamWConfig(lr=1e-2), sm.ParamSet([c.buffers()]), 3)
+    torch.cuda.synchronize()
+    for t in (c.w, c.master):
+        if t is not None:
+            x = np64(t)
+            assert x[5] == np.inf and x[700] == -np.inf and np.isfinite(x).sum() == 898
