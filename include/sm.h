@@ -439,7 +439,14 @@ sm_status sm_param_set_destroy(sm_param_set set);
  * 8-bit states are decoded, updated in float32 (the weights' update uses
  * those values) and encoded again with stochastic rounding: with beta2 =
  * 0.999 a step moves v by a tenth of a percent while neighbouring codes lie
- * 14-25 % apart, so rounding to nearest would leave v where it is.
+ * 14-25 % apart, so rounding to nearest would leave v where it is.  The chance
+ * of the code above or below is a multiple of 2^-16, off by 2^-17 at most.  A v
+ * that decays alone leaves a code that is k of the steps below it (5 to 8; 1 to
+ * 4 among the smallest codes) with a chance of (1 - beta2) k: right to 0.2 % at
+ * beta2 = 0.999, to 2 % at 0.9999 and to 16 % at 0.99999 (five times that among
+ * the smallest codes); m, of 9 to 16 steps, to 9 % at beta1 = 0.99999.  Slower
+ * averages would stand still: a set with 8-bit states takes no beta above
+ * 0.99999.
  * rounding: SM_ROUND_STOCHASTIC rounds bf16 weights without a master
  *   stochastically as well (unbiased over steps, where a nearest rounding
  *   loses updates below half a bf16 step); other weights ignore it.
@@ -465,7 +472,8 @@ sm_status sm_param_set_destroy(sm_param_set set);
  * Errors: SM_ERR_ARG (null config or set, a set with sm_grad_norm-only
  *   parameters, t < 1 without step, t != 0 with it, misaligned pointers, lr
  *   < 0 or not finite, betas outside [0, 1), eps < 1e-15 or not finite, bad
- *   rounding), SM_ERR_HIP.
+ *   rounding), SM_ERR_UNSUPPORTED (a beta above 0.99999 with 8-bit states),
+ *   SM_ERR_HIP.
  * ---------------------------------------------------------------------- */
 typedef enum { SM_ROUND_NEAREST = 0, SM_ROUND_STOCHASTIC = 1 } sm_rounding;
 

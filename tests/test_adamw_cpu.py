@@ -75,6 +75,20 @@ def test_stochastic_grid_is_unbiased_and_random_bits_are_uniform():
         assert (other == r).mean() < 1e-4
 
 
+@pytest.mark.parametrize("kind,steps", [("v", range(5, 9)), ("m", range(9, 17))])
+@pytest.mark.parametrize("beta,off", [(0.999, 0.002), (0.9999, 0.02), (0.99999, 0.2)])
+def test_decaying_moments_leave_their_codes_at_the_stated_rate(kind, steps, beta, off):
+    """A moment that is k of the steps below it (a power of two: of the finer
+    ones) falls with a chance of (1 - beta) k, in steps of 2^-16: over all
+    16-bit numbers, to 2^-17 / ((1 - beta) k), at k = 5 0.16, 1.6 and 16 %."""
+    u = (np.arange(65536) + 0.5) / 65536
+    for k in steps:
+        x = float(k) * 2.0 ** 3
+        want = (1 - beta) * k
+        got = (A.to_grid(np.full(65536, beta * x), kind, u) < x).mean()
+        assert abs(got - want) <= 2.0 ** -17 * 1.001 and abs(got / want - 1) < off
+
+
 @pytest.mark.parametrize("kind", ["m", "v"])
 def test_oracle_scale_brackets_the_largest(kind):
     largest = A.KINDS[kind][3]

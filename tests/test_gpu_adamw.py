@@ -1041,3 +1041,23 @@ def test_an_infinite_weight_stays_one(gpu_lib, w, fp8, wd):
         if t is not None:
             x = np64(t)
             assert x[5] == np.inf and x[700] == -np.inf and np.isfinite(x).sum() == 898
+
+
+# ---------------------------------------------------------------- slow averages
+
+def test_averages_too_slow_for_8_bit_states_are_refused(gpu_lib):
+    """Above 0.99999 such a moment would stand still; float32 states take any
+    beta below 1, and so does the limit itself."""
+    c8, c32 = Case(600, "f32", "f32", True), Case(600, "f32", "f32", False)
+    both = sm.ParamSet([c32.buffers(), c8.buffers()])
+    before = _snapshot([c8, c32])
+    for kw in (dict(beta2=0.999999), dict(beta1=0.999999), dict(beta2=0.999991)):
+        with pytest.raises(sm.SmError) as e:
+            sm.adamw(sm.AdamWConfig(**kw), both, 1)
+        assert e.value.code == 5, kw
+    torch.cuda.synchronize()
+    for x, y in zip(before, _snapshot([c8, c32])):
+        assert all(np.array_equal(p, q) for p, q in zip(x, y))
+    del both
+    run_and_check([c8], beta1=0.99999, beta2=0.99999)
+    run_and_check([c32], beta1=0.999999, beta2=0.999999)
