@@ -889,14 +889,23 @@ sm_status launch_set_fill(const FillTbl& t, int n, int index0, ParamEnt* ents, W
   for (int q = 0; q < n; ++q)
     most = std::max<int64_t>(most, step_items(t.e[q]));
   const dim3 grid((unsigned)std::min<int64_t>((most + kThreads - 1) / kThreads, 1024), n);
+  double bytes = 0.0;   // written
+  for (int q = 0; q < n; ++q)
+    bytes += sizeof(ParamEnt) + sizeof(WorkItem) * (double)(step_items(t.e[q]) +
+                                                            sm::norm_items(t.e[q].count));
+  prof_begin(SM_K_MISC, bytes, s);
   hipLaunchKernelGGL(k_set_fill, grid, dim3(kThreads), 0, s, t, index0, ents, items, norm_items,
                      counter);
+  prof_end(s);
   return check_launch();
 }
 
 sm_status launch_adamw_prep(const sm_adamw_config& c, int64_t* step, const float* gscale,
                             const float* lr_scale, AdamwScalars* out, hipStream_t s) {
+  // the step's index read and written, the factors, the scalars
+  prof_begin(SM_K_MISC, 16.0 + (gscale ? 4 : 0) + (lr_scale ? 4 : 0) + sizeof(AdamwScalars), s);
   hipLaunchKernelGGL(k_adamw_prep, dim3(1), dim3(64), 0, s, c, step, gscale, lr_scale, out);
+  prof_end(s);
   return check_launch();
 }
 

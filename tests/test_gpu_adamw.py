@@ -1061,3 +1061,22 @@ def test_averages_too_slow_for_8_bit_states_are_refused(gpu_lib):
     del both
     run_and_check([c8], beta1=0.99999, beta2=0.99999)
     run_and_check([c32], beta1=0.999999, beta2=0.999999)
+
+
+# ---------------------------------------------------------------- accounting
+
+def test_small_launches_are_accounted_as_well(gpu_lib):
+    """The tables' fill and the kernel of a device-side step index: kind misc."""
+    cases = [Case(40 + i) for i in range(70)]      # three fills
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    sm.profile_enable(True)
+    try:
+        sm.profile_reset()
+        ps = sm.ParamSet([c.buffers() for c in cases])
+        assert sm.profile_read("misc")[1] == 3
+        sm.adamw(sm.AdamWConfig(), ps, step=step)
+        ms, n, work = sm.profile_read("misc")
+        assert n == 4 and ms > 0 and work >= 70 * (88 + 16) + 16
+        assert sm.profile_read("adamw")[1] == 1
+    finally:
+        sm.profile_enable(False)
