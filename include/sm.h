@@ -544,6 +544,7 @@ sm_status sm_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* m_
  * fresh solve and cached candidate) are credited with the work of the
  * problems that actually ran: those kernels add it to a small device-side
  * accumulator, which reading and resetting synchronise the device to copy.
+ * Launches into a stream that is being captured are not accounted.
  * Enabling creates an event pool (up to 65536 launches); reading or
  * disabling never allocates.  Not thread-safe; meant for one benchmarking
  * thread, outside timed regions for reads and resets.

@@ -1080,3 +1080,34 @@ def test_small_launches_are_accounted_as_well(gpu_lib):
         assert sm.profile_read("adamw")[1] == 1
     finally:
         sm.profile_enable(False)
+
+
+def test_captured_launches_are_not_accounted(gpu_lib):
+    """Norm and step captured while the accounting is on: the totals are the
+    eager calls', and the graph replays."""
+    c = Case(5000, "bf16", "bf16", True)
+    ps = sm.ParamSet([c.buffers()])
+    out = torch.zeros(2, device="cuda")
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def one():
+        sm.grad_norm([ps], 1.0, out=out)
+        sm.adamw(sm.AdamWConfig(), ps, step=step, gscale=out[1:])
+
+    torch.cuda.synchronize()
+    sm.profile_enable(True)
+    try:
+        sm.profile_reset()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            one()
+        for _ in range(3):
+            graph.replay()
+            one()
+        torch.cuda.synchronize()
+        assert int(step) == 6
+        for kind in ("grad_norm", "adamw", "misc"):
+            ms, n, work = sm.profile_read(kind)
+            assert n == 3 and ms > 0, kind
+    finally:
+        sm.profile_enable(False)
