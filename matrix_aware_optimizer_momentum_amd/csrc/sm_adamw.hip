@@ -8,7 +8,6 @@
 
 struct sm_param_set_s {
   sm::ParamSetDev dev;
-  int nparam;
   bool update;        // every parameter has weights and states
   bool fp8;           // some have 8-bit states
   double step_bytes;  // of one AdamW step
@@ -222,7 +221,6 @@ sm_status sm_param_set_create(const sm_param* params, int n, int M, void* ws, si
   while (P < M) P *= 2;
   h->dev.inv_P = 1.0 / P;
   h->dev.P_over_M = (float)P / (float)M;
-  h->nparam = n;
   h->update = true;
   h->fp8 = has_fp8(params, n);
   h->step_bytes = h->grad_bytes = 0.0;
