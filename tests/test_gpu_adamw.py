@@ -1111,3 +1111,99 @@ def test_captured_launches_are_not_accounted(gpu_lib):
             assert n == 3 and ms > 0, kind
     finally:
         sm.profile_enable(False)
+
+
+# ---------------------------------------------------------------- any alignment, far rows, two at once
+
+@pytest.mark.parametrize("shift", [1, 3])
+@pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
+def test_step_of_long_unaligned_buffers(gpu_lib, fp8, shift):
+    """Whole work items, of one unit and of several, off alignment."""
+    run_and_check([Case(n, w, g, fp8, shift=shift, wd=0.05)
+                   for n in (6145, 20000) for w, g in (("f32", "f32"), ("master", "bf16"),
+                                                       ("bf16", "bf16"), ("bf16", "f32"))])
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3, 7])
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+def test_norm_of_long_unaligned_gradients(gpu_lib, g, shift):
+    """One worker's whole rounds (16384 entries) and the rest at any offset."""
+    cases = [Case(n, "f32", g, shift=shift) for n in (16384, 16385, 50007)]
+    out = sm.grad_norm([sm.ParamSet([c.grad_only() for c in cases])], 1.0)
+    _norm_ok(out, [(1, [c.grads64() for c in cases])], 1.0, 1.0)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("n", [1, 255, 2305, 9001])
+def test_conversion_of_codes_at_any_byte(gpu_lib, n, offset):
+    """Codes written to and read from odd addresses: as the aligned ones, and
+    nothing beside them written."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n)
+    m = torch.randn(n, generator=gen, device="cuda")
+    v = torch.randn(n, generator=gen, device="cuda").square()
+    m8, v8, ms, vs = sm.state8_pack(m, v)
+    bufs = [torch.full((n + 16,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.empty_like(ms) for _ in range(2)]
+    code = sm.lib().sm_state8_pack(m.data_ptr(), v.data_ptr(), n, bufs[0].data_ptr() + offset,
+                                   bufs[1].data_ptr() + offset, scales[0].data_ptr(),
+                                   scales[1].data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    torch.cuda.synchronize()
+    for buf, want, scale, want_scale in zip(bufs, (m8, v8), scales, (ms, vs)):
+        assert torch.equal(buf[offset:offset + n], want.view(torch.uint8))
+        assert bool((buf[:offset] == 0xA5).all()) and bool((buf[offset + n:] == 0xA5).all())
+        assert torch.equal(scale, want_scale)
+    odd = sm.state8_unpack(bufs[0][offset:offset + n].view(m8.dtype),
+                           bufs[1][offset:offset + n].view(v8.dtype), *scales)
+    assert all(torch.equal(a, b) for a, b in zip(odd, sm.state8_unpack(m8, v8, ms, vs)))
+
+
+def test_rows_further_apart_than_32_bits(gpu_lib):
+    """Two workers' rows 2^32 + 5 entries apart: step and norm."""
+    n, stride = 9000, (1 << 32) + 5
+    for fp8 in (False, True):
+        far, near = (Case(n, "f32", "bf16", fp8, M=2) for _ in range(2))
+        buf = torch.empty(stride + n, dtype=torch.bfloat16, device="cuda")
+        far.grad = torch.as_strided(buf, (2, n), (stride, 1))
+        far.grad.copy_(near.grad)
+        outs = []
+        for c in (far, near):
+            ps = sm.ParamSet([c.buffers()], M=2)
+            outs.append(sm.grad_norm([ps], 1.0))
+            sm.adamw(sm.AdamWConfig(seed=3), ps, 2, gscale=outs[-1][1:])
+        torch.cuda.synchronize()
+        assert torch.equal(*outs)
+        _norm_ok(outs[0], [(2, [near.grads64()])], 1.0, 1.0)
+        for x, y in zip(far.written(), near.written()):
+            assert np.array_equal(raw(x), raw(y))
+        del buf, far
+
+
+def test_two_sets_at_once(gpu_lib):
+    """Sets of their own may run on two streams at the same time."""
+    def make(k):
+        cs = [Case(n, "bf16", "bf16", f, wd=0.1) for n in (1000 + k, 400000 + k)
+              for f in (False, True)]
+        return cs, sm.ParamSet([c.buffers() for c in cs])
+    at_once, alone = [make(k) for k in range(2)], [make(k) for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    step = torch.zeros(4, dtype=torch.int64, device="cuda")
+    cfg = sm.AdamWConfig(seed=6, rounding=sm.ROUND_STOCHASTIC)
+    torch.cuda.synchronize()
+    outs = []
+    for t in range(5):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                outs.append(sm.grad_norm([at_once[k][1]], 1.0))
+                sm.adamw(cfg, at_once[k][1], step=step[k:k + 1], gscale=outs[-1][1:])
+    torch.cuda.synchronize()
+    for t in range(5):
+        for k in range(2):
+            out = sm.grad_norm([alone[k][1]], 1.0)
+            sm.adamw(cfg, alone[k][1], step=step[2 + k:3 + k], gscale=out[1:])
+            assert torch.equal(out, outs[2 * t + k])
+    torch.cuda.synchronize()
+    for (a, _), (b, _) in zip(at_once, alone):
+        for x, y in zip(_snapshot(a), _snapshot(b)):
+            assert all(np.array_equal(p, q) for p, q in zip(x, y))
