@@ -382,8 +382,9 @@ sm_status sm_graph_destroy(sm_graph g);
  *   m, v   : [count], first and second moment, updated in place; zero them
  *            before the first step.  state SM_STATE_F32: float32.  state
  *            SM_STATE_FP8: one byte per entry (see sm_state8_pack), with
- *            m_scale, v_scale: float32 [ceil(count/256)], zero or powers of
- *            two (as the library writes them).
+ *            m_scale, v_scale: float32 [ceil(count/256)], powers of two as
+ *            the library writes them, or zero where all of a block's codes
+ *            are zero.
  *   weight_decay >= 0, lr_mult >= 0 (a factor on the step's lr): finite.
  *   w, m and v NULL: a parameter that only sm_grad_norm takes (a Muon
  *   step's matrices enter the norm this way); wdt, state and master are
@@ -457,7 +458,8 @@ sm_status sm_param_set_destroy(sm_param_set set);
  *   key = mix((key ^ d) + C) for d = the low and high halves of seed and of
  *   t, the parameter's index, and the high half of the entry's; r = mix(low
  *   half of the entry's index ^ key).  m takes the low 16 bits of r, v the
- *   high ones, w the low 16 of mix(r ^ 0x9E3779B1).
+ *   high ones, w the low 16 of mix(r ^ 0x9E3779B1).  Two sets stepped with
+ *   one seed get equal bits at equal indices: give each a seed of its own.
  *
  * t: 1-based step index if step is NULL.  step: device int64, the number of
  *   steps done so far; then t must be 0, the step has index *step + 1, and
@@ -466,7 +468,8 @@ sm_status sm_param_set_destroy(sm_param_set set);
  * gscale: optional device float, a factor on the gradients (sm_grad_norm's
  *   out + 1).  lr_scale: optional device float >= 0, a factor on lr (a
  *   schedule's, for captured calls).  If one of them is not finite the whole
- *   step is skipped: nothing is written and *step stays.
+ *   step is skipped: nothing is written and *step stays.  step, gscale and
+ *   lr_scale lie outside the buffers that the set's steps write.
  * Calls on one set (steps and norms) must be ordered by the caller: they
  * share its tensors and its scratch.
  * Errors: SM_ERR_ARG (null config or set, a set with sm_grad_norm-only
@@ -499,6 +502,10 @@ sm_status sm_adamw(const sm_adamw_config* c, sm_param_set set, int64_t t, int64_
  * infinite; entries below 1e-19 lose bits of theirs, and below 1e-23 count as 0.
  * sets: 1..8 different sets (of any M and types), whose scratch the call
  * uses.  out: 2 floats, outside every set's buffers.
+ * The factor, and the skip of a step whose norm is not finite, reach the
+ * parameters that sm_adamw steps with it.  sm_step takes no factor: matrices
+ * that entered the norm are neither scaled nor skipped, and a caller who wants
+ * that reads out before calling sm_step.
  * Errors: SM_ERR_ARG (null or misaligned pointers, nsets < 1, a set twice,
  *   scale not finite, max_norm not > 0), SM_ERR_UNSUPPORTED (nsets > 8),
  *   SM_ERR_HIP.

@@ -489,7 +489,7 @@ class AdamWConfig:
     beta2: float = 0.999
     eps: float = 1e-8
     rounding: int = B.ROUND_NEAREST   # of bf16 weights without a master
-    seed: int = 0                     # of the stochastic rounding, 0 .. 2^64 - 1
+    seed: int = 0                     # of the stochastic rounding, 0 .. 2^64 - 1; one per set
 
     def c_struct(self) -> B.AdamWConfig:
         if not 0 <= self.seed < 1 << 64:
@@ -736,7 +736,8 @@ def grad_norm(psets: Sequence[ParamSet], max_norm: float, scale: float = 1.0,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """float32 [2]: the global norm of the sets' (mean) gradients times |scale|,
     and the factor scale * min(1, max_norm / (norm + 1e-6)) for adamw's gscale
-    (out[1:2]), NaN where the norm is not finite."""
+    (out[1:2]), NaN where the norm is not finite.  A Muon step takes no factor:
+    its matrices are neither scaled nor skipped."""
     if len(psets) == 0:
         raise ValueError("grad_norm needs at least one set")
     first = psets[0]

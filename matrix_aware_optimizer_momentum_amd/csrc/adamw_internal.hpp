@@ -146,8 +146,10 @@ sm_status launch_adamw(const ParamSetDev& set, const AdamwScalars& a, bool devic
 // Workgroups of a set's gradient norm, one sum of squares of the mean each.
 // Few, since each adds to one counter: 495 M bf16 entries of one worker take
 // 143 us with 512 workgroups, 148 with 1024, 158 with 2048.
-// Several workers' rows are read with fewer bytes in flight per lane: 270 M
-// float32 entries of four take 350 us with 1024, 556 with 512, 361 with 2048.
+// Several workers' rows are read with fewer bytes in flight per lane: 67.5 M
+// float32 entries of four workers (1.08 GB) take 207 us with 1024, 317 with
+// 512, 195 with 2048; 135 M bf16 entries of four 202, 322 and 205; 60 M bf16
+// entries of eight (0.96 GB) 150, 145 and 159.
 constexpr int kNormParts1 = 512, kNormPartsM = 1024;
 inline int norm_set_parts(int items, int M) {
   const int most = M == 1 ? kNormParts1 : kNormPartsM;

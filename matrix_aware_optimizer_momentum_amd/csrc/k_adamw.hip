@@ -617,12 +617,12 @@ __device__ __forceinline__ int xcd_run(int b, int items) {
   return first + 8 * RUN <= items ? first + (in % 8) * RUN + in / 8 : b;
 }
 
-// One work item: one unit, or kUnitsFp8 of them.  HBM bounds it: 1.81-1.85
+// One work item: one unit, or kUnitsFp8 of them.  HBM bounds it: 1.83-1.85
 // ms for 495 M bf16 entries with float32 states (22 bytes each, 5.9-6.0
-// TB/s), 164 us for a 64 M-entry embedding with 8-bit states and masters (16
-// bytes, 6.3 TB/s).  With 8-bit states and stochastic weights (10 bytes, 0.82
-// ms, 6.1 TB/s) the vector units are busy throughout as well, at 51
-// instructions an entry, half of them for the random bits.
+// TB/s), 163 us for a 64 M-entry embedding with 8-bit states and masters (16
+// bytes, 6.3 TB/s).  With 8-bit states and stochastic weights (10 bytes,
+// 0.81-0.84 ms, 5.9-6.2 TB/s) the vector units are busy throughout as well, at
+// 53 instructions an entry, half of them for the random bits.
 template <bool FP8, bool SCALED>
 __device__ __forceinline__ void adamw_item(const ParamSetDev& set, const AdamwScalars& arg,
                                            bool device, const float* gscale,

@@ -233,6 +233,8 @@ def test_step_over_many_lengths(gpu_lib, w, g, fp8):
     run_and_check([Case(n, w, g, fp8, wd=0.1 * (n % 2)) for n in LENGTHS], gscale=0.7, steps=2)
 
 
+# Accesses are wide at any alignment: only a tensor's last entries, fewer than
+# four, go one by one.
 @pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
 def test_step_of_unaligned_buffers(gpu_lib, fp8):
     """Buffers at every element offset: the element-wise path."""
@@ -241,6 +243,7 @@ def test_step_of_unaligned_buffers(gpu_lib, fp8):
                                                         ("bf16", "bf16")) for sh in (1, 3)])
 
 
+# Odd rows take the same wide accesses as even ones.
 @pytest.mark.parametrize("M", [2, 3, 64])
 @pytest.mark.parametrize("fp8", [False, True], ids=["f32state", "fp8"])
 def test_step_on_the_mean_of_workers(gpu_lib, M, fp8):
@@ -334,6 +337,7 @@ def test_entries_far_beyond_32_bits(gpu_lib):
     del w, g, p
 
 
+# Runs of items per XCD are taken by sets of any size that have enough items.
 @pytest.mark.parametrize("n,w,g,fp8,M", [
     (30_000_001, "bf16", "bf16", False, 1), (20_000_003, "f32", "f32", False, 1),
     (18_000_002, "f32", "f32", False, 2), (60_000_001, "bf16", "bf16", True, 1),
@@ -759,6 +763,7 @@ def test_norm_of_nothing(gpu_lib):
     assert sm.grad_norm([sets[0], three, sets[2]], float("inf")).tolist() == [3.0, 1.0]
 
 
+# One worker's norm takes at most 512 workgroups, each several items here.
 def test_norms_repeat_over_many_workgroups(gpu_lib):
     """2048 workgroups and more items than that: every call gives the same
     bits, whichever workgroup joins the sums, and leaves the counter ready."""
