@@ -485,7 +485,7 @@ def _check_all(**wanted):
 @dataclass
 class AdamWConfig:
     lr: float = 1e-3
-    beta1: float = 0.9
+    beta1: float = 0.9                # betas with 8-bit states: at most 0.99999
     beta2: float = 0.999
     eps: float = 1e-8
     rounding: int = B.ROUND_NEAREST   # of bf16 weights without a master

@@ -60,7 +60,10 @@ void prof_begin(int kind, double work, hipStream_t s, double bytes) {
   if (!g_prof_on) return;
   // an event in a capture becomes a node of the graph, which no read may wait for
   hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(s, &cap) == hipSuccess && cap != hipStreamCaptureStatusNone) return;
+  if (hipStreamIsCapturing(s, &cap) != hipSuccess)
+    (void)hipGetLastError();   // else the launch would be taken to have failed
+  else if (cap != hipStreamCaptureStatusNone)
+    return;
   const size_t i = g_prof_recs.size();
   if (2 * i + 1 >= g_prof_pool.size()) return;
   ProfRec r{kind, work, bytes < 0.0 ? work : bytes, g_prof_pool[2 * i], g_prof_pool[2 * i + 1]};
