@@ -2,7 +2,9 @@
  * sm.h - C ABI of the MI355X (gfx950) Muon-family optimizer step library.
  * Beside the Muon steps of weight matrices it has the AdamW step of a
  * model's other parameters (sm_param_set, sm_adamw, sm_grad_norm,
- * sm_state8_pack / sm_state8_unpack).
+ * sm_state8_pack / sm_state8_unpack), and the feed-forward layers whose
+ * gradients the steps read (sm_linear, sm_gated, their backward passes, and
+ * 8-bit checkpoints of their inputs).
  *
  * One optimizer step of Sign-Muon, CacheMuon or LionMuon on a set of weight
  * matrices, with M data-parallel workers simulated on one GPU as M gradient
@@ -539,6 +541,114 @@ sm_status sm_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* m_
                            hipStream_t s);
 
 /* ------------------------------------------------------------------------
+ * 8-bit checkpoints of activations: what a layer keeps of its input for the
+ * backward pass (sm_layer's x8), at half of bf16's bytes.
+ * x is [T][d], row r at x + r * ldx.  32 consecutive entries of a row share
+ * a scale 2^e (a row's last block may be shorter), e >= -117 the smallest
+ * exponent with max |x| <= 448 * 2^e over the block's finite entries; a code
+ * is the OCP e4m3 value of x / 2^e, to nearest even, and stands for (its
+ * value) * 2^e.  -117 keeps the smallest code's value, 2^-9 * 2^e, a normal
+ * bf16 number: every value a code stands for is exact in bf16.  Under the
+ * largest scale, 2^120, codes are at most 240's: the next one's value would
+ * be infinite.  An infinite
+ * or NaN entry is stored as NaN and does not touch its block's scale.
+ * x8: [T][d] bytes.  scale: [T][ceil(d/32)] bytes, e + 127 (OCP e8m0).
+ * Both are contiguous, at any alignment.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, ldx < d, an output
+ *   overlapping another buffer), SM_ERR_SHAPE (T < 0 or > 2^30, d < 1 or
+ *   > 2^20), SM_ERR_DTYPE, SM_ERR_HIP.  T == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+#define SM_ACT8_BLOCK 32
+sm_status sm_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int32_t d, uint8_t* x8,
+                       uint8_t* scale, hipStream_t s);
+sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_t T, int32_t d,
+                         void* x, int64_t ldx, hipStream_t s);
+
+/* ------------------------------------------------------------------------
+ * Feed-forward layers, forward and backward, for the gradients that the steps
+ * read: dw may be one worker's matrix of an sm_matrix's grad, dbias a row of
+ * an sm_param's.
+ *   sm_linear       y = act(x W^T + bias) + residual
+ *   sm_linear_grad  dz = dy * act'(x W^T + bias);
+ *                   dx = dz W, dW = dz^T x, dbias = the sum of dz's rows
+ *   sm_gated        y = act(x Wg^T) * (x Wu^T), in one kernel
+ *   sm_gated_grad   with a = x Wg^T, b = x Wu^T:
+ *                   da = dy * b * act'(a), db = dy * act(a);
+ *                   dx = da Wg + db Wu, dWg = da^T x, dWu = db^T x
+ * The backward passes keep nothing of the forward one but x, or its 8-bit
+ * checkpoint, and make z, or a and b, from it again (with a checkpoint: from
+ * the values that its codes stand for, which the gradients are then taken
+ * at).  residual's gradient is dy itself.  With act none dz is dy.
+ *
+ * act: none; relu (slope 0 at 0); silu z / (1 + e^-z); gelu z Phi(z), Phi the
+ *   normal distribution's; gelu_tanh z / (1 + e^-2u) = z (1 + tanh u) / 2, u
+ *   = sqrt(2/pi) (z + 0.044715 z^3).
+ * Precision: products and sums in float32; every result is rounded once, to
+ *   dt.  In between only dz (da, db) are rounded to dt: they are operands of
+ *   the matrix cores in the products that follow, and dbias sums the same
+ *   rounded values.
+ * accumulate: dw, dw2 and dbias are added to (in float32, then rounded), not
+ *   overwritten; dx is always overwritten.
+ * Which fields a call reads:
+ *   all            T, d, n, dt, act, w (and w2 = Wu if gated)
+ *   linear, gated  x, y; linear: bias, residual
+ *   *_grad         x, or x8 and x8_scale (x NULL); dy; dx, dw, (gated) dw2,
+ *                  (linear) bias and dbias; accumulate.  dx, dw, dw2 and
+ *                  dbias may be NULL: not wanted (one at least is).  bias is
+ *                  the forward pass's (read only where act is not none).
+ * Matrices are row-major, row r at p + r * ld entries (ld at least the row's
+ * length), aligned to their entries; operands whose rows are 16-byte aligned
+ * and a multiple of 16 bytes long are read in place, others are laid out in
+ * the workspace first.  y may be residual itself (same pointer and ld); apart
+ * from that no output may overlap another buffer, but matrices of one ld may
+ * be columns of one wider matrix.
+ * T == 0: sm_linear, sm_gated and dx are no-ops; dw, dw2 and dbias are set to
+ * 0, or left as they are with accumulate.
+ * A row of x or dy that holds a NaN or infinity makes its own rows of y and
+ * dx so, and dw, dw2 and dbias as the sums give.
+ * ws: scratch of at least the matching *_ws(...) bytes, 256-byte aligned
+ *   (may be NULL if that is 0); the query takes the call's own arguments.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, a row length above its ld,
+ *   both or neither of x and x8, a bad act, an overlap, no output wanted),
+ *   SM_ERR_SHAPE (T < 0 or > 2^30, d or n < 1 or > 2^20), SM_ERR_DTYPE,
+ *   SM_ERR_WORKSPACE, SM_ERR_HIP.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  SM_ACT_NONE = 0, SM_ACT_RELU = 1, SM_ACT_SILU = 2, SM_ACT_GELU = 3, SM_ACT_GELU_TANH = 4
+} sm_act;
+
+typedef struct {
+  int64_t T;                  /* tokens                                     */
+  int32_t d, n;               /* entries of a token's input and output      */
+  int32_t dt;                 /* sm_dtype of every tensor but the codes     */
+  int32_t act;                /* sm_act                                     */
+  const void* x;              /* [T][d]                                     */
+  const uint8_t* x8;          /* [T][d] codes in the place of x, and their  */
+  const uint8_t* x8_scale;    /*   scales (sm_act8_pack)                    */
+  const void* w;              /* [n][d] W, or Wg                            */
+  const void* w2;             /* [n][d] Wu                                  */
+  const void* bias;           /* [n], or NULL                               */
+  const void* residual;       /* [T][n], or NULL                            */
+  void* y;                    /* [T][n]                                     */
+  const void* dy;             /* [T][n]                                     */
+  void* dx;                   /* [T][d], or NULL                            */
+  void* dw;                   /* [n][d], or NULL                            */
+  void* dw2;                  /* [n][d], or NULL                            */
+  void* dbias;                /* [n], or NULL                               */
+  int64_t ldx, ldw, ldw2, ldr, ldy, lddy, lddx, lddw, lddw2;
+  int32_t accumulate;
+} sm_layer;
+
+sm_status sm_linear_ws(const sm_layer* l, size_t* ws_bytes);
+sm_status sm_linear(const sm_layer* l, void* ws, size_t ws_bytes, hipStream_t s);
+sm_status sm_linear_grad_ws(const sm_layer* l, size_t* ws_bytes);
+sm_status sm_linear_grad(const sm_layer* l, void* ws, size_t ws_bytes, hipStream_t s);
+sm_status sm_gated_ws(const sm_layer* l, size_t* ws_bytes);
+sm_status sm_gated(const sm_layer* l, void* ws, size_t ws_bytes, hipStream_t s);
+sm_status sm_gated_grad_ws(const sm_layer* l, size_t* ws_bytes);
+sm_status sm_gated_grad(const sm_layer* l, void* ws, size_t ws_bytes, hipStream_t s);
+
+/* ------------------------------------------------------------------------
  * Kernel-time accounting (for benchmarks; not part of the method).
  * While enabled, every kernel the library launches is bracketed by a pair of
  * HIP events on its stream, tagged with its kind and its algorithmic work
@@ -572,7 +682,9 @@ enum {
   SM_K_ADAMW = 12,       /* AdamW step over a set                  bytes  */
   SM_K_GRAD_NORM = 13,   /* global gradient norm                   bytes  */
   SM_K_STATE8 = 14,      /* 8-bit states from float32 and back     bytes  */
-  SM_K_NUM_KINDS = 15
+  SM_K_ACT8 = 15,        /* 8-bit checkpoints and back, layouts    bytes  */
+  SM_K_LAYER = 16,       /* feed-forward layers' products          flops  */
+  SM_K_NUM_KINDS = 17
 };
 sm_status sm_profile_enable(int on);
 sm_status sm_profile_reset(void);

@@ -24,11 +24,13 @@ ENC_BITS, ENC_INT8 = 0, 1
 STATE_F32, STATE_FP8 = 0, 1
 ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
 STATE8_BLOCK = 256             # SM_STATE8_BLOCK
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+ACT8_BLOCK = 32                # SM_ACT8_BLOCK
 NS_NOALLOC_MAX_WS = 64 << 20   # SM_NS_NOALLOC_MAX_WS
 
 KERNEL_KINDS = ["ema", "norm", "gemm_gram", "gemm_apply", "gemm_rr", "probe", "sign_pack",
                 "vote_update", "lion", "polar_update", "misc", "spectral", "adamw", "grad_norm",
-                "state8"]
+                "state8", "act8", "layer"]
 
 # Every function the header declares, with its ctypes signature.
 c_int, c_int32, c_int64, c_float, c_double = (ctypes.c_int, ctypes.c_int32, ctypes.c_int64,
@@ -64,6 +66,16 @@ class Param(ctypes.Structure):
 class AdamWConfig(ctypes.Structure):
     _fields_ = [("lr", c_float), ("beta1", c_float), ("beta2", c_float), ("eps", c_float),
                 ("rounding", c_int32), ("seed", c_uint64)]
+
+
+class Layer(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("d", c_int32), ("n", c_int32), ("dt", c_int32), ("act", c_int32),
+                *((name, c_void_p) for name in ("x", "x8", "x8_scale", "w", "w2", "bias",
+                                                "residual", "y", "dy", "dx", "dw", "dw2",
+                                                "dbias")),
+                *((name, c_int64) for name in ("ldx", "ldw", "ldw2", "ldr", "ldy", "lddy", "lddx",
+                                               "lddw", "lddw2")),
+                ("accumulate", c_int32)]
 
 
 P = ctypes.POINTER
@@ -109,6 +121,14 @@ SIGNATURES = {
                                c_void_p, c_void_p]),
     "sm_state8_unpack": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
                                  c_void_p, c_void_p]),
+    "sm_act8_pack": (c_int, [c_void_p, c_int64, c_int, c_int64, c_int32, c_void_p, c_void_p,
+                             c_void_p]),
+    "sm_act8_unpack": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int32, c_void_p, c_int64,
+                               c_void_p]),
+    **{f"sm_{name}_ws": (c_int, [P(Layer), P(c_size_t)])
+       for name in ("linear", "linear_grad", "gated", "gated_grad")},
+    **{f"sm_{name}": (c_int, [P(Layer), c_void_p, c_size_t, c_void_p])
+       for name in ("linear", "linear_grad", "gated", "gated_grad")},
     "sm_profile_enable": (c_int, [c_int]),
     "sm_profile_reset": (c_int, []),
     "sm_profile_read": (c_int, [c_int, P(c_double), P(c_int64), P(c_double)]),

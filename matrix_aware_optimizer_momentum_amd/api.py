@@ -788,6 +788,250 @@ def state8_unpack(m8: torch.Tensor, v8: torch.Tensor, m_scale: torch.Tensor,
     return m, v
 
 
+# ------------------------------------------------------------------ feed-forward layers
+
+@dataclass
+class Act8:
+    """An 8-bit checkpoint of activations (act8_pack): what the backward passes
+    take in the place of x."""
+    codes: torch.Tensor    # [..., d] float8_e4m3fn
+    scale: torch.Tensor    # [..., ceil(d / 32)] float8_e8m0fnu
+
+
+def _rows(t: torch.Tensor, name: str, width: int, dtype, device, rows: Optional[int] = None):
+    """(pointer, row stride) of t as a matrix [rows, width]: dtype, on device, rows contiguous,
+    the leading dimensions at one stride."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() < 1 or t.shape[-1] != width:
+        raise ValueError(f"{name} must have {width} columns, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if rows is not None and t.numel() != rows * width:
+        raise ValueError(f"{name} must have {rows} rows, got {tuple(t.shape)}")
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = span = None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is not None and stride != span:
+            raise ValueError(f"{name}'s rows must be at one stride")
+        if ld is None:
+            ld = stride
+        span = stride * size
+    return t.data_ptr(), width if ld is None else ld
+
+
+def _out_rows(out, like: torch.Tensor, width: int, name: str):
+    """out, or a new tensor of like's leading dimensions and `width` columns."""
+    shape = (*like.shape[:-1], width)
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(out.shape)}")
+    return out
+
+
+def act8_pack(x: torch.Tensor) -> Act8:
+    """x [..., d] (float32 / bfloat16) in 8 bits, 32 entries of a row to a
+    scale, rounded to nearest."""
+    _dt(x)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., d]")
+    d = x.shape[-1]
+    ptr, ld = _rows(x, "x", d, x.dtype, x.device)
+    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty((*x.shape[:-1], (d + B.ACT8_BLOCK - 1) // B.ACT8_BLOCK), dtype=torch.uint8,
+                        device=x.device).view(torch.float8_e8m0fnu)
+    index = x.device.index
+    _call_on(index, "sm_act8_pack", ptr, ld, _dt(x), x.numel() // max(d, 1), d, codes.data_ptr(),
+             scale.data_ptr(), _stream_of(index))
+    return Act8(codes, scale)
+
+
+def _act8(a: Act8, d: int, device, rows: Optional[int] = None):
+    """The pointers of a checkpoint of `rows` rows of d entries."""
+    blocks = (d + B.ACT8_BLOCK - 1) // B.ACT8_BLOCK
+    shape = tuple(a.codes.shape)
+    if a.codes.dim() < 1 or shape[-1] != d or (rows is not None and a.codes.numel() != rows * d):
+        raise ValueError(f"codes must be [{'...' if rows is None else rows}, {d}], got {shape}")
+    _expect(a.codes, "codes", dtype=torch.float8_e4m3fn)
+    _expect(a.scale, "scale", (*shape[:-1], blocks), torch.float8_e8m0fnu)
+    if a.codes.device != device or a.scale.device != device:
+        raise ValueError(f"codes and scale must be on {device}")
+    return a.codes.data_ptr(), a.scale.data_ptr()
+
+
+def act8_unpack(a: Act8, dtype: torch.dtype, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that a checkpoint's codes stand for (exact in both types)."""
+    if dtype not in _DT:
+        raise TypeError(f"dtype {dtype} not supported (float32 / bfloat16)")
+    if a.codes.dim() < 1:
+        raise ValueError("codes must be [..., d]")
+    d, dev = a.codes.shape[-1], a.codes.device
+    codes, scale = _act8(a, d, dev)
+    if out is None:
+        out = torch.empty(a.codes.shape, dtype=dtype, device=dev)
+    elif out.shape != a.codes.shape:
+        raise ValueError(f"out must have shape {tuple(a.codes.shape)}, got {tuple(out.shape)}")
+    ptr, ld = _rows(out, "out", d, dtype, dev)
+    _call_on(dev.index, "sm_act8_unpack", codes, scale, _DT[dtype], out.numel() // max(d, 1), d,
+             ptr, ld, _stream_of(dev.index))
+    return out
+
+
+class _LayerCall:
+    """A sm_layer being filled in: every tensor's check, pointer and stride."""
+
+    def __init__(self, w: torch.Tensor, act: int, tokens: torch.Tensor):
+        """tokens: x or dy, whose leading dimensions are the call's tokens."""
+        _dt(w)
+        if w.dim() != 2 or w.numel() == 0:
+            raise ValueError(f"weights must be [n, d], got {tuple(w.shape)}")
+        if tokens.dim() < 1:
+            raise ValueError("tokens must be [..., width]")
+        self.dtype, self.device = w.dtype, w.device
+        self.n, self.d = w.shape
+        self.T = tokens.numel() // max(tokens.shape[-1], 1)
+        self.c = B.Layer(T=self.T, d=self.d, n=self.n, dt=_DT[w.dtype], act=act)
+        self.weights("w", w)
+
+    def _set(self, field, t, name, width, rows):
+        if t is not None:
+            ptr, ld = _rows(t, name, width, self.dtype, self.device, rows)
+            setattr(self.c, field, ptr)
+            ld_name = {"residual": "ldr"}.get(field, "ld" + field)
+            setattr(self.c, ld_name, ld)
+
+    def weights(self, field, t, name=None):
+        if t is not None and tuple(t.shape) != (self.n, self.d):
+            raise ValueError(f"{name or field} must have shape {(self.n, self.d)}, "
+                             f"got {tuple(t.shape)}")
+        self._set(field, t, name or field, self.d, self.n)
+
+    def inputs(self, field, t, name=None):    # [T, d]
+        self._set(field, t, name or field, self.d, self.T)
+
+    def outputs(self, field, t, name=None):   # [T, n]
+        self._set(field, t, name or field, self.n, self.T)
+
+    def bias(self, field, t, name):
+        if t is not None:
+            _expect(t, name, (self.n,), self.dtype)
+            if t.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+            setattr(self.c, field, t.data_ptr())
+
+    def kept(self, x):
+        if isinstance(x, Act8):
+            self.c.x8, self.c.x8_scale = _act8(x, self.d, self.device, self.T)
+        else:
+            self.inputs("x", x)
+
+    def __call__(self, name: str, ws: Optional[torch.Tensor]):
+        need = ctypes.c_size_t(0)
+        B.check(getattr(B.lib(), name + "_ws")(ctypes.byref(self.c), ctypes.byref(need)), name)
+        size = need.value
+        if ws is None:
+            ws = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        else:
+            _dev(ws, "ws")
+            if ws.device != self.device:
+                raise ValueError("ws must be on the tensors' device")
+            if ws.numel() * ws.element_size() < size:
+                raise ValueError("workspace too small")
+        index = self.device.index
+        _call_on(index, name, ctypes.byref(self.c), ws.data_ptr() if size else None, size,
+                 _stream_of(index))
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           act: int = B.ACT_NONE, residual: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x W^T + bias) + residual in one kernel; x [..., d], w [n, d], bias
+    [n], residual [..., n], all float32 or all bfloat16.  out may be residual."""
+    c = _LayerCall(w, act, x)
+    c.inputs("x", x)
+    c.bias("bias", bias, "bias")
+    c.outputs("residual", residual)
+    out = _out_rows(out, x, c.n, "out")
+    c.outputs("y", out, "out")
+    c("sm_linear", ws)
+    return out
+
+
+def gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: int = B.ACT_SILU,
+          out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x Wg^T) * (x Wu^T) in one kernel; x [..., d], wg and wu [n, d]."""
+    c = _LayerCall(wg, act, x)
+    c.weights("w2", wu, "wu")
+    c.inputs("x", x)
+    out = _out_rows(out, x, c.n, "out")
+    c.outputs("y", out, "out")
+    c("sm_gated", ws)
+    return out
+
+
+def linear_grad(dy: torch.Tensor, x, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                act: int = B.ACT_NONE, dx: Optional[torch.Tensor] = None,
+                dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                need_dx: bool = True, need_dw: bool = True, accumulate: bool = False,
+                ws: Optional[torch.Tensor] = None):
+    """(dx, dw, db) of linear for the gradient dy [..., n] of its result; x is the
+    input or its Act8 checkpoint.  dw (and db, if bias or db is given) may be a
+    worker's gradients of a MatrixBuffers (a ParamBuffers), which accumulate
+    adds to; need_dx, need_dw: False leaves that one out (None)."""
+    c = _LayerCall(w, act, dy)
+    c.bias("bias", bias, "bias")
+    c.kept(x)
+    c.outputs("dy", dy)
+    if accumulate and need_dw and dw is None:
+        raise ValueError("accumulate needs dw")
+    if accumulate and bias is not None and db is None:
+        raise ValueError("accumulate needs db")
+    dx = _out_rows(dx, dy, c.d, "dx") if need_dx else None
+    if need_dw and dw is None:
+        dw = torch.empty_like(w, memory_format=torch.contiguous_format)
+    dw = dw if need_dw else None
+    if bias is not None and db is None:
+        db = torch.empty_like(bias)
+    c.inputs("dx", dx)
+    c.weights("dw", dw)
+    c.bias("dbias", db, "db")
+    c.c.accumulate = int(accumulate)
+    c("sm_linear_grad", ws)
+    return dx, dw, db
+
+
+def gated_grad(dy: torch.Tensor, x, wg: torch.Tensor, wu: torch.Tensor, act: int = B.ACT_SILU,
+               dx: Optional[torch.Tensor] = None, dwg: Optional[torch.Tensor] = None,
+               dwu: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
+               accumulate: bool = False, ws: Optional[torch.Tensor] = None):
+    """(dx, dwg, dwu) of gated for the gradient dy [..., n] of its result; x, the
+    outputs and the rest as for linear_grad."""
+    c = _LayerCall(wg, act, dy)
+    c.weights("w2", wu, "wu")
+    c.kept(x)
+    c.outputs("dy", dy)
+    if accumulate and need_dw and (dwg is None or dwu is None):
+        raise ValueError("accumulate needs dwg and dwu")
+    dx = _out_rows(dx, dy, c.d, "dx") if need_dx else None
+    if need_dw:
+        dwg = torch.empty_like(wg, memory_format=torch.contiguous_format) if dwg is None else dwg
+        dwu = torch.empty_like(wu, memory_format=torch.contiguous_format) if dwu is None else dwu
+    else:
+        dwg = dwu = None
+    c.inputs("dx", dx)
+    c.weights("dw", dwg, "dwg")
+    c.weights("dw2", dwu, "dwu")
+    c.c.accumulate = int(accumulate)
+    c("sm_gated_grad", ws)
+    return dx, dwg, dwu
+
+
 # ------------------------------------------------------------------ kernel accounting
 
 def mfma_ceiling(out: torch.Tensor, blocks: int, iters: int, mode: int = 1,

@@ -1,0 +1,57 @@
+// Declarations shared by the feed-forward layers' kernels (k_layer*.hip,
+// k_act8.hip) and their C ABI (sm_layer.hip).
+#pragma once
+
+#include "sm_internal.hpp"
+
+namespace sm {
+
+// What a product of a layer computes, and with it its operands' layouts.
+// An operand is k-contiguous (KC: rows x K, row-major) or k-major (KR: K x
+// rows).
+//   kLinear      c = act(A B^T + bias) + in          A = x KC,  B = W KC
+//   kSlope       c = in * act'(A B^T + bias)         A = x KC,  B = W KC
+//   kGated       c = act(a) b,  a = A B^T, b = A B2^T      x, Wg and Wu KC
+//   kGatedSlope  c = in b act'(a),  c2 = in act(a)         x, Wg and Wu KC
+//   kDx          c = A B (+ A2 B2)                   A = dz KC, B = W KR
+//   kDw          c (+)= A^T B  (and c2 (+)= A2^T B)  A = dz KR, B = x KR
+enum ProductKind : int { kLinear, kSlope, kGated, kGatedSlope, kDx, kDw };
+constexpr bool kind_dual(int k) { return k == kGated || k == kGatedSlope; }
+constexpr bool kind_a_kr(int k) { return k == kDw; }
+constexpr bool kind_b_kr(int k) { return k == kDx || k == kDw; }
+
+struct Operand {
+  const void* p;
+  int64_t ld;   // entries
+};
+struct Product {
+  int kind, dt, act;
+  int M, N, K;        // c is M x N, sums over K
+  int parts;          // kDx: 2 with a[1], b[1]; kDw: 2 with a[1], c[1]
+  Operand a[2], b[2]; // kGated*: b[1] is Wu
+  Operand in;         // residual or null; dy
+  const void* bias;   // or null
+  void* c[2];
+  int64_t ldc[2];
+  int pad;            // kSlope, kGatedSlope: columns N .. pad - 1 of c get zeros
+  int accumulate;     // kDw
+};
+
+// Launches p.
+sm_status launch_product(const Product& p, hipStream_t s);
+
+// The sums over T rows of dz (ld entries apart) of n columns, in float32, to
+// out (added to it with accumulate).
+sm_status launch_column_sums(const void* dz, int64_t ld, int64_t T, int n, int dt, void* out,
+                             int accumulate, hipStream_t s);
+
+// rows x cols entries (row stride ld) set to 0.
+sm_status launch_zero(void* p, int64_t ld, int64_t rows, int cols, int dt, hipStream_t s);
+
+// 8-bit checkpoints (sm_act8_pack, sm_act8_unpack).
+sm_status launch_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int d, uint8_t* x8,
+                           uint8_t* scale, hipStream_t s);
+sm_status launch_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_t T, int d,
+                             void* x, int64_t ldx, hipStream_t s);
+
+}  // namespace sm

@@ -1357,7 +1357,7 @@ const char* sm_status_string(int s) {
 
 int sm_last_hip_error(void) { return g_last_hip.load(); }
 
-int sm_version(void) { return 5; }
+int sm_version(void) { return 6; }
 
 sm_status sm_ns_polar_ws(int dt, int batch, int m, int n, size_t* ws_bytes) {
   if (!ws_bytes) return SM_ERR_ARG;
@@ -2015,7 +2015,7 @@ const char* sm_kernel_kind_name(int kind) {
   static const char* names[SM_K_NUM_KINDS] = {
       "ema", "norm", "gemm_gram", "gemm_apply", "gemm_rr", "probe",
       "sign_pack", "vote_update", "lion", "polar_update", "misc", "spectral",
-      "adamw", "grad_norm", "state8"};
+      "adamw", "grad_norm", "state8", "act8", "layer"};
   if (kind < 0 || kind >= SM_K_NUM_KINDS) return "unknown";
   return names[kind];
 }

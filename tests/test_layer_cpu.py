@@ -1,0 +1,268 @@
+"""The feed-forward layers without a GPU: the oracle's definitions, the C ABI's
+structs, workspace sizes and refusals, and the front end's checks."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import matrix_aware_optimizer_momentum_amd as sm
+from matrix_aware_optimizer_momentum_amd import _binding as B
+from oracle import layer_oracle as L
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, ARG, SHAPE, DTYPE, WORKSPACE = 0, 1, 2, 3, 4
+
+
+# ---------------------------------------------------------------- the oracle
+
+def test_code_values_are_torchs_e4m3():
+    want = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(L.code_values(), want)
+
+
+def test_oracle_pack_matches_torchs_conversion():
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((7, 70)) * np.exp(3 * rng.standard_normal((7, 70)))
+    x = x.astype(np.float32).astype(np.float64)
+    codes, scales = L.act8_pack(x)
+    s = np.repeat(2.0 ** (scales.astype(float) - 127), 32, 1)[:, :70]
+    want = torch.from_numpy(x / s).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(codes, want)
+    # the scale is the smallest: half of it would not hold the block's largest
+    for b in range(3):
+        top = np.abs(x[:, 32 * b:32 * b + 32]).max(1)
+        assert np.all(top <= 448 * s[:, 32 * b]) and np.all(top > 224 * s[:, 32 * b])
+
+
+@pytest.mark.parametrize("name", L.ACTS)
+def test_oracle_activations_match_torchs(name):
+    z = np.linspace(-12, 12, 4001)
+    t = torch.from_numpy(z).requires_grad_()
+    f = {"none": lambda v: v, "relu": torch.relu, "silu": torch.nn.functional.silu,
+         "gelu": torch.nn.functional.gelu,
+         "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[name]
+    y = f(t)
+    y.sum().backward()
+    np.testing.assert_allclose(L.act(name, z), y.detach().numpy(), rtol=1e-12, atol=1e-14)
+    np.testing.assert_allclose(L.slope(name, z), t.grad.numpy(), rtol=1e-10, atol=1e-14)
+
+
+@pytest.mark.parametrize("name", L.ACTS)
+def test_oracle_gradients_match_autograd(name):
+    gen = torch.Generator().manual_seed(3)
+    t = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64, requires_grad=True)
+    x, wg, wu, bias, dy = t(5, 7), t(6, 7), t(6, 7), t(6), t(5, 6).detach()
+    f = {"none": lambda v: v, "relu": torch.relu, "silu": torch.nn.functional.silu,
+         "gelu": torch.nn.functional.gelu,
+         "gelu_tanh": lambda v: torch.nn.functional.gelu(v, approximate="tanh")}[name]
+    n = lambda v: v.detach().numpy()
+    got = torch.autograd.grad(f(x @ wg.T + bias), (x, wg, bias), dy)
+    for g, want in zip(L.linear_grad(n(dy), n(x), n(wg), n(bias), name), got):
+        np.testing.assert_allclose(g, n(want), rtol=1e-9, atol=1e-12)
+    got = torch.autograd.grad(f(x @ wg.T) * (x @ wu.T), (x, wg, wu), dy)
+    for g, want in zip(L.gated_grad(n(dy), n(x), n(wg), n(wu), name), got):
+        np.testing.assert_allclose(g, n(want), rtol=1e-9, atol=1e-12)
+
+
+# ---------------------------------------------------------------- the boundary
+
+def test_layer_struct_matches_c(tmp_path):
+    src = tmp_path / "layout.c"
+    fields = ["sizeof(sm_layer)"] + [f"offsetof(sm_layer, {f})" for f, _ in B.Layer._fields_]
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "sm.h"\nint main(void){'
+                   + "".join(f'printf("%zu ", {f});' for f in fields)
+                   + 'printf("%d %d %d %d %d %d\\n", SM_ACT_NONE, SM_ACT_RELU, SM_ACT_SILU,'
+                     ' SM_ACT_GELU, SM_ACT_GELU_TANH, SM_ACT8_BLOCK);return 0;}\n')
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-D__HIP_PLATFORM_AMD__", f"-I{ROOT}/include", "-I/opt/rocm/include",
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    want = [ctypes.sizeof(B.Layer)] + [getattr(B.Layer, f).offset for f, _ in B.Layer._fields_]
+    assert got == want + [sm.ACT_NONE, sm.ACT_RELU, sm.ACT_SILU, sm.ACT_GELU, sm.ACT_GELU_TANH,
+                          B.ACT8_BLOCK]
+
+
+def _layer(**kw):
+    """A good call of every kind: T 6, d 16, n 24, float32, no buffer near another."""
+    f = dict(T=6, d=16, n=24, dt=B.F32, act=sm.ACT_SILU)
+    for i, name in enumerate(("x", "w", "w2", "bias", "residual", "y", "dy", "dx", "dw", "dw2",
+                              "dbias")):
+        f[name] = 0x100000 * (i + 1)
+    f.update(ldx=16, ldw=16, ldw2=16, ldr=24, ldy=24, lddy=24, lddx=16, lddw=16, lddw2=16)
+    f.update(kw)
+    return B.Layer(**f)
+
+
+CALLS = ["linear", "linear_grad", "gated", "gated_grad"]
+
+
+def _refusal(call, **kw):
+    """The query's status, and the call's own (with a workspace that would do)."""
+    lib = B.lib()
+    l, need = _layer(**kw), ctypes.c_size_t(0)
+    q = getattr(lib, f"sm_{call}_ws")(ctypes.byref(l), ctypes.byref(need))
+    if q == OK:
+        return OK
+    assert getattr(lib, f"sm_{call}")(ctypes.byref(l), 0x10000000, 1 << 30, None) == q
+    assert lib.sm_last_hip_error() == 0
+    return q
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_good_arguments_pass_the_checks(call):
+    assert _refusal(call) == OK
+    assert _refusal(call, T=0, x=None, dy=None, y=None, dx=None) == OK
+    assert _refusal(call, dt=B.BF16, x=0x100002, w=0x200006) == OK
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), SHAPE), (dict(T=(1 << 30) + 1), SHAPE), (dict(d=0), SHAPE), (dict(n=0), SHAPE),
+    (dict(d=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21), SHAPE), (dict(n=(1 << 20) + 1), SHAPE),
+    (dict(dt=2), DTYPE), (dict(act=-1), ARG), (dict(act=5), ARG),
+    (dict(x=None), ARG), (dict(x=0x100002), ARG), (dict(ldx=15), ARG),
+    (dict(w=None), ARG), (dict(w=0x200001), ARG), (dict(ldw=15), ARG),
+    (dict(ldx=(1 << 40) + 1), ARG),
+])
+def test_refusals_of_every_call(call, kw, want):
+    assert _refusal(call, **kw) == want
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("linear", dict(y=None)), ("linear", dict(y=0x600002)), ("linear", dict(ldy=23)),
+    ("linear", dict(residual=0x500001)), ("linear", dict(ldr=23)), ("linear", dict(bias=0x400002)),
+    ("gated", dict(y=None)), ("gated", dict(w2=None)), ("gated", dict(ldw2=15)),
+    ("gated", dict(w2=0x300002)),
+    ("linear_grad", dict(dy=None)), ("linear_grad", dict(lddy=23)), ("linear_grad", dict(lddx=15)),
+    ("linear_grad", dict(lddw=15)), ("linear_grad", dict(dbias=0xB00002)),
+    ("linear_grad", dict(dx=None, dw=None, dbias=None)),
+    ("gated_grad", dict(dx=None, dw=None, dw2=None)), ("gated_grad", dict(lddw2=15)),
+    ("gated_grad", dict(w2=None)),
+    # both x and its checkpoint, a checkpoint without scales
+    ("linear_grad", dict(x8=0xF00000, x8_scale=0xF80000)),
+    ("gated_grad", dict(x=None, x8=0xF00000)),
+    # outputs over inputs or each other: by one entry, by the last row
+    ("linear", dict(y=0x100000)), ("linear", dict(y=0x100000 + 4 * 16 * 5 + 4 * 15)),
+    ("linear", dict(residual=0x600000 + 4)), ("linear", dict(y=0x500000, ldr=32)),
+    ("gated", dict(y=0x300000)), ("gated", dict(y=0x100000 - 4 * (24 * 5 + 24) + 4)),
+    ("linear_grad", dict(dx=0x700000)), ("linear_grad", dict(dw=0x200000)),
+    ("linear_grad", dict(dbias=0x400000)), ("linear_grad", dict(dbias=0x900000 + 4 * 16 * 24 - 4)),
+    ("gated_grad", dict(dw2=0x900000)), ("gated_grad", dict(dx=0x100000)),
+    ("gated_grad", dict(x=None, x8=0x900000, x8_scale=0xF80000)),
+    ("gated_grad", dict(x=None, x8=0xF80000, x8_scale=0x800000)),
+    # columns of one wider matrix that share one
+    ("linear", dict(ldx=64, ldy=64, y=0x100000 + 4 * 15)),
+    ("linear", dict(ldx=64, ldy=64, y=0x100000 + 4 * 41)),
+])
+def test_refusals_by_call(call, kw):
+    assert _refusal(call, **kw) == ARG
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("linear", dict(bias=None, residual=None)),
+    ("linear", dict(residual=0x600000)),                          # onto the residual itself
+    ("linear", dict(ldx=64, ldy=64, y=0x100000 + 4 * 16)),        # columns side by side
+    ("linear", dict(ldx=64, ldy=64, y=0x100000 + 4 * 40)),
+    ("linear", dict(y=0x100000 + 4 * 16 * 6)),                    # right behind x
+    ("linear", dict(w2=None, dy=None, dw=None)),                  # fields that it does not read
+    ("gated", dict(bias=0x1, residual=0x100000)),
+    ("gated_grad", dict(dx=None)), ("gated_grad", dict(dw=None)), ("gated_grad", dict(dw2=None)),
+    ("gated_grad", dict(dbias=0x3)),
+    ("linear_grad", dict(dw=None, dbias=None)), ("linear_grad", dict(dx=None, dw=None)),
+    ("linear_grad", dict(x=None, x8=0xF00001, x8_scale=0xF80003)),
+    ("linear_grad", dict(lddw=32, lddw2=7)),
+])
+def test_what_the_checks_let_pass(call, kw):
+    assert _refusal(call, **kw) == OK
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_workspace_too_small_or_misaligned(call):
+    lib = B.lib()
+    l, need = _layer(T=50, d=17, n=33, ldx=17, ldw=17, ldw2=17, ldr=33, ldy=33, lddy=33, lddx=17,
+                     lddw=17, lddw2=17), ctypes.c_size_t(0)
+    assert getattr(lib, f"sm_{call}_ws")(ctypes.byref(l), ctypes.byref(need)) == OK
+    fn = getattr(lib, f"sm_{call}")
+    assert getattr(lib, f"sm_{call}_ws")(ctypes.byref(l), None) == ARG
+    if need.value:
+        assert fn(ctypes.byref(l), 0x10000000, need.value - 1, None) == WORKSPACE
+        assert fn(ctypes.byref(l), 0x10000010, need.value, None) == ARG
+        assert fn(ctypes.byref(l), None, need.value, None) == ARG
+    assert fn(None, None, 0, None) == ARG
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), ARG), (dict(x8=None), ARG), (dict(scale=None), ARG), (dict(x=0x100002), ARG),
+    (dict(ldx=69), ARG), (dict(T=-1), SHAPE), (dict(T=(1 << 30) + 1), SHAPE), (dict(d=0), SHAPE),
+    (dict(d=(1 << 20) + 1, ldx=1 << 21), SHAPE), (dict(dt=3), DTYPE),
+    (dict(x8=0x100000), ARG), (dict(scale=0x100000 + 5 * 70 * 4 - 1), ARG), (dict(T=0, x=None), OK),
+])
+def test_act8_refusals(kw, want):
+    a = dict(x=0x100000, ldx=70, dt=B.F32, T=5, d=70, x8=0x200000, scale=0x300000)
+    a.update(kw)
+    lib = B.lib()
+    assert lib.sm_act8_pack(a["x"], a["ldx"], a["dt"], a["T"], a["d"], a["x8"], a["scale"],
+                            None) == want
+    assert lib.sm_act8_unpack(a["x8"], a["scale"], a["dt"], a["T"], a["d"], a["x"], a["ldx"],
+                              None) == want
+    assert lib.sm_last_hip_error() == 0
+
+
+def test_act8_codes_over_scales_are_refused():
+    assert B.lib().sm_act8_pack(0x100000, 70, B.F32, 5, 70, 0x200000, 0x200000 + 5 * 70 - 1,
+                                None) == ARG
+
+
+# ---------------------------------------------------------------- the front end
+
+def test_front_end_refuses_cpu_tensors_and_wrong_types():
+    x, w = torch.zeros(3, 8), torch.zeros(4, 8)
+    for call in (lambda: sm.linear(x, w), lambda: sm.gated(x, w, w),
+                 lambda: sm.linear_grad(torch.zeros(3, 4), x, w),
+                 lambda: sm.gated_grad(torch.zeros(3, 4), x, w, w), lambda: sm.act8_pack(x)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(TypeError):
+        sm.linear(x.half(), w.half())
+    with pytest.raises(TypeError):
+        sm.act8_pack(x.half())
+    with pytest.raises(TypeError):
+        sm.act8_unpack(sm.Act8(x, x), torch.float16)
+
+
+def test_row_strides():
+    from matrix_aware_optimizer_momentum_amd.api import _rows
+
+    class Fake:   # a GPU tensor's layout, without a GPU
+        is_cuda = True
+        device = "gpu"
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    def ld(t, width, rows=None):
+        return _rows(Fake(t), "t", width, t.dtype, "gpu", rows)[1]
+
+    base = torch.zeros(4, 6, 40)
+    assert ld(base, 40) == 40 and ld(base[..., 3:19], 16) == 40
+    assert ld(base[:, :, :40].view(24, 40), 40, 24) == 40
+    assert ld(base[2], 40) == 40 and ld(base[2, 3], 40) == 40 and ld(base[:1, :1], 40) == 40
+    assert ld(base[:, 2], 40) == 240 and ld(base[::2, :1], 40) == 480
+    assert ld(torch.zeros(5, 1).expand(5, 7)[:, :1], 1) == 1
+    assert ld(torch.zeros(1, 7).expand(5, 7), 7) == 0        # refused by the library (ld < d)
+    for bad in (base[:, :4], base.transpose(0, 1)):
+        with pytest.raises(ValueError, match="one stride"):
+            ld(bad, 40)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        ld(base[..., ::2], 20)
+    with pytest.raises(ValueError, match="columns"):
+        ld(base, 39)
+    with pytest.raises(ValueError, match="rows"):
+        ld(base, 40, 23)
