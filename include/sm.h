@@ -610,8 +610,8 @@ sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_
  *   (may be NULL if that is 0); the query takes the call's own arguments.
  * Errors: SM_ERR_ARG (null or misaligned pointers, a row length above its ld,
  *   both or neither of x and x8, a bad act, an overlap, no output wanted),
- *   SM_ERR_SHAPE (T < 0 or > 2^30, d or n < 1 or > 2^20), SM_ERR_DTYPE,
- *   SM_ERR_WORKSPACE, SM_ERR_HIP.
+ *   SM_ERR_SHAPE (T < 0 or > 2^30, d or n < 1 or > 2^20, T d or T n >
+ *   2^40), SM_ERR_DTYPE, SM_ERR_WORKSPACE, SM_ERR_HIP.
  * ---------------------------------------------------------------------- */
 typedef enum {
   SM_ACT_NONE = 0, SM_ACT_RELU = 1, SM_ACT_SILU = 2, SM_ACT_GELU = 3, SM_ACT_GELU_TANH = 4

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void k_act8_pack(const T* x, int64_t ldx,
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_act8_unpack(const uint8_t* x8, const uint8_t* scale,
                                                           int64_t items, int blocks, int d, T* x,
-                                                          int64_t ldx) {
+                                                          int64_t ldx, bool pad) {
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < items;
        i += (int64_t)gridDim.x * kThreads) {
     const int64_t blk = i >> 2;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads) void k_act8_unpack(const uint8_t* x8, con
       const uint32_t c = e < left ? in[e] : 0u;
       v[e] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * q;
     }
-    put8(x + row * ldx + col, left, v);
+    put8(x + row * ldx + col, pad && left > 0 ? 8 : left, v);
   }
 }
 
@@ -128,13 +128,13 @@ sm_status launch_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int d,
 }
 
 sm_status launch_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_t T, int d,
-                             void* x, int64_t ldx, hipStream_t s) {
+                             void* x, int64_t ldx, bool pad, hipStream_t s) {
   const int blocks = (d + SM_ACT8_BLOCK - 1) / SM_ACT8_BLOCK;
   const int64_t items = T * blocks * 4;
   prof_begin(SM_K_ACT8, (double)T * (d * (1.0 + dt_size(dt)) + blocks), s);
   SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_act8_unpack<E>, dim3(grid_for(items)), dim3(kThreads),
                                            0, s, x8, scale, items, blocks, d, static_cast<E*>(x),
-                                           ldx));
+                                           ldx, pad));
   prof_end(s);
   return check_launch();
 }

@@ -1,0 +1,603 @@
+// The feed-forward layers' matrix products on the matrix cores.
+//
+// Work split.  A launch walks the flat list of output tiles (of both results,
+// where a call makes two weight gradients at once) with one workgroup per CU,
+// or two of the small ones; workgroups of one XCD take consecutive tiles, in
+// bands of four tile rows (ns_tiles.hpp), so that they share operand panels
+// in that XCD's L2.  256 threads are 2 x 2 waves; a wave owns MI x MI blocks
+// of 32 x 32 sums: tiles of 256 x 256 (MI 4) or 128 x 128 (MI 2).
+//
+// A gated layer's tile holds both projections of the same columns: the rows
+// of B that a wave multiplies are half Wg's and half Wu's, so that the wave
+// has act's argument and the factor of an output in its own registers, and
+// x is read once for both.
+//
+// Pipeline.  Operands go HBM -> LDS with direct-to-LDS buffer loads into a
+// ring of five k stages of 64 bytes a row (32 bf16 or 16 float32).  Step k
+// multiplies stage k in two slices: during the first the second's fragments
+// are read; then each wave waits for its own loads of stage k + 1 and the
+// workgroup meets; during the second slice stage k + 1's first fragments are
+// read and the loads of stage k + 4 are issued into the buffer that stage k -
+// 1 has left.  The ring runs on across tiles and across the two parts of a
+// sum (da Wg + db Wu), so that a tile's first stages load during the last
+// steps and the epilogue of the one before.
+//
+// Edges.  Rows past an operand's last read the last one (their sums are not
+// stored).  Where k ends inside a stage, the lanes past it load from beyond
+// the buffer descriptor's range, which puts zeros into LDS: no garbage meets
+// the sums, and no NaN of memory behind a matrix.
+//
+// Epilogue.  The sums go through LDS (the wave's share of the stage buffer
+// just multiplied) in chunks of 16 rows, float32, and come back as four
+// columns of a row per lane, so that bias, residual and dy are read, and
+// results written, in whole 128-byte lines or more; finish4 is the same code
+// for every kernel.
+#pragma once
+
+#include "layer_math.hpp"
+
+#define SM_HD __host__ __device__
+#include "ns_tiles.hpp"
+
+namespace sm {
+namespace layer {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int NT = 256;
+constexpr int NBUF = 5;
+constexpr int ROW = 64;   // bytes of an operand row in a stage
+
+struct TileArgs {
+  Product p;
+  int tiles_m, tiles_n, per_prob, total, xcd_chunk;
+};
+
+// ---------------------------------------------------------------- four results
+
+// Four consecutive entries, at any alignment (global memory takes wide
+// accesses at the entries' own).
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  typedef f32x4 V __attribute__((aligned(4)));
+  return *reinterpret_cast<const V*>(p);
+}
+__device__ __forceinline__ f32x4 load4(const bf16_t* p) {
+  typedef u32x2 V __attribute__((aligned(2)));
+  const u32x2 a = *reinterpret_cast<const V*>(p);
+  return f32x4{__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u),
+               __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xFFFF0000u)};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) {
+  typedef f32x4 V __attribute__((aligned(4)));
+  *reinterpret_cast<V*>(p) = v;
+}
+__device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
+  typedef u32x2 V __attribute__((aligned(2)));
+  const f32x2 a = {v[0], v[1]}, b = {v[2], v[3]};
+  *reinterpret_cast<V*>(p) =
+      u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2)),
+            __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2))};
+}
+// Of which `left` exist.
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T* p, int left) {
+  if (left >= 4) return load4(p);
+  f32x4 v = {};
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if (e < left) v[e] = Elem<T>::load(p + e);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 v, int left) {
+  if (left >= 4) {
+    store4(p, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if (e < left) Elem<T>::store(p + e, v[e]);
+}
+
+template <typename T, int KIND>
+__device__ __forceinline__ f32x4 load_bias(const Product& p, int col) {
+  if constexpr (KIND == kLinear || KIND == kSlope)
+    if (p.bias && col < p.N) return load4(static_cast<const T*>(p.bias) + col, p.N - col);
+  return f32x4{};
+}
+// The entries that the results are combined with, ahead of their use.
+template <typename T, int KIND>
+__device__ __forceinline__ f32x4 load_in(const Product& p, int prob, int row, int col) {
+  f32x4 v = {};
+  if (row < p.M && col < p.N) {
+    if constexpr (KIND == kDw) {
+      if (p.accumulate)
+        v = load4(static_cast<const T*>(prob ? p.c[1] : p.c[0]) +
+                      row * (prob ? p.ldc[1] : p.ldc[0]) + col,
+                  p.N - col);
+    } else if constexpr (KIND != kGated && KIND != kDx) {
+      if (p.in.p) v = load4(static_cast<const T*>(p.in.p) + row * p.in.ld + col, p.N - col);
+    }
+  }
+  return v;
+}
+// Columns col .. col + 3 of a row's results, from the sums g (and u of a
+// gated layer).
+template <typename T, int KIND>
+__device__ __forceinline__ void finish4(const Product& p, int prob, int row, int col, f32x4 g,
+                                        f32x4 u, f32x4 bias, f32x4 in) {
+  constexpr bool FINE = sizeof(T) == 4;
+  if (row >= p.M) return;
+  f32x4 v, v2 = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (KIND == kLinear) {
+      v[e] = act_value<FINE>(p.act, g[e] + bias[e]) + in[e];
+    } else if constexpr (KIND == kSlope) {
+      v[e] = in[e] * act_both<FINE>(p.act, g[e] + bias[e]).slope;
+    } else if constexpr (KIND == kGated) {
+      v[e] = act_value<FINE>(p.act, g[e]) * u[e];
+    } else if constexpr (KIND == kGatedSlope) {
+      const ActBoth h = act_both<FINE>(p.act, g[e]);
+      v[e] = in[e] * u[e] * h.slope;
+      v2[e] = in[e] * h.value;
+    } else if constexpr (KIND == kDw) {
+      v[e] = g[e] + in[e];
+    } else {
+      v[e] = g[e];
+    }
+  }
+  int left = p.N - col;
+  if constexpr (KIND == kSlope || KIND == kGatedSlope) {
+    // dz has zeros up to a multiple of 8 columns
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e >= left) v[e] = 0.f;
+      if (e >= left) v2[e] = 0.f;
+    }
+    left = p.pad - col;
+  }
+  store4(static_cast<T*>(prob ? p.c[1] : p.c[0]) + row * (prob ? p.ldc[1] : p.ldc[0]) + col, v,
+         left);
+  if constexpr (KIND == kGatedSlope)
+    store4(static_cast<T*>(p.c[1]) + row * p.ldc[1] + col, v2, left);
+}
+
+// ---------------------------------------------------------------- small things
+
+// The thread id, opaque to the optimizer: what is derived from it where it is
+// used does not stay live across the k loop.
+__device__ __forceinline__ int fresh_tid() {
+  int t = (int)threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// s_waitcnt vmcnt(N), other counters untouched.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// Workgroup barrier without a memory fence: no wait for the loads in flight.
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// One direct-to-LDS load: each lane's 16 bytes at base + voff land at LDS
+// byte address m0 + 16 lane, zeros where voff is kNowhere.  In inline
+// assembly so that the compiler, which cannot tell which LDS bytes a pending
+// load writes, adds no wait for all of them before every LDS read.  It has no
+// register result.  Its wait states: 5 between a VALU write of the
+// descriptor's registers and the load, 1 between writing M0 and the load.
+constexpr uint32_t kNowhere = 0x80000000u;   // the range that the descriptor allows
+__device__ __forceinline__ void dma16(uint64_t base, uint32_t voff, uint32_t m0) {
+  const i32x4 r = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNowhere, 0x00020000};
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(m0)
+               : "memory", "m0");
+}
+
+// ---------------------------------------------------------------- stages in LDS
+//
+// KC: rows of 64 bytes; the 16-byte chunk c of row R sits at position c ^
+// ((R >> 2) & 3), so that 16 rows read at one chunk hit 16 different 4-bank
+// groups.  KR: k rows of 64 MI entries; of bf16, chunk c of k row r sits at
+// position c ^ (4 (r & 3)), so that the four k rows of a transposing read lie
+// in four different 64-byte bank ranges.
+template <typename T, int MI>
+struct Geo {
+  static constexpr int SIZE = sizeof(T);
+  static constexpr int EPC = 16 / SIZE;              // entries of a chunk
+  static constexpr int BK = ROW / SIZE;              // k of a stage
+  static constexpr int ROWS = 64 * MI;               // operand rows of a tile
+  static constexpr int HALF = ROWS * ROW;            // bytes of an operand's stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int CPR = ROWS * SIZE / 16;       // chunks of a k row (KR)
+  static __device__ __forceinline__ int swz(int krow) { return SIZE == 2 ? 4 * (krow & 3) : 0; }
+};
+
+// This lane's byte offsets, from the tile's first entry of a stage, of its MI
+// loads, and the first k of each within the stage.
+template <typename T, int MI, bool KR, bool DUAL>
+struct LoadOffs {
+  typedef Geo<T, MI> G;
+  uint32_t off[MI];
+  // KC: the lane's chunk starts at k; KR: load q reads k row k + q * STEP
+  int k;
+  static constexpr int STEP = KR ? (64 / G::CPR > 0 ? 64 / G::CPR : 1) : 0;
+  static_assert(G::CPR <= 64, "a load covers whole k rows");
+
+  // row0: the tile's first row (column, KR) of the operand; rows: how many it has.
+  __device__ __forceinline__ void set(int64_t ld, int row0, int rows) {
+    const int tid = fresh_tid(), lane = tid & 63, wave = uniform(tid >> 6);
+    if constexpr (!KR) {
+      k = ((lane & 3) ^ ((lane >> 4) & 3)) * G::EPC;
+#pragma unroll
+      for (int q = 0; q < MI; ++q) {
+        int r = 16 * (MI * wave + q) + (lane >> 2);
+        if constexpr (DUAL) r = (wave >> 1) * (16 * MI) + r % (16 * MI);
+        r = min(r, rows - 1 - row0);
+        off[q] = (uint32_t)r * (uint32_t)(ld * G::SIZE) + (uint32_t)(k * G::SIZE);
+      }
+    } else {
+      const int last = (rows + G::EPC - 1) / G::EPC * G::EPC - G::EPC - row0;
+#pragma unroll
+      for (int q = 0; q < MI; ++q) {
+        const int at = (MI * wave + q) * 64 + lane;
+        const int krow = at / G::CPR, chunk = (at % G::CPR) ^ G::swz(krow);
+        if (q == 0) k = krow;
+        off[q] = (uint32_t)krow * (uint32_t)(ld * G::SIZE) +
+                 (uint32_t)(min(chunk * G::EPC, last) * G::SIZE);
+      }
+    }
+  }
+  // left: the k that exist from the stage's first on.
+  __device__ __forceinline__ uint32_t at(int q, int left) const {
+    return k + q * STEP < left ? off[q] : kNowhere;
+  }
+};
+
+// Fragments: 16 bytes of a row for a lane, whose k are one slice's (half a
+// stage): 8 bf16, or 4 float32 of which the e-th goes into the e-th product
+// (lanes 0-31 and 32-63 hold different k; A and B the same ones).
+template <typename T, int MI>
+struct Frags {
+  u32x4 a[MI], b[MI];
+};
+
+template <typename T, int MI, bool KR>
+struct FragOffs {
+  typedef Geo<T, MI> G;
+  uint32_t o[KR ? (G::SIZE == 2 ? 2 * MI : 1) : 2];
+  __device__ __forceinline__ explicit FragOffs(int rbase) {
+    const int lane = fresh_tid() & 63;
+    if constexpr (!KR) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int R = rbase + (lane & 31), c = 2 * s + (lane >> 5);
+        o[s] = (uint32_t)(R * ROW + 16 * (c ^ ((R >> 2) & 3)));
+      }
+    } else if constexpr (G::SIZE == 2) {
+      const int g = lane >> 4, j = lane & 15;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int krow = 8 * (g >> 1) + 4 * r + (j >> 2);
+          const int col = rbase + 32 * i + 16 * (g & 1) + 4 * (j & 3);
+          o[2 * i + r] = (uint32_t)(krow * G::ROWS * 2 + 16 * ((col >> 3) ^ G::swz(krow)) +
+                                    2 * (col & 7));
+        }
+    } else {
+      o[0] = (uint32_t)((4 * (lane >> 5) * G::ROWS + rbase + (lane & 31)) * 4);
+    }
+  }
+  // Block i of slice s of the operand half at h.
+  __device__ __forceinline__ u32x4 read(const char* h, int i, int s) const {
+    if constexpr (!KR) {
+      return *reinterpret_cast<const u32x4*>(h + o[s] + i * 32 * ROW);
+    } else if constexpr (G::SIZE == 2) {
+      typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+      const char* p0 = h + o[2 * i] + s * 16 * G::ROWS * 2;
+      const char* p1 = h + o[2 * i + 1] + s * 16 * G::ROWS * 2;
+      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_i16x4*)(__attribute__((address_space(3))) void*)(p0));
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_i16x4*)(__attribute__((address_space(3))) void*)(p1));
+      const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+      return u32x4{l2.x, l2.y, h2.x, h2.y};
+    } else {
+      const char* p = h + o[0] + (s * 8 * G::ROWS + 32 * i) * 4;
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = *reinterpret_cast<const uint32_t*>(p + e * G::ROWS * 4);
+      return v;
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void mma(f32x16& acc, u32x4 a, u32x4 b) {
+  if constexpr (sizeof(T) == 2) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]), __uint_as_float(b[e]),
+                                                 acc, 0, 0, 0);
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct Tile {
+  int prob, tm, tn;
+};
+__device__ __forceinline__ Tile decode_tile(const TileArgs& A, int t) {
+  Tile r;
+  r.prob = t / A.per_prob;
+  ns_tile_coords(t - r.prob * A.per_prob, A.tiles_m, A.tiles_n, 0, &r.tm, &r.tn);
+  return r;
+}
+
+// Where the loads are: a stage of a tile (or of a part of its sums).
+template <typename T, int KIND, int MI>
+struct LoadPos {
+  typedef Geo<T, MI> G;
+  static constexpr bool AKR = kind_a_kr(KIND), BKR = kind_b_kr(KIND), DUAL = kind_dual(KIND);
+  LoadOffs<T, MI, AKR, false> a;
+  LoadOffs<T, MI, BKR, DUAL> b;
+  uint64_t abase, bbase;    // of the stage
+  uint64_t astep, bstep;    // bytes from a stage to the next
+  int left;                 // k that exist from the stage's first on
+  int part, tile;
+
+  __device__ __forceinline__ void set(const TileArgs& A, int t, int q) {
+    const Product& p = A.p;
+    t = uniform(t);
+    q = uniform(q);
+    const Tile tl = decode_tile(A, t);
+    const Operand oa = (KIND == kDw ? tl.prob : KIND == kDx ? q : 0) ? p.a[1] : p.a[0];
+    Operand ob = (KIND == kDx && q) ? p.b[1] : p.b[0];
+    if constexpr (DUAL)   // odd waves load Wu's rows
+      if (uniform(fresh_tid() >> 6) & 1) ob = p.b[1];
+    constexpr int NB = DUAL ? G::ROWS / 2 : G::ROWS;
+    const int am = tl.tm * G::ROWS, bn = tl.tn * NB;
+    a.set(oa.ld, am, p.M);
+    b.set(ob.ld, bn, p.N);
+    abase = reinterpret_cast<uint64_t>(oa.p) + (uint64_t)((AKR ? am : am * oa.ld) * G::SIZE);
+    bbase = reinterpret_cast<uint64_t>(ob.p) + (uint64_t)((BKR ? bn : bn * ob.ld) * G::SIZE);
+    abase = uniform64(abase);
+    bbase = uniform64(bbase);
+    astep = uniform64((uint64_t)(AKR ? G::BK * oa.ld * G::SIZE : ROW));
+    bstep = uniform64((uint64_t)(BKR ? G::BK * ob.ld * G::SIZE : ROW));
+    left = p.K;
+    part = q;
+    tile = t;
+  }
+  // The next stage: of this part, of the next part, of the workgroup's next
+  // tile; past the last one it stays (that stage is then loaded again, into
+  // buffers that nobody multiplies).
+  __device__ __forceinline__ void advance(const TileArgs& A, int stride) {
+    if (left > G::BK) {
+      left -= G::BK;
+      abase += astep;
+      bbase += bstep;
+    } else {
+      const bool more = KIND == kDx && part + 1 < A.p.parts;
+      const int t = more ? tile : tile + stride;
+      if (t < A.total) set(A, t, more ? part + 1 : 0);
+    }
+  }
+  // Load q of this wave (A's, then B's) into the stage buffer at LDS address buf.
+  __device__ __forceinline__ void load(uint32_t buf, int q) const {
+    if (q < MI) dma16(abase, a.at(q, left), buf + 1024u * q);
+    else dma16(bbase, b.at(q - MI, left), buf + G::HALF + 1024u * (q - MI));
+  }
+};
+
+// One step: see the pipeline above.  cur, nxt: this stage and the next one;
+// ldb: LDS address of this wave's slots in the buffer to load into.
+// sched_barrier keeps the order of the products and the memory instructions
+// between them.
+template <typename T, int KIND, int MI>
+__device__ __forceinline__ void step(f32x16 (&acc)[MI][MI], Frags<T, MI>& f0, Frags<T, MI>& f1,
+                                     const char* cur, const char* nxt, uint32_t ldb,
+                                     const LoadPos<T, KIND, MI>& L,
+                                     const FragOffs<T, MI, kind_a_kr(KIND)>& fa,
+                                     const FragOffs<T, MI, kind_b_kr(KIND)>& fb) {
+  typedef Geo<T, MI> G;
+  constexpr int Q = MI * MI;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    mma<T>(acc[q / MI][q % MI], f0.a[q / MI], f0.b[q % MI]);
+    if (q < MI) f1.a[q] = fa.read(cur, q, 1);
+    else if (q < 2 * MI) f1.b[q - MI] = fb.read(cur + G::HALF, q - MI, 1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // stage k + 1 must have landed; stages k + 2 and k + 3 may be in flight
+  wait_vm<4 * MI>();
+  meet();
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    mma<T>(acc[q / MI][q % MI], f1.a[q / MI], f1.b[q % MI]);
+    if (q < MI) f0.a[q] = fa.read(nxt, q, 0);
+    else if (q < 2 * MI) f0.b[q - MI] = fb.read(nxt + G::HALF, q - MI, 0);
+    if (Q == 2 * MI) L.load(ldb, q);
+    else if (q >= 2 * MI && q < 4 * MI) L.load(ldb, q - 2 * MI);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Half h (16 rows) of a row of blocks into a chunk of 32 MI columns; those of
+// rows with bit 2 set are turned by 32, which puts the two halves of a wave
+// into different banks.
+template <int MI>
+__device__ __forceinline__ void put_chunk(const f32x16 (&acc)[MI], int h, float* stage) {
+  constexpr int W = 32 * MI;
+  const int lane = fresh_tid() & 63;
+#pragma unroll
+  for (int j = 0; j < MI; ++j)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+      const int c = 32 * j + (lane & 31) + 32 * (lane >> 5);   // bit 2 of row: lane >> 5
+      stage[row * W + (c & (W - 1))] = acc[j][8 * h + r];
+    }
+}
+
+// The results of this wave's blocks, 16 rows at a time through its share of
+// the stage buffer.
+template <typename T, int KIND, int MI>
+__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][MI], const TileArgs& A, Tile t,
+                                         float* stage) {
+  constexpr bool DUAL = kind_dual(KIND);
+  constexpr int W = 32 * MI;               // columns of a chunk
+  constexpr int OUT = DUAL ? W / 2 : W;    // and of its results
+  constexpr int LPR = OUT / 4;             // lanes of a result row
+  constexpr int RPI = 64 / LPR;            // rows of a read
+  const int tid = fresh_tid(), lane = tid & 63, wave = uniform(tid >> 6);
+  const int row0 = t.tm * (64 * MI) + (wave >> 1) * W;
+  const int col = t.tn * (2 * OUT) + (wave & 1) * OUT + 4 * (lane % LPR);
+  const f32x4 bias = load_bias<T, KIND>(A.p, col);
+  const bool cols_in = col < (KIND == kSlope || KIND == kGatedSlope ? A.p.pad : A.p.N);
+  // one copy of what follows the registers: a chunk's sums are picked by a
+  // uniform switch, so that the registers' numbers stay constants
+#pragma unroll 1
+  for (int chunk = 0; chunk < 2 * MI; ++chunk) {
+    const int r0 = row0 + 16 * chunk + lane / LPR;
+    f32x4 in[16 / RPI];
+#pragma unroll
+    for (int k = 0; k < 16 / RPI; ++k)
+      in[k] = load_in<T, KIND>(A.p, t.prob, r0 + RPI * k, col);
+    switch (chunk) {
+#define SM_CHUNK(C) \
+  case C: \
+    if constexpr ((C) < 2 * MI) put_chunk<MI>(acc[(C) / 2 % MI], (C) % 2, stage); \
+    break;
+      SM_CHUNK(0)
+      SM_CHUNK(1)
+      SM_CHUNK(2)
+      SM_CHUNK(3)
+      SM_CHUNK(4)
+      SM_CHUNK(5)
+      SM_CHUNK(6)
+      SM_CHUNK(7)
+#undef SM_CHUNK
+    }
+#pragma unroll
+    for (int k = 0; k < 16 / RPI; ++k) {
+      const int row = lane / LPR + RPI * k;
+      const int turn = 32 * ((row >> 2) & 1);
+      const int cg = 4 * (lane % LPR);
+      const f32x4 g = *reinterpret_cast<const f32x4*>(stage + row * W + ((cg + turn) & (W - 1)));
+      f32x4 u = {};
+      if constexpr (DUAL)
+        u = *reinterpret_cast<const f32x4*>(stage + row * W + ((cg + OUT + turn) & (W - 1)));
+      if (cols_in) finish4<T, KIND>(A.p, t.prob, r0 + RPI * k, col, g, u, bias, in[k]);
+    }
+  }
+}
+
+template <typename T, int KIND, int MI>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(MI == 4 ? 1 : 2, MI == 4 ? 1 : 2)))
+void k_tile(TileArgs A) {
+  typedef Geo<T, MI> G;
+  __shared__ __attribute__((aligned(16))) char smem[NBUF * G::STAGE];
+  int t = blockIdx.x;
+  if (A.xcd_chunk > 0) t = (t & 7) * A.xcd_chunk + (t >> 3);
+  const int stride = gridDim.x;
+  if (t >= A.total) return;
+  const int wave = uniform(fresh_tid() >> 6);
+  const uint32_t la0 =
+      (uint32_t)uniform((int)(uint32_t)(size_t)(__attribute__((address_space(3))) void*)smem) +
+      1024u * MI * wave;
+  LoadPos<T, KIND, MI> L;
+  L.set(A, t, 0);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+#pragma unroll
+    for (int q = 0; q < 2 * MI; ++q) L.load(la0 + s * G::STAGE, q);
+    L.advance(A, stride);
+  }
+  wait_vm<6 * MI>();
+  meet();
+  const int wm = wave >> 1, wn = wave & 1;
+  const FragOffs<T, MI, kind_a_kr(KIND)> fa(wm * 32 * MI);
+  const FragOffs<T, MI, kind_b_kr(KIND)> fb(wn * 32 * MI);
+  Frags<T, MI> f0, f1;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    f0.a[i] = fa.read(smem, i, 0);
+    f0.b[i] = fb.read(smem + G::HALF, i, 0);
+  }
+  int cb = 0;
+  const int steps = (A.p.K + G::BK - 1) / G::BK * (KIND == kDx ? A.p.parts : 1);
+  for (; t < A.total; t += stride) {
+    f32x16 acc[MI][MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < MI; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    for (int k = 0; k < steps; ++k) {
+      const int nb = cb == NBUF - 1 ? 0 : cb + 1;
+      const int lb = cb == 0 ? NBUF - 1 : cb - 1;
+      step<T, KIND, MI>(acc, f0, f1, smem + cb * G::STAGE, smem + nb * G::STAGE,
+                        la0 + lb * G::STAGE, L, fa, fb);
+      L.advance(A, stride);
+      cb = nb;
+    }
+    // every wave is past its reads of the last stage once all have met
+    meet();
+    epilogue<T, KIND, MI>(acc, A, decode_tile(A, uniform(t)),
+                          reinterpret_cast<float*>(smem + (cb == 0 ? NBUF - 1 : cb - 1) * G::STAGE +
+                                                   wave * (G::STAGE / 4)));
+  }
+  wait_vm<0>();   // loads past the last stage target this workgroup's LDS
+}
+
+template <typename T, int MI>
+void launch_tile(const TileArgs& a, int grid, hipStream_t s) {
+  switch (a.p.kind) {
+#define SM_KIND(K) \
+  case K: hipLaunchKernelGGL((k_tile<T, K, MI>), dim3(grid), dim3(NT), 0, s, a); break;
+    SM_KIND(kLinear)
+    SM_KIND(kSlope)
+    SM_KIND(kGated)
+    SM_KIND(kGatedSlope)
+    SM_KIND(kDx)
+    SM_KIND(kDw)
+#undef SM_KIND
+  }
+}
+
+// One translation unit for each type and tile.
+void launch_tile_bf16_4(const TileArgs& a, int grid, hipStream_t s);
+void launch_tile_bf16_2(const TileArgs& a, int grid, hipStream_t s);
+void launch_tile_f32_4(const TileArgs& a, int grid, hipStream_t s);
+void launch_tile_f32_2(const TileArgs& a, int grid, hipStream_t s);
+
+}  // namespace layer
+}  // namespace sm

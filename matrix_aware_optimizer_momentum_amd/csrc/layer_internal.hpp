@@ -37,8 +37,19 @@ struct Product {
   int accumulate;     // kDw
 };
 
-// Launches p.
+// Launches p.  Every operand's rows (as they are stored) are 16-byte aligned,
+// less than 2^31 / 256 bytes apart, and a multiple of 16 bytes long, or have
+// readable memory up to one, zeros if they run along k.
 sm_status launch_product(const Product& p, hipStream_t s);
+inline bool laid_out(const void* p, int64_t ld, int64_t len, int dt) {
+  const int64_t size = (int64_t)dt_size(dt);
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && len * size % 16 == 0 &&
+         ld * size < (int64_t(1) << 31) / 256;
+}
+// A copy of a matrix that is so: rows x cols entries to rows x ld ones (ld a
+// multiple of 8), zeros behind them.
+sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int dt, void* out,
+                         int64_t ld, hipStream_t s);
 
 // The sums over T rows of dz (ld entries apart) of n columns, in float32, to
 // out (added to it with accumulate).
@@ -51,7 +62,8 @@ sm_status launch_zero(void* p, int64_t ld, int64_t rows, int cols, int dt, hipSt
 // 8-bit checkpoints (sm_act8_pack, sm_act8_unpack).
 sm_status launch_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int d, uint8_t* x8,
                            uint8_t* scale, hipStream_t s);
+// pad: entries d .. round_up(d, 8) - 1 of the rows of x get zeros.
 sm_status launch_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_t T, int d,
-                             void* x, int64_t ldx, hipStream_t s);
+                             void* x, int64_t ldx, bool pad, hipStream_t s);
 
 }  // namespace sm

@@ -8,6 +8,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int kMaxWidth = 1 << 20;
+constexpr int64_t kMaxCount = int64_t(1) << 40;   // entries of x or y: their tiles stay countable
 constexpr int64_t kMaxLd = int64_t(1) << 40;
 
 bool multiple_of(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -89,6 +90,7 @@ sm_status check_layer(const sm_layer* lp, Call c) {
   const sm_layer& l = *lp;
   SM_TRY(check_sizes(l.T, l.d, l.dt));
   if (l.n < 1 || l.n > kMaxWidth) return SM_ERR_SHAPE;
+  if (l.T * std::max(l.d, l.n) > kMaxCount) return SM_ERR_SHAPE;
   if (l.act < SM_ACT_NONE || l.act > SM_ACT_GELU_TANH) return SM_ERR_ARG;
   const size_t z = dt_size(l.dt);
   const int64_t size = (int64_t)z;
@@ -148,10 +150,12 @@ sm_status check_layer(const sm_layer* lp, Call c) {
   return areas.conflict() ? SM_ERR_ARG : SM_OK;
 }
 
-// What a call keeps in its workspace.
+// What a call keeps in its workspace: offsets of the operands that it lays out
+// anew, of x from a checkpoint, and of dz.
 struct LayerWs {
-  size_t x, dz, dz2, bytes;   // offsets; absent ones are the end
-  int64_t ldx, lddz;
+  bool lay_x, lay_w, lay_w2, lay_dy;
+  size_t x, w, w2, dy, dz, dz2, bytes;
+  int64_t ldd, ldn;   // rows of d and of n entries
 };
 LayerWs layer_ws(const sm_layer& l, Call c) {
   LayerWs w{};
@@ -160,12 +164,21 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
     if (wanted) w.bytes += (size_t)round_up(rows * ld * (int64_t)dt_size(l.dt), 256);
     return at;
   };
-  w.ldx = round_up(l.d, 8);
-  w.lddz = round_up(l.n, 8);
-  const bool grad = is_grad(c);
-  w.x = take(grad && l.x8 && reads_x(l, c), l.T, w.ldx);
-  w.dz = take(grad && makes_dz(l, c), l.T, w.lddz);
-  w.dz2 = take(grad && is_gated(c), l.T, w.lddz);
+  w.ldd = round_up(l.d, 8);
+  w.ldn = round_up(l.n, 8);
+  if (l.T == 0) return w;
+  const bool grad = is_grad(c), x8 = grad && l.x8;
+  const bool again = !grad || makes_dz(l, c);   // x W^T is computed
+  w.lay_x = !x8 && reads_x(l, c) && !laid_out(l.x, l.ldx, l.d, l.dt);
+  w.lay_w = (again || l.dx) && !laid_out(l.w, l.ldw, l.d, l.dt);
+  w.lay_w2 = is_gated(c) && !laid_out(l.w2, l.ldw2, l.d, l.dt);
+  w.lay_dy = grad && !again && (l.dx || l.dw) && !laid_out(l.dy, l.lddy, l.n, l.dt);
+  w.x = take(w.lay_x || (x8 && reads_x(l, c)), l.T, w.ldd);
+  w.w = take(w.lay_w, l.n, w.ldd);
+  w.w2 = take(w.lay_w2, l.n, w.ldd);
+  w.dy = take(w.lay_dy, l.T, w.ldn);
+  w.dz = take(grad && again, l.T, w.ldn);
+  w.dz2 = take(grad && is_gated(c), l.T, w.ldn);
   return w;
 }
 
@@ -195,28 +208,85 @@ Product product_of(const sm_layer& l, int kind) {
   return p;
 }
 
+// The operands of a call, laid out if they have to be.
+struct Operands {
+  Operand x, w, w2, dz[2];
+};
+sm_status lay_out(const sm_layer& l, const LayerWs& w, char* ws, Operands* o, bool checkpoint,
+                  hipStream_t s) {
+  o->x = {l.x, l.ldx};
+  o->w = {l.w, l.ldw};
+  o->w2 = {l.w2, l.ldw2};
+  o->dz[0] = {l.dy, l.lddy};
+  o->dz[1] = {nullptr, 0};
+  if (checkpoint) {
+    o->x = {ws + w.x, w.ldd};
+    SM_TRY(launch_act8_unpack(l.x8, l.x8_scale, l.dt, l.T, l.d, ws + w.x, w.ldd, true, s));
+  }
+  if (w.lay_x) {
+    o->x = {ws + w.x, w.ldd};
+    SM_TRY(launch_lay_out(l.x, l.ldx, l.T, l.d, l.dt, ws + w.x, w.ldd, s));
+  }
+  if (w.lay_w) {
+    o->w = {ws + w.w, w.ldd};
+    SM_TRY(launch_lay_out(l.w, l.ldw, l.n, l.d, l.dt, ws + w.w, w.ldd, s));
+  }
+  if (w.lay_w2) {
+    o->w2 = {ws + w.w2, w.ldd};
+    SM_TRY(launch_lay_out(l.w2, l.ldw2, l.n, l.d, l.dt, ws + w.w2, w.ldd, s));
+  }
+  if (w.lay_dy) {
+    o->dz[0] = {ws + w.dy, w.ldn};
+    SM_TRY(launch_lay_out(l.dy, l.lddy, l.T, l.n, l.dt, ws + w.dy, w.ldn, s));
+  }
+  return SM_OK;
+}
+
+sm_status check_ws(const LayerWs& w, const void* ws, size_t ws_bytes) {
+  if (w.bytes && (!ws || !multiple_of(ws, 256))) return SM_ERR_ARG;
+  return ws_bytes < w.bytes ? SM_ERR_WORKSPACE : SM_OK;
+}
+
+Product product_of(const sm_layer& l, int kind, const Operands& o) {
+  Product p;
+  std::memset(&p, 0, sizeof(p));
+  p.kind = kind;
+  p.dt = l.dt;
+  p.act = l.act;
+  p.M = (int)l.T;
+  p.N = l.n;
+  p.K = l.d;
+  p.parts = 1;
+  p.a[0] = o.x;
+  p.b[0] = o.w;
+  p.b[1] = o.w2;
+  if (kind == kLinear || kind == kSlope) p.bias = l.bias;
+  return p;
+}
+
 sm_status run_forward(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hipStream_t s) {
   SM_TRY(check_layer(lp, c));
   const sm_layer& l = *lp;
   const LayerWs w = layer_ws(l, c);
-  if (w.bytes && (!ws || !multiple_of(ws, 256))) return SM_ERR_ARG;
-  if (ws_bytes < w.bytes) return SM_ERR_WORKSPACE;
+  SM_TRY(check_ws(w, ws, ws_bytes));
   if (l.T == 0) return SM_OK;
-  Product p = product_of(l, c == kCallGated ? kGated : kLinear);
-  if (c == kCallGated) p.bias = nullptr;
-  else p.in = {l.residual, l.ldr};
+  Operands o;
+  SM_TRY(lay_out(l, w, static_cast<char*>(ws), &o, false, s));
+  Product p = product_of(l, c == kCallGated ? kGated : kLinear, o);
+  if (c == kCallLinear) p.in = {l.residual, l.ldr};
+  p.c[0] = l.y;
+  p.ldc[0] = l.ldy;
   return launch_product(p, s);
 }
 
-sm_status run_grad(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hipStream_t s) {
+sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipStream_t s) {
   SM_TRY(check_layer(lp, c));
   const sm_layer& l = *lp;
   const bool gated = is_gated(c);
   void* dw2 = gated ? l.dw2 : nullptr;
   void* dbias = gated ? nullptr : l.dbias;
   const LayerWs w = layer_ws(l, c);
-  if (w.bytes && (!ws || !multiple_of(ws, 256))) return SM_ERR_ARG;
-  if (ws_bytes < w.bytes) return SM_ERR_WORKSPACE;
+  SM_TRY(check_ws(w, wsp, ws_bytes));
   if (l.T == 0) {
     if (l.accumulate) return SM_OK;
     if (l.dw) SM_TRY(launch_zero(l.dw, l.lddw, l.n, l.d, l.dt, s));
@@ -224,54 +294,46 @@ sm_status run_grad(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hipStr
     if (dbias) SM_TRY(launch_zero(dbias, l.n, 1, l.n, l.dt, s));
     return SM_OK;
   }
-  char* base = static_cast<char*>(ws);
-  Operand x = {l.x, l.ldx};
-  if (l.x8 && reads_x(l, c)) {
-    x = {base + w.x, w.ldx};
-    SM_TRY(launch_act8_unpack(l.x8, l.x8_scale, l.dt, l.T, l.d, base + w.x, w.ldx, s));
-  }
-  Operand dz[2] = {{l.dy, l.lddy}, {nullptr, 0}};
+  char* ws = static_cast<char*>(wsp);
+  Operands o;
+  SM_TRY(lay_out(l, w, ws, &o, l.x8 && reads_x(l, c), s));
   if (makes_dz(l, c)) {
-    Product p = product_of(l, gated ? kGatedSlope : kSlope);
-    if (gated) p.bias = nullptr;
-    p.a[0] = x;
+    Product p = product_of(l, gated ? kGatedSlope : kSlope, o);
     p.in = {l.dy, l.lddy};
-    p.c[0] = base + w.dz;
-    p.c[1] = base + w.dz2;
-    p.ldc[0] = p.ldc[1] = w.lddz;
-    p.pad = (int)w.lddz;
-    dz[0] = {base + w.dz, w.lddz};
-    dz[1] = {base + w.dz2, w.lddz};
+    p.c[0] = ws + w.dz;
+    p.c[1] = ws + w.dz2;
+    p.ldc[0] = p.ldc[1] = w.ldn;
+    p.pad = (int)w.ldn;
+    o.dz[0] = {ws + w.dz, w.ldn};
+    o.dz[1] = {ws + w.dz2, w.ldn};
     SM_TRY(launch_product(p, s));
   }
   if (l.dx) {
-    Product p = product_of(l, kDx);
+    Product p = product_of(l, kDx, o);
     p.N = l.d;
     p.K = l.n;
     p.parts = gated ? 2 : 1;
-    p.a[0] = dz[0];
-    p.a[1] = dz[1];
-    p.bias = nullptr;
+    p.a[0] = o.dz[0];
+    p.a[1] = o.dz[1];
     p.c[0] = l.dx;
     p.ldc[0] = l.lddx;
     SM_TRY(launch_product(p, s));
   }
   if (l.dw || dw2) {
-    Product p = product_of(l, kDw);
+    Product p = product_of(l, kDw, o);
     p.M = l.n;
     p.N = l.d;
     p.K = (int)l.T;
-    p.b[0] = x;
-    p.bias = nullptr;
+    p.b[0] = o.x;
     p.accumulate = l.accumulate;
     int q = 0;
-    if (l.dw) p.a[q] = dz[0], p.c[q] = l.dw, p.ldc[q++] = l.lddw;
-    if (dw2) p.a[q] = dz[1], p.c[q] = dw2, p.ldc[q++] = l.lddw2;
+    if (l.dw) p.a[q] = o.dz[0], p.c[q] = l.dw, p.ldc[q++] = l.lddw;
+    if (dw2) p.a[q] = o.dz[1], p.c[q] = dw2, p.ldc[q++] = l.lddw2;
     p.parts = q;
     SM_TRY(launch_product(p, s));
   }
   if (dbias)
-    SM_TRY(launch_column_sums(dz[0].p, dz[0].ld, l.T, l.n, l.dt, dbias, l.accumulate, s));
+    SM_TRY(launch_column_sums(o.dz[0].p, o.dz[0].ld, l.T, l.n, l.dt, dbias, l.accumulate, s));
   return SM_OK;
 }
 
@@ -291,7 +353,7 @@ sm_status sm_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int32_t d,
 sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_t T, int32_t d,
                          void* x, int64_t ldx, hipStream_t s) {
   SM_TRY(check_act8(x, ldx, dt, T, d, x8, scale, false));
-  return T == 0 ? SM_OK : launch_act8_unpack(x8, scale, dt, T, d, x, ldx, s);
+  return T == 0 ? SM_OK : launch_act8_unpack(x8, scale, dt, T, d, x, ldx, false, s);
 }
 
 sm_status sm_linear_ws(const sm_layer* l, size_t* ws_bytes) {

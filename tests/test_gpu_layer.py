@@ -128,6 +128,37 @@ def test_whole_numbers_gated(gpu_lib, dt, shape, layout):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,n", [(2900, 2904, 2888), (2883, 2901, 2897), (4200, 72, 4104), (40, 4104, 4200)])
+def test_whole_numbers_large(gpu_lib, dt, T, d, n):
+    """Enough rows and columns for the large tiles in every product; float64 on the GPU as the
+    reference (whole numbers: exact there too)."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    f = lambda top, *s: torch.randint(-top, top + 1, s, generator=gen, device="cuda").to(DT[dt])
+    x, wg, wu, bias, res, dy = f(1, T, d), f(2, n, d), f(1, n, d), f(9, n), f(20, T, n), f(1, T, n)
+    X, G, U, BI, R, DY = (v.double() for v in (x, wg, wu, bias, res, dy))
+    a, b = X @ G.T, X @ U.T
+
+    def same(got, want):
+        assert torch.equal(got, want.to(DT[dt]))
+
+    relu = dict(act=sm.ACT_RELU)
+    same(sm.linear(x, wg, bias=bias, residual=res, **relu), (a + BI).relu() + R)
+    same(sm.gated(x, wg, wu, **relu), a.relu() * b)
+    dz = DY * (a + BI > 0)
+    dx, dw, db = sm.linear_grad(dy, x, wg, bias=bias, **relu)
+    same(dx, dz @ G)
+    same(dw, dz.T @ X)
+    same(db, dz.sum(0))
+    da, dbb = (v.to(DT[dt]).double() for v in (DY * b * (a > 0), DY * a.relu()))
+    old = f(50, 2, n, d)
+    new = old.clone()
+    dx, _, _ = sm.gated_grad(dy, x, wg, wu, dwg=new[0], dwu=new[1], accumulate=True, **relu)
+    same(dx, da @ G + dbb @ U)
+    same(new[0], old[0].double() + da.T @ X)
+    same(new[1], old[1].double() + dbb.T @ X)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,d,n", [(5, 40, 24), (70, 130, 90), (200, 64, 300)])
 def test_accumulate_and_left_out_results(gpu_lib, dt, T, d, n):
     rng = np.random.default_rng(T)
