@@ -4,13 +4,15 @@
 // where a call makes two weight gradients at once) with one workgroup per CU,
 // or two of the small ones; workgroups of one XCD take consecutive tiles, in
 // bands of four tile rows (ns_tiles.hpp), so that they share operand panels
-// in that XCD's L2.  256 threads are 2 x 2 waves; a wave owns MI x MI blocks
-// of 32 x 32 sums: tiles of 256 x 256 (MI 4) or 128 x 128 (MI 2).
+// in that XCD's L2.  A wave owns MI x 2 blocks of 32 x 32 sums; tiles of 256 x
+// 256 have 2 x 4 waves with MI 4, tiles of 128 x 128 2 x 2 with MI 2.  Either
+// way two waves share a SIMD: while one waits, or issues a load (which holds
+// it up for as long as two products), the other multiplies.
 //
-// A gated layer's tile holds both projections of the same columns: the rows
-// of B that a wave multiplies are half Wg's and half Wu's, so that the wave
-// has act's argument and the factor of an output in its own registers, and
-// x is read once for both.
+// A gated layer's tile holds both projections of the same columns: of the 64
+// rows of B that a wave multiplies 32 are Wg's and 32 the same ones of Wu, so
+// that the wave has act's argument and the factor of an output in its own
+// registers, and x is read once for both.
 //
 // Pipeline.  Operands go HBM -> LDS with direct-to-LDS buffer loads into a
 // ring of five k stages of 64 bytes a row (32 bf16 or 16 float32).  Step k
@@ -52,7 +54,6 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int NT = 256;
 constexpr int NBUF = 5;
 constexpr int ROW = 64;   // bytes of an operand row in a stage
 
@@ -231,19 +232,24 @@ struct Geo {
   static constexpr int HALF = ROWS * ROW;            // bytes of an operand's stage
   static constexpr int STAGE = 2 * HALF;
   static constexpr int CPR = ROWS * SIZE / 16;       // chunks of a k row (KR)
+  static constexpr int WN = MI;                      // waves: 2 rows of WN
+  static constexpr int THREADS = 128 * WN;
   static __device__ __forceinline__ int swz(int krow) { return SIZE == 2 ? 4 * (krow & 3) : 0; }
 };
 
-// This lane's byte offsets, from the tile's first entry of a stage, of its MI
+// A wave loads 32 rows' worth of each operand's stage, by two loads of 1 KB.
+constexpr int LQ = 2;
+
+// This lane's byte offsets, from the tile's first entry of a stage, of its
 // loads, and the first k of each within the stage.
 template <typename T, int MI, bool KR, bool DUAL>
 struct LoadOffs {
   typedef Geo<T, MI> G;
-  uint32_t off[MI];
+  uint32_t off[LQ];
   // KC: the lane's chunk starts at k; KR: load q reads k row k + q * STEP
   int k;
-  static constexpr int STEP = KR ? (64 / G::CPR > 0 ? 64 / G::CPR : 1) : 0;
   static_assert(G::CPR <= 64, "a load covers whole k rows");
+  static constexpr int STEP = KR ? 64 / G::CPR : 0;
 
   // row0: the tile's first row (column, KR) of the operand; rows: how many it has.
   __device__ __forceinline__ void set(int64_t ld, int row0, int rows) {
@@ -251,17 +257,18 @@ struct LoadOffs {
     if constexpr (!KR) {
       k = ((lane & 3) ^ ((lane >> 4) & 3)) * G::EPC;
 #pragma unroll
-      for (int q = 0; q < MI; ++q) {
-        int r = 16 * (MI * wave + q) + (lane >> 2);
-        if constexpr (DUAL) r = (wave >> 1) * (16 * MI) + r % (16 * MI);
+      for (int q = 0; q < LQ; ++q) {
+        // of both projections, even waves load 32 rows of Wg and odd ones
+        // the same rows of Wu
+        int r = 32 * (DUAL ? wave >> 1 : wave) + 16 * q + (lane >> 2);
         r = min(r, rows - 1 - row0);
         off[q] = (uint32_t)r * (uint32_t)(ld * G::SIZE) + (uint32_t)(k * G::SIZE);
       }
     } else {
       const int last = (rows + G::EPC - 1) / G::EPC * G::EPC - G::EPC - row0;
 #pragma unroll
-      for (int q = 0; q < MI; ++q) {
-        const int at = (MI * wave + q) * 64 + lane;
+      for (int q = 0; q < LQ; ++q) {
+        const int at = (LQ * wave + q) * 64 + lane;
         const int krow = at / G::CPR, chunk = (at % G::CPR) ^ G::swz(krow);
         if (q == 0) k = krow;
         off[q] = (uint32_t)krow * (uint32_t)(ld * G::SIZE) +
@@ -278,15 +285,16 @@ struct LoadOffs {
 // Fragments: 16 bytes of a row for a lane, whose k are one slice's (half a
 // stage): 8 bf16, or 4 float32 of which the e-th goes into the e-th product
 // (lanes 0-31 and 32-63 hold different k; A and B the same ones).
-template <typename T, int MI>
+template <int MI>
 struct Frags {
-  u32x4 a[MI], b[MI];
+  u32x4 a[MI], b[2];
 };
 
-template <typename T, int MI, bool KR>
+// Of NB blocks of an operand.
+template <typename T, int MI, int NB, bool KR>
 struct FragOffs {
   typedef Geo<T, MI> G;
-  uint32_t o[KR ? (G::SIZE == 2 ? 2 * MI : 1) : 2];
+  uint32_t o[KR ? (G::SIZE == 2 ? 2 * NB : 1) : 2];
   __device__ __forceinline__ explicit FragOffs(int rbase) {
     const int lane = fresh_tid() & 63;
     if constexpr (!KR) {
@@ -298,7 +306,7 @@ struct FragOffs {
     } else if constexpr (G::SIZE == 2) {
       const int g = lane >> 4, j = lane & 15;
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int krow = 8 * (g >> 1) + 4 * r + (j >> 2);
@@ -411,8 +419,8 @@ struct LoadPos {
   }
   // Load q of this wave (A's, then B's) into the stage buffer at LDS address buf.
   __device__ __forceinline__ void load(uint32_t buf, int q) const {
-    if (q < MI) dma16(abase, a.at(q, left), buf + 1024u * q);
-    else dma16(bbase, b.at(q - MI, left), buf + G::HALF + 1024u * (q - MI));
+    if (q < LQ) dma16(abase, a.at(q, left), buf + 1024u * q);
+    else dma16(bbase, b.at(q - LQ, left), buf + (uint32_t)G::HALF + 1024u * (q - LQ));
   }
 };
 
@@ -421,64 +429,61 @@ struct LoadPos {
 // sched_barrier keeps the order of the products and the memory instructions
 // between them.
 template <typename T, int KIND, int MI>
-__device__ __forceinline__ void step(f32x16 (&acc)[MI][MI], Frags<T, MI>& f0, Frags<T, MI>& f1,
+__device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI>& f0, Frags<MI>& f1,
                                      const char* cur, const char* nxt, uint32_t ldb,
                                      const LoadPos<T, KIND, MI>& L,
-                                     const FragOffs<T, MI, kind_a_kr(KIND)>& fa,
-                                     const FragOffs<T, MI, kind_b_kr(KIND)>& fb) {
+                                     const FragOffs<T, MI, MI, kind_a_kr(KIND)>& fa,
+                                     const FragOffs<T, MI, 2, kind_b_kr(KIND)>& fb) {
   typedef Geo<T, MI> G;
-  constexpr int Q = MI * MI;
+  constexpr int Q = 2 * MI;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / MI][q % MI], f0.a[q / MI], f0.b[q % MI]);
-    if (q < MI) f1.a[q] = fa.read(cur, q, 1);
-    else if (q < 2 * MI) f1.b[q - MI] = fb.read(cur + G::HALF, q - MI, 1);
+    mma<T>(acc[q / 2][q % 2], f0.a[q / 2], f0.b[q % 2]);
+    if (q < 2) f1.b[q] = fb.read(cur + G::HALF, q, 1);
+    else if (q - 2 < MI) f1.a[q - 2] = fa.read(cur, q - 2, 1);
     __builtin_amdgcn_sched_barrier(0);
   }
   // stage k + 1 must have landed; stages k + 2 and k + 3 may be in flight
-  wait_vm<4 * MI>();
+  wait_vm<4 * LQ>();
   meet();
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / MI][q % MI], f1.a[q / MI], f1.b[q % MI]);
-    if (q < MI) f0.a[q] = fa.read(nxt, q, 0);
-    else if (q < 2 * MI) f0.b[q - MI] = fb.read(nxt + G::HALF, q - MI, 0);
-    if (Q == 2 * MI) L.load(ldb, q);
-    else if (q >= 2 * MI && q < 4 * MI) L.load(ldb, q - 2 * MI);
+    mma<T>(acc[q / 2][q % 2], f1.a[q / 2], f1.b[q % 2]);
+    if (q < 2) f0.b[q] = fb.read(nxt + G::HALF, q, 0);
+    else if (q - 2 < MI) f0.a[q - 2] = fa.read(nxt, q - 2, 0);
+    if (q >= Q - 2 * LQ) L.load(ldb, q - (Q - 2 * LQ));
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Half h (16 rows) of a row of blocks into a chunk of 32 MI columns; those of
+// Half h (16 rows) of a row of blocks into a chunk of 64 columns; those of
 // rows with bit 2 set are turned by 32, which puts the two halves of a wave
 // into different banks.
-template <int MI>
-__device__ __forceinline__ void put_chunk(const f32x16 (&acc)[MI], int h, float* stage) {
-  constexpr int W = 32 * MI;
+__device__ __forceinline__ void put_chunk(const f32x16 (&acc)[2], int h, float* stage) {
   const int lane = fresh_tid() & 63;
 #pragma unroll
-  for (int j = 0; j < MI; ++j)
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
       const int c = 32 * j + (lane & 31) + 32 * (lane >> 5);   // bit 2 of row: lane >> 5
-      stage[row * W + (c & (W - 1))] = acc[j][8 * h + r];
+      stage[row * 64 + (c & 63)] = acc[j][8 * h + r];
     }
 }
 
-// The results of this wave's blocks, 16 rows at a time through its share of
-// the stage buffer.
+// The results of this wave's blocks, 16 rows at a time through its share (4
+// KB) of the stage buffer.
 template <typename T, int KIND, int MI>
-__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][MI], const TileArgs& A, Tile t,
+__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const TileArgs& A, Tile t,
                                          float* stage) {
+  typedef Geo<T, MI> G;
   constexpr bool DUAL = kind_dual(KIND);
-  constexpr int W = 32 * MI;               // columns of a chunk
-  constexpr int OUT = DUAL ? W / 2 : W;    // and of its results
+  constexpr int OUT = DUAL ? 32 : 64;      // result columns of a chunk
   constexpr int LPR = OUT / 4;             // lanes of a result row
   constexpr int RPI = 64 / LPR;            // rows of a read
   const int tid = fresh_tid(), lane = tid & 63, wave = uniform(tid >> 6);
-  const int row0 = t.tm * (64 * MI) + (wave >> 1) * W;
-  const int col = t.tn * (2 * OUT) + (wave & 1) * OUT + 4 * (lane % LPR);
+  const int row0 = t.tm * G::ROWS + (wave / G::WN) * (32 * MI);
+  const int col = (t.tn * G::WN + wave % G::WN) * OUT + 4 * (lane % LPR);
   const f32x4 bias = load_bias<T, KIND>(A.p, col);
   const bool cols_in = col < (KIND == kSlope || KIND == kGatedSlope ? A.p.pad : A.p.N);
   // one copy of what follows the registers: a chunk's sums are picked by a
@@ -493,7 +498,7 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][MI], const Tile
     switch (chunk) {
 #define SM_CHUNK(C) \
   case C: \
-    if constexpr ((C) < 2 * MI) put_chunk<MI>(acc[(C) / 2 % MI], (C) % 2, stage); \
+    if constexpr ((C) < 2 * MI) put_chunk(acc[(C) / 2 % MI], (C) % 2, stage); \
     break;
       SM_CHUNK(0)
       SM_CHUNK(1)
@@ -509,18 +514,18 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][MI], const Tile
     for (int k = 0; k < 16 / RPI; ++k) {
       const int row = lane / LPR + RPI * k;
       const int turn = 32 * ((row >> 2) & 1);
-      const int cg = 4 * (lane % LPR);
-      const f32x4 g = *reinterpret_cast<const f32x4*>(stage + row * W + ((cg + turn) & (W - 1)));
+      const int c = 4 * (lane % LPR);
+      const f32x4 g = *reinterpret_cast<const f32x4*>(stage + row * 64 + ((c + turn) & 63));
       f32x4 u = {};
       if constexpr (DUAL)
-        u = *reinterpret_cast<const f32x4*>(stage + row * W + ((cg + OUT + turn) & (W - 1)));
+        u = *reinterpret_cast<const f32x4*>(stage + row * 64 + ((c + OUT + turn) & 63));
       if (cols_in) finish4<T, KIND>(A.p, t.prob, r0 + RPI * k, col, g, u, bias, in[k]);
     }
   }
 }
 
 template <typename T, int KIND, int MI>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(MI == 4 ? 1 : 2, MI == 4 ? 1 : 2)))
+__global__ __launch_bounds__(128 * MI) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void k_tile(TileArgs A) {
   typedef Geo<T, MI> G;
   __shared__ __attribute__((aligned(16))) char smem[NBUF * G::STAGE];
@@ -531,34 +536,32 @@ void k_tile(TileArgs A) {
   const int wave = uniform(fresh_tid() >> 6);
   const uint32_t la0 =
       (uint32_t)uniform((int)(uint32_t)(size_t)(__attribute__((address_space(3))) void*)smem) +
-      1024u * MI * wave;
+      1024u * LQ * wave;
   LoadPos<T, KIND, MI> L;
   L.set(A, t, 0);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
 #pragma unroll
-    for (int q = 0; q < 2 * MI; ++q) L.load(la0 + s * G::STAGE, q);
+    for (int q = 0; q < 2 * LQ; ++q) L.load(la0 + s * G::STAGE, q);
     L.advance(A, stride);
   }
-  wait_vm<6 * MI>();
+  wait_vm<6 * LQ>();
   meet();
-  const int wm = wave >> 1, wn = wave & 1;
-  const FragOffs<T, MI, kind_a_kr(KIND)> fa(wm * 32 * MI);
-  const FragOffs<T, MI, kind_b_kr(KIND)> fb(wn * 32 * MI);
-  Frags<T, MI> f0, f1;
+  const FragOffs<T, MI, MI, kind_a_kr(KIND)> fa((wave / G::WN) * 32 * MI);
+  const FragOffs<T, MI, 2, kind_b_kr(KIND)> fb((wave % G::WN) * 64);
+  Frags<MI> f0, f1;
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    f0.a[i] = fa.read(smem, i, 0);
-    f0.b[i] = fb.read(smem + G::HALF, i, 0);
-  }
+  for (int i = 0; i < MI; ++i) f0.a[i] = fa.read(smem, i, 0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) f0.b[j] = fb.read(smem + G::HALF, j, 0);
   int cb = 0;
   const int steps = (A.p.K + G::BK - 1) / G::BK * (KIND == kDx ? A.p.parts : 1);
   for (; t < A.total; t += stride) {
-    f32x16 acc[MI][MI];
+    f32x16 acc[MI][2];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < MI; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     for (int k = 0; k < steps; ++k) {
@@ -573,16 +576,17 @@ void k_tile(TileArgs A) {
     meet();
     epilogue<T, KIND, MI>(acc, A, decode_tile(A, uniform(t)),
                           reinterpret_cast<float*>(smem + (cb == 0 ? NBUF - 1 : cb - 1) * G::STAGE +
-                                                   wave * (G::STAGE / 4)));
+                                                   wave * 4096));
   }
   wait_vm<0>();   // loads past the last stage target this workgroup's LDS
 }
 
 template <typename T, int MI>
 void launch_tile(const TileArgs& a, int grid, hipStream_t s) {
+  constexpr int threads = Geo<T, MI>::THREADS;
   switch (a.p.kind) {
 #define SM_KIND(K) \
-  case K: hipLaunchKernelGGL((k_tile<T, K, MI>), dim3(grid), dim3(NT), 0, s, a); break;
+  case K: hipLaunchKernelGGL((k_tile<T, K, MI>), dim3(grid), dim3(threads), 0, s, a); break;
     SM_KIND(kLinear)
     SM_KIND(kSlope)
     SM_KIND(kGated)
