@@ -556,7 +556,7 @@ sm_status sm_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* m_
  * Both are contiguous, at any alignment.
  * Errors: SM_ERR_ARG (null or misaligned pointers, ldx < d, an output
  *   overlapping another buffer), SM_ERR_SHAPE (T < 0 or > 2^30, d < 1 or
- *   > 2^20), SM_ERR_DTYPE, SM_ERR_HIP.  T == 0 is a no-op.
+ *   > 2^20, T d > 2^40), SM_ERR_DTYPE, SM_ERR_HIP.  T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 #define SM_ACT8_BLOCK 32
 sm_status sm_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int32_t d, uint8_t* x8,

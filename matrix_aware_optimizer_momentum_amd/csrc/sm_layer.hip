@@ -62,6 +62,7 @@ int act8_blocks(int d) { return (d + SM_ACT8_BLOCK - 1) / SM_ACT8_BLOCK; }
 sm_status check_act8(const void* x, int64_t ldx, int dt, int64_t T, int32_t d, const uint8_t* x8,
                      const uint8_t* scale, bool pack) {
   SM_TRY(check_sizes(T, d, dt));
+  if (T * d > kMaxCount) return SM_ERR_SHAPE;
   if (T == 0) return SM_OK;
   SM_TRY(check_matrix(x, ldx, d, dt_size(dt)));
   if (!x8 || !scale) return SM_ERR_ARG;
