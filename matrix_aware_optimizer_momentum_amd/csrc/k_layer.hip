@@ -61,6 +61,12 @@ __global__ __launch_bounds__(256) void k_lay_out(const T* p, int64_t ldp, int64_
 
 sm_status launch_product(const Product& p, hipStream_t s) {
   using namespace layer;
+  if (few_tokens(p.kind, p.M)) {
+    prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : 1), s, 0.0);
+    launch_few(p, s);
+    prof_end(s);
+    return check_launch();
+  }
   TileArgs a;
   a.p = p;
   const int cols = std::max(p.N, p.pad);

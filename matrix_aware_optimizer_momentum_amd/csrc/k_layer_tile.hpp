@@ -597,6 +597,9 @@ void launch_tile(const TileArgs& a, int grid, hipStream_t s) {
   }
 }
 
+// kLinear and kGated of few tokens (k_layer_few.hip).
+void launch_few(const Product& p, hipStream_t s);
+
 // One translation unit for each type and tile.
 void launch_tile_bf16_4(const TileArgs& a, int grid, hipStream_t s);
 void launch_tile_bf16_2(const TileArgs& a, int grid, hipStream_t s);

@@ -37,7 +37,11 @@ struct Product {
   int accumulate;     // kDw
 };
 
-// Launches p.  Every operand's rows (as they are stored) are 16-byte aligned,
+// The kernel for few tokens takes the product, operands of any alignment.
+inline bool few_tokens(int kind, int64_t T) {
+  return (kind == kLinear || kind == kGated) && T <= 32;
+}
+// Launches p.  Unless few_tokens, every operand's rows (as they are stored) are 16-byte aligned,
 // less than 2^31 / 256 bytes apart, and a multiple of 16 bytes long, or have
 // readable memory up to one, zeros if they run along k.
 sm_status launch_product(const Product& p, hipStream_t s);

@@ -167,7 +167,7 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
   };
   w.ldd = round_up(l.d, 8);
   w.ldn = round_up(l.n, 8);
-  if (l.T == 0) return w;
+  if (l.T == 0 || (!is_grad(c) && few_tokens(is_gated(c) ? kGated : kLinear, l.T))) return w;
   const bool grad = is_grad(c), x8 = grad && l.x8;
   const bool again = !grad || makes_dz(l, c);   // x W^T is computed
   w.lay_x = !x8 && reads_x(l, c) && !laid_out(l.x, l.ldx, l.d, l.dt);
