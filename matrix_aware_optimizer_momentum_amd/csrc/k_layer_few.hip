@@ -119,8 +119,18 @@ __global__ __launch_bounds__(1024) void k_few(Product p) {
     for (int i = 0; i < W; ++i) s[i] += sums[q][i * TB + wave][lane];
   const int row = 16 * wave + r, col = n0 + 4 * (lane >> 4);
   if (col >= p.N) return;
-  finish4<T, KIND>(p, 0, row, col, s[0], s[W - 1], load_bias<T, KIND>(p, col),
-                   load_in<T, KIND>(p, 0, row, col));
+  const f32x4 bias = load_bias<T, KIND>(p, col);
+  const f32x4 in = load_in<T, KIND>(p, 0, row, col);
+  switch (p.act) {
+#define SM_ACT(A) \
+  case A: finish4<T, KIND, A>(p, 0, row, col, s[0], s[W - 1], bias, in); break;
+    SM_ACT(SM_ACT_NONE)
+    SM_ACT(SM_ACT_RELU)
+    SM_ACT(SM_ACT_SILU)
+    SM_ACT(SM_ACT_GELU)
+    SM_ACT(SM_ACT_GELU_TANH)
+#undef SM_ACT
+  }
 }
 
 // 16 waves, where the rows have a piece for each.  (One token, us, with 4 / 8 /

@@ -29,11 +29,10 @@
 // the buffer descriptor's range, which puts zeros into LDS: no garbage meets
 // the sums, and no NaN of memory behind a matrix.
 //
-// Epilogue.  The sums go through LDS (the wave's share of the stage buffer
-// just multiplied) in chunks of 16 rows, float32, and come back as four
-// columns of a row per lane, so that bias, residual and dy are read, and
-// results written, in whole 128-byte lines or more; finish4 is the same code
-// for every kernel.
+// Epilogue.  The products are taken as B A^T, whose sums a lane holds as four
+// consecutive columns of one row at a time.  Results are made from them in the
+// registers; residual, dy or old gradients come to them, and they go to
+// memory, through the wave's 4 KB share of the stage buffer just multiplied.
 #pragma once
 
 #include "layer_math.hpp"
@@ -87,6 +86,24 @@ __device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
       u32x2{__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2)),
             __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2))};
 }
+// Four entries as they are stored (in half the registers, of bf16 ones).
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+  f32x4 r;
+  __device__ __forceinline__ f32x4 value() const { return r; }
+};
+template <> struct Raw4<bf16_t> {
+  u32x2 r;
+  __device__ __forceinline__ f32x4 value() const {
+    return f32x4{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
+                 __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u)};
+  }
+};
+template <typename T>
+__device__ __forceinline__ Raw4<T> load_raw4(const T* p) {
+  typedef decltype(Raw4<T>::r) V __attribute__((aligned(2)));
+  return Raw4<T>{*reinterpret_cast<const V*>(p)};
+}
 // Of which `left` exist.
 template <typename T>
 __device__ __forceinline__ f32x4 load4(const T* p, int left) {
@@ -117,37 +134,36 @@ __device__ __forceinline__ f32x4 load_bias(const Product& p, int col) {
 // The entries that the results are combined with, ahead of their use.
 template <typename T, int KIND>
 __device__ __forceinline__ f32x4 load_in(const Product& p, int prob, int row, int col) {
-  f32x4 v = {};
   if (row < p.M && col < p.N) {
     if constexpr (KIND == kDw) {
       if (p.accumulate)
-        v = load4(static_cast<const T*>(prob ? p.c[1] : p.c[0]) +
-                      row * (prob ? p.ldc[1] : p.ldc[0]) + col,
-                  p.N - col);
+        return load4(static_cast<const T*>(prob ? p.c[1] : p.c[0]) +
+                         row * (prob ? p.ldc[1] : p.ldc[0]) + col,
+                     p.N - col);
     } else if constexpr (KIND != kGated && KIND != kDx) {
-      if (p.in.p) v = load4(static_cast<const T*>(p.in.p) + row * p.in.ld + col, p.N - col);
+      if (p.in.p) return load4(static_cast<const T*>(p.in.p) + row * p.in.ld + col, p.N - col);
     }
   }
-  return v;
+  return f32x4{};
 }
-// Columns col .. col + 3 of a row's results, from the sums g (and u of a
-// gated layer).
-template <typename T, int KIND>
-__device__ __forceinline__ void finish4(const Product& p, int prob, int row, int col, f32x4 g,
-                                        f32x4 u, f32x4 bias, f32x4 in) {
+// Four columns of a row's results, from the sums g (and u of a gated layer).
+struct Results4 {
+  f32x4 v, v2;
+};
+template <typename T, int KIND, int ACT>
+__device__ __forceinline__ Results4 results4(f32x4 g, f32x4 u, f32x4 bias, f32x4 in) {
   constexpr bool FINE = sizeof(T) == 4;
-  if (row >= p.M) return;
   f32x4 v, v2 = {};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if constexpr (KIND == kLinear) {
-      v[e] = act_value<FINE>(p.act, g[e] + bias[e]) + in[e];
+      v[e] = act_value<FINE>(ACT, g[e] + bias[e]) + in[e];
     } else if constexpr (KIND == kSlope) {
-      v[e] = in[e] * act_both<FINE>(p.act, g[e] + bias[e]).slope;
+      v[e] = in[e] * act_both<FINE>(ACT, g[e] + bias[e]).slope;
     } else if constexpr (KIND == kGated) {
-      v[e] = act_value<FINE>(p.act, g[e]) * u[e];
+      v[e] = act_value<FINE>(ACT, g[e]) * u[e];
     } else if constexpr (KIND == kGatedSlope) {
-      const ActBoth h = act_both<FINE>(p.act, g[e]);
+      const ActBoth h = act_both<FINE>(ACT, g[e]);
       v[e] = in[e] * u[e] * h.slope;
       v2[e] = in[e] * h.value;
     } else if constexpr (KIND == kDw) {
@@ -156,20 +172,28 @@ __device__ __forceinline__ void finish4(const Product& p, int prob, int row, int
       v[e] = g[e];
     }
   }
+  return {v, v2};
+}
+// And stored, where they exist.
+template <typename T, int KIND, int ACT>
+__device__ __forceinline__ void finish4(const Product& p, int prob, int row, int col, f32x4 g,
+                                        f32x4 u, f32x4 bias, f32x4 in) {
+  if (row >= p.M) return;
+  Results4 r = results4<T, KIND, ACT>(g, u, bias, in);
   int left = p.N - col;
   if constexpr (KIND == kSlope || KIND == kGatedSlope) {
     // dz has zeros up to a multiple of 8 columns
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (e >= left) v[e] = 0.f;
-      if (e >= left) v2[e] = 0.f;
+      if (e >= left) r.v[e] = 0.f;
+      if (e >= left) r.v2[e] = 0.f;
     }
     left = p.pad - col;
   }
-  store4(static_cast<T*>(prob ? p.c[1] : p.c[0]) + row * (prob ? p.ldc[1] : p.ldc[0]) + col, v,
+  store4(static_cast<T*>(prob ? p.c[1] : p.c[0]) + row * (prob ? p.ldc[1] : p.ldc[0]) + col, r.v,
          left);
   if constexpr (KIND == kGatedSlope)
-    store4(static_cast<T*>(p.c[1]) + row * p.ldc[1] + col, v2, left);
+    store4(static_cast<T*>(p.c[1]) + row * p.ldc[1] + col, r.v2, left);
 }
 
 // ---------------------------------------------------------------- small things
@@ -438,7 +462,7 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI>& f0, Frags<
   constexpr int Q = 2 * MI;
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / 2][q % 2], f0.a[q / 2], f0.b[q % 2]);
+    mma<T>(acc[q / 2][q % 2], f0.b[q % 2], f0.a[q / 2]);
     if (q < 2) f1.b[q] = fb.read(cur + G::HALF, q, 1);
     else if (q - 2 < MI) f1.a[q - 2] = fa.read(cur, q - 2, 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -448,7 +472,7 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI>& f0, Frags<
   meet();
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / 2][q % 2], f1.a[q / 2], f1.b[q % 2]);
+    mma<T>(acc[q / 2][q % 2], f1.b[q % 2], f1.a[q / 2]);
     if (q < 2) f0.b[q] = fb.read(nxt + G::HALF, q, 0);
     else if (q - 2 < MI) f0.a[q - 2] = fa.read(nxt, q - 2, 0);
     if (q >= Q - 2 * LQ) L.load(ldb, q - (Q - 2 * LQ));
@@ -456,71 +480,190 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI>& f0, Frags<
   }
 }
 
-// Half h (16 rows) of a row of blocks into a chunk of 64 columns; those of
-// rows with bit 2 set are turned by 32, which puts the two halves of a wave
-// into different banks.
-__device__ __forceinline__ void put_chunk(const f32x16 (&acc)[2], int h, float* stage) {
+// The results of this wave's blocks, some of which lie past an edge: from the
+// registers, entry by entry where a row ends.
+template <typename T, int KIND, int ACT, int MI>
+__device__ __forceinline__ void epilogue_edge(const f32x16 (&acc)[MI][2], const Product& p,
+                                              int prob, int row0, int col0) {
+  constexpr bool DUAL = kind_dual(KIND);
   const int lane = fresh_tid() & 63;
+  const int row = row0 + (lane & 31), col = col0 + 4 * (lane >> 5);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < (DUAL ? 1 : 2); ++j)
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int row = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      const int c = 32 * j + (lane & 31) + 32 * (lane >> 5);   // bit 2 of row: lane >> 5
-      stage[row * 64 + (c & 63)] = acc[j][8 * h + r];
+    for (int q = 0; q < 4; ++q) {
+      const int c = col + 32 * j + 8 * q;
+      const f32x4 bias = load_bias<T, KIND>(p, c);
+      f32x4 in[MI];
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        in[i] = load_in<T, KIND>(p, prob, row + 32 * i, c);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        f32x4 g, u = {};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = acc[i][j][4 * q + e];
+          if constexpr (DUAL) u[e] = acc[i][1][4 * q + e];
+        }
+        finish4<T, KIND, ACT>(p, prob, row + 32 * i, c, g, u, bias, in[i]);
+      }
     }
 }
 
-// The results of this wave's blocks, 16 rows at a time through its share (4
-// KB) of the stage buffer.
-template <typename T, int KIND, int MI>
-__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const TileArgs& A, Tile t,
-                                         float* stage) {
-  typedef Geo<T, MI> G;
+// A patch of 32 rows of RB bytes in LDS, by which a wave turns between its
+// sums' layout (a row to a lane) and whole lines: the 16-byte pieces of row r
+// are permuted so that neither side's accesses meet in few banks.  One wave's
+// LDS accesses take effect in order, so no barrier is needed between them, but
+// the compiler has to keep that order (a lane's accesses are not its own alone).
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
+template <int RB>
+__device__ __forceinline__ uint32_t patch_at(int row, int byte) {
+  const int s = RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+  return (uint32_t)(row * RB + (((byte >> 4) ^ s) << 4) + (byte & 15));
+}
+
+// The same where all of them exist: what they are combined with, and they
+// themselves, go through a patch, so that memory sees 16 bytes a lane and
+// whole lines.  (Straight from the registers, 16 bytes of each of 32 rows at
+// a time, a 256 x 256 tile took 15 us longer to store.)
+template <typename T, int KIND, int ACT, int MI>
+__device__ __forceinline__ void epilogue_inside(const f32x16 (&acc)[MI][2], const Product& p,
+                                                int prob, int row0, int col0, char* patch) {
   constexpr bool DUAL = kind_dual(KIND);
-  constexpr int OUT = DUAL ? 32 : 64;      // result columns of a chunk
-  constexpr int LPR = OUT / 4;             // lanes of a result row
-  constexpr int RPI = 64 / LPR;            // rows of a read
-  const int tid = fresh_tid(), lane = tid & 63, wave = uniform(tid >> 6);
-  const int row0 = t.tm * G::ROWS + (wave / G::WN) * (32 * MI);
-  const int col = (t.tn * G::WN + wave % G::WN) * OUT + 4 * (lane % LPR);
-  const f32x4 bias = load_bias<T, KIND>(A.p, col);
-  const bool cols_in = col < (KIND == kSlope || KIND == kGatedSlope ? A.p.pad : A.p.N);
-  // one copy of what follows the registers: a chunk's sums are picked by a
-  // uniform switch, so that the registers' numbers stay constants
-#pragma unroll 1
-  for (int chunk = 0; chunk < 2 * MI; ++chunk) {
-    const int r0 = row0 + 16 * chunk + lane / LPR;
-    f32x4 in[16 / RPI];
+  constexpr int SIZE = sizeof(T);
+  constexpr int JC = !DUAL && SIZE == 2 ? 2 : 1;      // column blocks of a patch
+  constexpr int RB = 32 * JC * SIZE;                  // bytes of its rows
+  constexpr int LPR = RB / 16, RPI = 64 / LPR;        // lanes of a row, rows of an access
+  constexpr int NR = 32 / RPI;
+  constexpr int JP = DUAL ? 1 : 2 / JC;               // patches side by side
+  constexpr int NP = MI * JP;
+  constexpr bool HAS_IN = KIND == kLinear || KIND == kSlope || KIND == kGatedSlope || KIND == kDw;
+  typedef u32x4 V __attribute__((aligned(2)));
+  const int lane = fresh_tid() & 63;
+  const int prow = lane / LPR, pbyte = 16 * (lane % LPR);
+  const int srow = lane & 31, sbyte = 4 * SIZE * (lane >> 5);
+  char* c0 = static_cast<char*>(prob ? p.c[1] : p.c[0]);
+  const int64_t ldc = (prob ? p.ldc[1] : p.ldc[0]) * SIZE;
+  const char* in0 = nullptr;
+  int64_t ldin = 0;
+  if constexpr (KIND == kDw) {
+    if (p.accumulate) in0 = c0, ldin = ldc;
+  } else if constexpr (HAS_IN) {
+    in0 = static_cast<const char*>(p.in.p);
+    ldin = p.in.ld * SIZE;
+  }
+  // this lane's place in a patch's first rows, and a patch's k-th ones from there
+  const int64_t at_in = prow * ldin + pbyte, at_c = prow * ldc + pbyte;
+  auto patch_of = [&](int n, int k, int64_t ld) {
+    return (row0 + 32 * (n % MI) + RPI * k) * ld + (col0 + 32 * (n / MI)) * SIZE;
+  };
+  u32x4 ahead[NR] = {};
+  auto load_patch = [&](int n) {
+    if (in0) {
 #pragma unroll
-    for (int k = 0; k < 16 / RPI; ++k)
-      in[k] = load_in<T, KIND>(A.p, t.prob, r0 + RPI * k, col);
-    switch (chunk) {
-#define SM_CHUNK(C) \
-  case C: \
-    if constexpr ((C) < 2 * MI) put_chunk(acc[(C) / 2 % MI], (C) % 2, stage); \
-    break;
-      SM_CHUNK(0)
-      SM_CHUNK(1)
-      SM_CHUNK(2)
-      SM_CHUNK(3)
-      SM_CHUNK(4)
-      SM_CHUNK(5)
-      SM_CHUNK(6)
-      SM_CHUNK(7)
-#undef SM_CHUNK
+      for (int k = 0; k < NR; ++k)
+        ahead[k] = *reinterpret_cast<const V*>(in0 + patch_of(n, k, ldin) + at_in);
+    }
+  };
+  if constexpr (HAS_IN) load_patch(0);
+  constexpr int Q = 4 * JC;   // a lane's fours of columns in a patch
+  constexpr bool HAS_BIAS = KIND == kLinear || KIND == kSlope;
+  Raw4<T> bias[HAS_BIAS ? Q : 1] = {};
+  meet();   // every wave is past its reads of the stage that the patches take
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    if constexpr (HAS_BIAS) {
+      if (n % MI == 0 && p.bias) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          bias[q] = load_raw4(static_cast<const T*>(p.bias) + col0 + 32 * (n / MI) + 8 * q +
+                              4 * (lane >> 5));
+      }
+    }
+    Raw4<T> in[Q] = {}, out2[Q];
+    if constexpr (HAS_IN) {
+      if (in0) {
+#pragma unroll
+        for (int k = 0; k < NR; ++k)
+          *reinterpret_cast<u32x4*>(patch + patch_at<RB>(prow + RPI * k, pbyte)) = ahead[k];
+        in_order();
+        if (n + 1 < NP) load_patch(n + 1);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          in[q] = load_raw4(
+              reinterpret_cast<const T*>(patch + patch_at<RB>(srow, 8 * SIZE * q + sbyte)));
+        in_order();
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 16 / RPI; ++k) {
-      const int row = lane / LPR + RPI * k;
-      const int turn = 32 * ((row >> 2) & 1);
-      const int c = 4 * (lane % LPR);
-      const f32x4 g = *reinterpret_cast<const f32x4*>(stage + row * 64 + ((c + turn) & 63));
-      f32x4 u = {};
-      if constexpr (DUAL)
-        u = *reinterpret_cast<const f32x4*>(stage + row * 64 + ((c + OUT + turn) & 63));
-      if (cols_in) finish4<T, KIND>(A.p, t.prob, r0 + RPI * k, col, g, u, bias, in[k]);
+    for (int q = 0; q < Q; ++q) {
+      const int i = n % MI, j = DUAL ? 0 : n / MI + q / 4;
+      f32x4 g, u = {};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = acc[i][j][4 * (q % 4) + e];
+        if constexpr (DUAL) u[e] = acc[i][1][4 * (q % 4) + e];
+      }
+      const f32x4 b = HAS_BIAS ? bias[HAS_BIAS ? q : 0].value() : f32x4{};
+      const Results4 r = results4<T, KIND, ACT>(g, u, b, in[q].value());
+      store4(reinterpret_cast<T*>(patch + patch_at<RB>(srow, 8 * SIZE * q + sbyte)), r.v);
+      if constexpr (KIND == kGatedSlope) store4(reinterpret_cast<T*>(&out2[q]), r.v2);
     }
+    auto write_patch = [&](char* c) {
+      in_order();
+#pragma unroll
+      for (int k = 0; k < NR; ++k)
+        *reinterpret_cast<V*>(c + patch_of(n, k, ldc) + at_c) =
+            *reinterpret_cast<const u32x4*>(patch + patch_at<RB>(prow + RPI * k, pbyte));
+      in_order();
+    };
+    write_patch(c0);
+    if constexpr (KIND == kGatedSlope) {   // da and db have one ld
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        *reinterpret_cast<Raw4<T>*>(patch + patch_at<RB>(srow, 8 * SIZE * q + sbyte)) = out2[q];
+      write_patch(static_cast<char*>(p.c[1]));
+    }
+    __builtin_amdgcn_sched_barrier(0);   // one patch at a time keeps few values live
+  }
+}
+
+template <typename T, int KIND, int ACT, int MI>
+__device__ __forceinline__ void epilogue_of(const f32x16 (&acc)[MI][2], const Product& p,
+                                            int prob, int row0, int col0, bool inside,
+                                            char* patch) {
+  if (inside) {
+    epilogue_inside<T, KIND, ACT, MI>(acc, p, prob, row0, col0, patch);
+  } else {
+    meet();   // as the waves whose blocks are inside
+    epilogue_edge<T, KIND, ACT, MI>(acc, p, prob, row0, col0);
+  }
+}
+
+template <typename T, int KIND, int MI>
+__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const Product& p, Tile t,
+                                         char* stage) {
+  typedef Geo<T, MI> G;
+  constexpr int OUT = kind_dual(KIND) ? 32 : 64;   // a wave's result columns
+  const int wave = uniform(fresh_tid() >> 6);
+  const int row0 = uniform(t.tm * G::ROWS + (wave / G::WN) * (32 * MI));
+  const int col0 = uniform((t.tn * G::WN + wave % G::WN) * OUT);
+  char* patch = stage + 4096 * wave;
+  const bool inside = row0 + 32 * MI <= p.M && col0 + OUT <= p.N;
+  if constexpr (kind_acts(KIND)) {
+    switch (p.act) {
+#define SM_ACT(A) \
+  case A: epilogue_of<T, KIND, A, MI>(acc, p, t.prob, row0, col0, inside, patch); break;
+      SM_ACT(SM_ACT_NONE)
+      SM_ACT(SM_ACT_RELU)
+      SM_ACT(SM_ACT_SILU)
+      SM_ACT(SM_ACT_GELU)
+      SM_ACT(SM_ACT_GELU_TANH)
+#undef SM_ACT
+    }
+  } else {
+    epilogue_of<T, KIND, SM_ACT_NONE, MI>(acc, p, t.prob, row0, col0, inside, patch);
   }
 }
 
@@ -549,11 +692,6 @@ void k_tile(TileArgs A) {
   meet();
   const FragOffs<T, MI, MI, kind_a_kr(KIND)> fa((wave / G::WN) * 32 * MI);
   const FragOffs<T, MI, 2, kind_b_kr(KIND)> fb((wave % G::WN) * 64);
-  Frags<MI> f0, f1;
-#pragma unroll
-  for (int i = 0; i < MI; ++i) f0.a[i] = fa.read(smem, i, 0);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) f0.b[j] = fb.read(smem + G::HALF, j, 0);
   int cb = 0;
   const int steps = (A.p.K + G::BK - 1) / G::BK * (KIND == kDx ? A.p.parts : 1);
   for (; t < A.total; t += stride) {
@@ -564,6 +702,13 @@ void k_tile(TileArgs A) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    // the first stage's first fragments, again after an epilogue (whose
+    // registers they would take)
+    Frags<MI> f0, f1;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) f0.a[i] = fa.read(smem + cb * G::STAGE, i, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) f0.b[j] = fb.read(smem + cb * G::STAGE + G::HALF, j, 0);
     for (int k = 0; k < steps; ++k) {
       const int nb = cb == NBUF - 1 ? 0 : cb + 1;
       const int lb = cb == 0 ? NBUF - 1 : cb - 1;
@@ -572,11 +717,8 @@ void k_tile(TileArgs A) {
       L.advance(A, stride);
       cb = nb;
     }
-    // every wave is past its reads of the last stage once all have met
-    meet();
-    epilogue<T, KIND, MI>(acc, A, decode_tile(A, uniform(t)),
-                          reinterpret_cast<float*>(smem + (cb == 0 ? NBUF - 1 : cb - 1) * G::STAGE +
-                                                   wave * 4096));
+    epilogue<T, KIND, MI>(acc, A.p, decode_tile(A, uniform(t)),
+                          smem + (cb == 0 ? NBUF - 1 : cb - 1) * G::STAGE);
   }
   wait_vm<0>();   // loads past the last stage target this workgroup's LDS
 }

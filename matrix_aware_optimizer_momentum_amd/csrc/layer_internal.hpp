@@ -17,6 +17,7 @@ namespace sm {
 //   kDw          c (+)= A^T B  (and c2 (+)= A2^T B)  A = dz KR, B = x KR
 enum ProductKind : int { kLinear, kSlope, kGated, kGatedSlope, kDx, kDw };
 constexpr bool kind_dual(int k) { return k == kGated || k == kGatedSlope; }
+constexpr bool kind_acts(int k) { return k == kLinear || k == kSlope || kind_dual(k); }
 constexpr bool kind_a_kr(int k) { return k == kDw; }
 constexpr bool kind_b_kr(int k) { return k == kDx || k == kDw; }
 
