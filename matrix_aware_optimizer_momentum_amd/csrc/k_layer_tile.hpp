@@ -14,15 +14,18 @@
 // that the wave has act's argument and the factor of an output in its own
 // registers, and x is read once for both.
 //
-// Pipeline.  Operands go HBM -> LDS with direct-to-LDS buffer loads into a
-// ring of five k stages of 64 bytes a row (32 bf16 or 16 float32).  Step k
-// multiplies stage k in two slices: during the first the second's fragments
-// are read; then each wave waits for its own loads of stage k + 1 and the
-// workgroup meets; during the second slice stage k + 1's first fragments are
-// read and the loads of stage k + 4 are issued into the buffer that stage k -
-// 1 has left.  The ring runs on across tiles and across the two parts of a
-// sum (da Wg + db Wu), so that a tile's first stages load during the last
-// steps and the epilogue of the one before.
+// Pipeline.  Operands go HBM -> LDS with direct-to-LDS buffer loads, in stages
+// of 128 bytes a row (64 bf16 or 32 float32 of k): whole lines, since the L2
+// serves a line or half of one in the same time (stages of 64 bytes a row
+// asked it for twice as many).  There are two stage buffers.  A step multiplies
+// a stage in four slices of its k, reading the next slice's fragments
+// meanwhile; ahead of the last slice each wave waits for its reads of this
+// stage and its loads of the next one, and the workgroup meets; during the
+// last slice the next stage's first fragments are read and the loads of the
+// stage after that are issued into this stage's buffer.  So loads have a step
+// less a slice to land.  The stages run on across tiles and across the two
+// parts of a sum (da Wg + db Wu): a tile's first ones load during the last
+// step and the epilogue of the one before.
 //
 // Edges.  Rows past an operand's last read the last one (their sums are not
 // stored).  Where k ends inside a stage, the lanes past it load from beyond
@@ -32,7 +35,7 @@
 // Epilogue.  The products are taken as B A^T, whose sums a lane holds as four
 // consecutive columns of one row at a time.  Results are made from them in the
 // registers; residual, dy or old gradients come to them, and they go to
-// memory, through the wave's 4 KB share of the stage buffer just multiplied.
+// memory, through 4 KB of LDS of the wave's own.
 #pragma once
 
 #include "layer_math.hpp"
@@ -53,8 +56,7 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int NBUF = 5;
-constexpr int ROW = 64;   // bytes of an operand row in a stage
+constexpr int ROW = 128;   // bytes of an operand row in a stage
 
 struct TileArgs {
   Product p;
@@ -242,8 +244,8 @@ __device__ __forceinline__ void dma16(uint64_t base, uint32_t voff, uint32_t m0)
 
 // ---------------------------------------------------------------- stages in LDS
 //
-// KC: rows of 64 bytes; the 16-byte chunk c of row R sits at position c ^
-// ((R >> 2) & 3), so that 16 rows read at one chunk hit 16 different 4-bank
+// KC: rows of 128 bytes; the 16-byte chunk c of row R sits at position c ^
+// ((R >> 1) & 7), so that 16 rows read at one chunk hit 16 different 4-bank
 // groups.  KR: k rows of 64 MI entries; of bf16, chunk c of k row r sits at
 // position c ^ (4 (r & 3)), so that the four k rows of a transposing read lie
 // in four different 64-byte bank ranges.
@@ -261,8 +263,8 @@ struct Geo {
   static __device__ __forceinline__ int swz(int krow) { return SIZE == 2 ? 4 * (krow & 3) : 0; }
 };
 
-// A wave loads 32 rows' worth of each operand's stage, by two loads of 1 KB.
-constexpr int LQ = 2;
+// A wave loads 32 rows' worth of each operand's stage, by four loads of 1 KB.
+constexpr int LQ = 4;
 
 // This lane's byte offsets, from the tile's first entry of a stage, of its
 // loads, and the first k of each within the stage.
@@ -270,23 +272,29 @@ template <typename T, int MI, bool KR, bool DUAL>
 struct LoadOffs {
   typedef Geo<T, MI> G;
   uint32_t off[LQ];
-  // KC: the lane's chunk starts at k; KR: load q reads k row k + q * STEP
+  // KC: the lane's chunk starts at k, of odd loads 4 chunks from there; KR:
+  // load q reads k row k + q * STEP
   int k;
   static_assert(G::CPR <= 64, "a load covers whole k rows");
   static constexpr int STEP = KR ? 64 / G::CPR : 0;
+  __device__ __forceinline__ int k_of(int q) const {
+    if constexpr (KR) return k + q * STEP;
+    else return q & 1 ? k ^ (4 * G::EPC) : k;
+  }
 
   // row0: the tile's first row (column, KR) of the operand; rows: how many it has.
   __device__ __forceinline__ void set(int64_t ld, int row0, int rows) {
     const int tid = fresh_tid(), lane = tid & 63, wave = uniform(tid >> 6);
     if constexpr (!KR) {
-      k = ((lane & 3) ^ ((lane >> 4) & 3)) * G::EPC;
+      // load q covers rows 8 (4 wave + q) + lane / 8
+      k = ((lane & 7) ^ (lane >> 4)) * G::EPC;
 #pragma unroll
       for (int q = 0; q < LQ; ++q) {
         // of both projections, even waves load 32 rows of Wg and odd ones
         // the same rows of Wu
-        int r = 32 * (DUAL ? wave >> 1 : wave) + 16 * q + (lane >> 2);
+        int r = 32 * (DUAL ? wave >> 1 : wave) + 8 * q + (lane >> 3);
         r = min(r, rows - 1 - row0);
-        off[q] = (uint32_t)r * (uint32_t)(ld * G::SIZE) + (uint32_t)(k * G::SIZE);
+        off[q] = (uint32_t)r * (uint32_t)(ld * G::SIZE) + (uint32_t)(k_of(q) * G::SIZE);
       }
     } else {
       const int last = (rows + G::EPC - 1) / G::EPC * G::EPC - G::EPC - row0;
@@ -302,12 +310,12 @@ struct LoadOffs {
   }
   // left: the k that exist from the stage's first on.
   __device__ __forceinline__ uint32_t at(int q, int left) const {
-    return k + q * STEP < left ? off[q] : kNowhere;
+    return k_of(q) < left ? off[q] : kNowhere;
   }
 };
 
-// Fragments: 16 bytes of a row for a lane, whose k are one slice's (half a
-// stage): 8 bf16, or 4 float32 of which the e-th goes into the e-th product
+// Fragments: 16 bytes of a row for a lane, whose k are one slice's (a quarter
+// of a stage): 8 bf16, or 4 float32 of which the e-th goes into the e-th product
 // (lanes 0-31 and 32-63 hold different k; A and B the same ones).
 template <int MI>
 struct Frags {
@@ -318,14 +326,14 @@ struct Frags {
 template <typename T, int MI, int NB, bool KR>
 struct FragOffs {
   typedef Geo<T, MI> G;
-  uint32_t o[KR ? (G::SIZE == 2 ? 2 * NB : 1) : 2];
+  uint32_t o[KR ? (G::SIZE == 2 ? 2 * NB : 1) : 4];
   __device__ __forceinline__ explicit FragOffs(int rbase) {
     const int lane = fresh_tid() & 63;
     if constexpr (!KR) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 4; ++s) {
         const int R = rbase + (lane & 31), c = 2 * s + (lane >> 5);
-        o[s] = (uint32_t)(R * ROW + 16 * (c ^ ((R >> 2) & 3)));
+        o[s] = (uint32_t)(R * ROW + 16 * (c ^ ((R >> 1) & 7)));
       }
     } else if constexpr (G::SIZE == 2) {
       const int g = lane >> 4, j = lane & 15;
@@ -449,34 +457,39 @@ struct LoadPos {
 };
 
 // One step: see the pipeline above.  cur, nxt: this stage and the next one;
-// ldb: LDS address of this wave's slots in the buffer to load into.
+// ldb: LDS address of this wave's slots in cur.  f[0] holds the fragments of
+// the stage's first slice, and on return those of the next one's.
 // sched_barrier keeps the order of the products and the memory instructions
 // between them.
 template <typename T, int KIND, int MI>
-__device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI>& f0, Frags<MI>& f1,
-                                     const char* cur, const char* nxt, uint32_t ldb,
+__device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI> (&f)[2], const char* cur,
+                                     const char* nxt, uint32_t ldb,
                                      const LoadPos<T, KIND, MI>& L,
                                      const FragOffs<T, MI, MI, kind_a_kr(KIND)>& fa,
                                      const FragOffs<T, MI, 2, kind_b_kr(KIND)>& fb) {
   typedef Geo<T, MI> G;
   constexpr int Q = 2 * MI;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / 2][q % 2], f0.b[q % 2], f0.a[q / 2]);
-    if (q < 2) f1.b[q] = fb.read(cur + G::HALF, q, 1);
-    else if (q - 2 < MI) f1.a[q - 2] = fa.read(cur, q - 2, 1);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  // stage k + 1 must have landed; stages k + 2 and k + 3 may be in flight
-  wait_vm<4 * LQ>();
-  meet();
+  for (int s = 0; s < 4; ++s) {
+    const Frags<MI>& now = f[s & 1];
+    Frags<MI>& then = f[(s + 1) & 1];
+    const char* from = s < 3 ? cur : nxt;
+    if (s == 3) {
+      // this wave's reads of cur are done, and its loads of nxt
+      __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
+      meet();
+    }
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    mma<T>(acc[q / 2][q % 2], f1.b[q % 2], f1.a[q / 2]);
-    if (q < 2) f0.b[q] = fb.read(nxt + G::HALF, q, 0);
-    else if (q - 2 < MI) f0.a[q - 2] = fa.read(nxt, q - 2, 0);
-    if (q >= Q - 2 * LQ) L.load(ldb, q - (Q - 2 * LQ));
-    __builtin_amdgcn_sched_barrier(0);
+    for (int q = 0; q < Q; ++q) {
+      mma<T>(acc[q / 2][q % 2], now.b[q % 2], now.a[q / 2]);
+      if (q < 2) then.b[q] = fb.read(from + G::HALF, q, (s + 1) & 3);
+      else if (q - 2 < MI) then.a[q - 2] = fa.read(from, q - 2, (s + 1) & 3);
+      if (s == 3) {
+#pragma unroll
+        for (int l = 0; l < 2 * LQ / Q; ++l) L.load(ldb, 2 * LQ / Q * q + l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 }
 
@@ -570,7 +583,6 @@ __device__ __forceinline__ void epilogue_inside(const f32x16 (&acc)[MI][2], cons
   constexpr int Q = 4 * JC;   // a lane's fours of columns in a patch
   constexpr bool HAS_BIAS = KIND == kLinear || KIND == kSlope;
   Raw4<T> bias[HAS_BIAS ? Q : 1] = {};
-  meet();   // every wave is past its reads of the stage that the patches take
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
     if constexpr (HAS_BIAS) {
@@ -633,23 +645,18 @@ template <typename T, int KIND, int ACT, int MI>
 __device__ __forceinline__ void epilogue_of(const f32x16 (&acc)[MI][2], const Product& p,
                                             int prob, int row0, int col0, bool inside,
                                             char* patch) {
-  if (inside) {
-    epilogue_inside<T, KIND, ACT, MI>(acc, p, prob, row0, col0, patch);
-  } else {
-    meet();   // as the waves whose blocks are inside
-    epilogue_edge<T, KIND, ACT, MI>(acc, p, prob, row0, col0);
-  }
+  if (inside) epilogue_inside<T, KIND, ACT, MI>(acc, p, prob, row0, col0, patch);
+  else epilogue_edge<T, KIND, ACT, MI>(acc, p, prob, row0, col0);
 }
 
 template <typename T, int KIND, int MI>
 __device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const Product& p, Tile t,
-                                         char* stage) {
+                                         char* patch) {
   typedef Geo<T, MI> G;
   constexpr int OUT = kind_dual(KIND) ? 32 : 64;   // a wave's result columns
   const int wave = uniform(fresh_tid() >> 6);
   const int row0 = uniform(t.tm * G::ROWS + (wave / G::WN) * (32 * MI));
   const int col0 = uniform((t.tn * G::WN + wave % G::WN) * OUT);
-  char* patch = stage + 4096 * wave;
   const bool inside = row0 + 32 * MI <= p.M && col0 + OUT <= p.N;
   if constexpr (kind_acts(KIND)) {
     switch (p.act) {
@@ -671,7 +678,7 @@ template <typename T, int KIND, int MI>
 __global__ __launch_bounds__(128 * MI) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void k_tile(TileArgs A) {
   typedef Geo<T, MI> G;
-  __shared__ __attribute__((aligned(16))) char smem[NBUF * G::STAGE];
+  __shared__ __attribute__((aligned(16))) char smem[2 * G::STAGE + 4096 * (2 * G::WN)];
   int t = blockIdx.x;
   if (A.xcd_chunk > 0) t = (t & 7) * A.xcd_chunk + (t >> 3);
   const int stride = gridDim.x;
@@ -683,16 +690,16 @@ void k_tile(TileArgs A) {
   LoadPos<T, KIND, MI> L;
   L.set(A, t, 0);
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < 2; ++s) {
 #pragma unroll
     for (int q = 0; q < 2 * LQ; ++q) L.load(la0 + s * G::STAGE, q);
     L.advance(A, stride);
   }
-  wait_vm<6 * LQ>();
+  wait_vm<2 * LQ>();
   meet();
   const FragOffs<T, MI, MI, kind_a_kr(KIND)> fa((wave / G::WN) * 32 * MI);
   const FragOffs<T, MI, 2, kind_b_kr(KIND)> fb((wave % G::WN) * 64);
-  int cb = 0;
+  int cb = 0;   // the current stage's buffer
   const int steps = (A.p.K + G::BK - 1) / G::BK * (KIND == kDx ? A.p.parts : 1);
   for (; t < A.total; t += stride) {
     f32x16 acc[MI][2];
@@ -704,21 +711,18 @@ void k_tile(TileArgs A) {
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     // the first stage's first fragments, again after an epilogue (whose
     // registers they would take)
-    Frags<MI> f0, f1;
+    Frags<MI> f[2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) f0.a[i] = fa.read(smem + cb * G::STAGE, i, 0);
+    for (int i = 0; i < MI; ++i) f[0].a[i] = fa.read(smem + cb * G::STAGE, i, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) f0.b[j] = fb.read(smem + cb * G::STAGE + G::HALF, j, 0);
+    for (int j = 0; j < 2; ++j) f[0].b[j] = fb.read(smem + cb * G::STAGE + G::HALF, j, 0);
     for (int k = 0; k < steps; ++k) {
-      const int nb = cb == NBUF - 1 ? 0 : cb + 1;
-      const int lb = cb == 0 ? NBUF - 1 : cb - 1;
-      step<T, KIND, MI>(acc, f0, f1, smem + cb * G::STAGE, smem + nb * G::STAGE,
-                        la0 + lb * G::STAGE, L, fa, fb);
+      step<T, KIND, MI>(acc, f, smem + cb * G::STAGE, smem + (cb ^ 1) * G::STAGE,
+                        la0 + cb * G::STAGE, L, fa, fb);
       L.advance(A, stride);
-      cb = nb;
+      cb ^= 1;
     }
-    epilogue<T, KIND, MI>(acc, A.p, decode_tile(A, uniform(t)),
-                          smem + (cb == 0 ? NBUF - 1 : cb - 1) * G::STAGE);
+    epilogue<T, KIND, MI>(acc, A.p, decode_tile(A, uniform(t)), smem + 2 * G::STAGE + 4096 * wave);
   }
   wait_vm<0>();   // loads past the last stage target this workgroup's LDS
 }
