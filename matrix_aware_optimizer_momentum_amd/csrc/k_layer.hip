@@ -59,32 +59,122 @@ __global__ __launch_bounds__(256) void k_lay_out(const T* p, int64_t ldp, int64_
 
 }  // namespace
 
-sm_status launch_product(const Product& p, hipStream_t s) {
-  using namespace layer;
-  if (few_tokens(p.kind, p.M)) {
-    prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : 1), s, 0.0);
-    launch_few(p, s);
-    prof_end(s);
-    return check_launch();
-  }
-  TileArgs a;
-  a.p = p;
-  const int cols = std::max(p.N, p.pad);
-  const int nprob = p.kind == kDw ? p.parts : 1, cus = cu_count();
-  auto tiles = [&](int mi) {
-    const int rows = 64 * mi, width = kind_dual(p.kind) ? 32 * mi : 64 * mi;
-    a.tiles_m = (p.M + rows - 1) / rows;
-    a.tiles_n = (cols + width - 1) / width;
-    a.per_prob = a.tiles_m * a.tiles_n;
-    a.total = a.per_prob * nprob;
-    return a.total;
+namespace {
+
+// How a product is launched: tiles of 64 mi rows, columns from `cut` on by a
+// second launch of small tiles, sums in `splits` shares.
+struct Plan {
+  int mi, splits, cut;
+};
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+int tile_rows(int mi) { return 64 * mi; }
+int tile_cols(int kind, int mi) { return kind_dual(kind) ? 32 * mi : 64 * mi; }
+
+Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
+  const int cus = cu_count();
+  const int nprob = kind == kDw ? parts : 1;
+  const int steps = ceil_div(K, dt == BF16 ? 64 : 32) * (kind == kDx ? parts : 1);
+  const int64_t large = (int64_t)ceil_div(M, tile_rows(4)) * ceil_div(N, tile_cols(kind, 4)) * nprob;
+  const int64_t small = (int64_t)ceil_div(M, tile_rows(2)) * ceil_div(N, tile_cols(kind, 2)) * nprob;
+  // us for a step of a large tile, of one small tile on a CU and of two, and
+  // around a tile
+  const double f = dt == BF16 ? 1.0 : 8.0;
+  const double t4 = 1.5 * f, t1 = 0.55 * f, t2 = 1.0 * f, c4 = 9.0, c2 = 6.0;
+  auto smalls = [&](int64_t n, double st) {   // n small tiles of st steps
+    return ceil_div(n, 2 * cus) > 1 || n > cus ? ceil_div(n, 2 * cus) * (st * t2 + c2)
+                                               : st * t1 + c2;
   };
-  const bool large = tiles(4) >= cus / 2;
-  const int grid = std::min(tiles(large ? 4 : 2), large ? cus : 2 * cus);
+  Plan best = {4, 1, N};
+  double least = ceil_div(large, cus) * (steps * t4 + c4);
+  auto consider = [&](Plan p, double us) {
+    if (us < least) least = us, best = p;
+  };
+  consider({2, 1, N}, smalls(small, steps));
+  for (int s = 2; s <= 16 && s * 2 <= steps; ++s) {
+    const double sums = (double)ceil_div(M, 128) * 128 * ceil_div(N, tile_cols(kind, 2)) * 128 *
+                        nprob * s;
+    consider({2, s, N}, smalls(small * s, (double)steps / s) + 5.0 + sums * 8.0 / 4.0e6);
+  }
+  if (nprob == 1 && large > cus) {   // whole rounds of large tiles, the rest by small ones
+    const int tm = ceil_div(M, tile_rows(4));
+    const int n1 = (int)(large / cus * cus / tm) * tile_cols(kind, 4);
+    if (n1 > 0 && n1 < N) {
+      const int64_t rest = (int64_t)ceil_div(M, 128) * ceil_div(N - n1, tile_cols(kind, 2));
+      consider({4, 1, n1}, large / cus * (steps * t4 + c4) + smalls(rest, steps) + 2.0);
+    }
+  }
+  return best;
+}
+
+layer::TileArgs tile_args(const Product& p, int mi, int splits) {
+  layer::TileArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.p = p;
+  a.tiles_m = ceil_div(p.M, tile_rows(mi));
+  a.tiles_n = ceil_div(std::max(p.N, p.pad), tile_cols(p.kind, mi));
+  a.per_prob = a.tiles_m * a.tiles_n;
+  a.splits = splits;
+  a.total = a.per_prob * (p.kind == kDw ? p.parts : 1) * splits;
+  a.rows = a.tiles_m * tile_rows(mi);
+  a.width = a.tiles_n * 64 * mi;
+  return a;
+}
+
+void launch_tiles(const Product& p, int mi, int splits, void* sums, hipStream_t s) {
+  using namespace layer;
+  TileArgs a = tile_args(p, mi, splits);
+  a.sums = static_cast<float*>(sums);
+  const int grid = std::min(a.total, mi == 4 ? cu_count() : 2 * cu_count());
   a.xcd_chunk = grid % 8 == 0 ? grid / 8 : 0;
+  if (p.dt == BF16) (mi == 4 ? launch_tile_bf16_4 : launch_tile_bf16_2)(a, grid, s);
+  else (mi == 4 ? launch_tile_f32_4 : launch_tile_f32_2)(a, grid, s);
+}
+
+}  // namespace
+
+size_t product_ws(int kind, int dt, int M, int N, int K, int parts) {
+  if (few_tokens(kind, M)) return 0;
+  const Plan plan = plan_product(kind, dt, M, N, K, parts);
+  if (plan.splits == 1) return 0;
+  Product p;
+  std::memset(&p, 0, sizeof(p));
+  p.kind = kind;
+  p.M = M;
+  p.N = N;
+  p.pad = (N + 7) / 8 * 8;
+  p.parts = parts;
+  const layer::TileArgs a = tile_args(p, plan.mi, plan.splits);
+  return (size_t)a.rows * a.width * 4 * (kind == kDw ? parts : 1) * plan.splits;
+}
+
+sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
   prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : p.parts), s, 0.0);
-  if (p.dt == BF16) (large ? launch_tile_bf16_4 : launch_tile_bf16_2)(a, grid, s);
-  else (large ? launch_tile_f32_4 : launch_tile_f32_2)(a, grid, s);
+  if (few_tokens(p.kind, p.M)) {
+    layer::launch_few(p, s);
+  } else {
+    const Plan plan = plan_product(p.kind, p.dt, p.M, p.N, p.K, p.parts);
+    Product q = p;
+    q.N = std::min(p.N, plan.cut);
+    if (plan.cut < p.N && p.pad) q.pad = q.N;
+    launch_tiles(q, plan.mi, plan.splits, sums, s);
+    if (plan.cut < p.N) {
+      const int64_t size = (int64_t)dt_size(p.dt), at = plan.cut * size;
+      auto on = [](const void* m, int64_t bytes) {
+        return m ? static_cast<const char*>(m) + bytes : nullptr;
+      };
+      q = p;
+      q.N = p.N - plan.cut;
+      q.pad = p.pad ? p.pad - plan.cut : 0;
+      for (int i = 0; i < 2; ++i) {
+        q.b[i].p = on(p.b[i].p, kind_b_kr(p.kind) ? at : at * p.b[i].ld);
+        q.c[i] = const_cast<char*>(on(p.c[i], at));
+      }
+      q.bias = on(p.bias, at);
+      q.in.p = on(p.in.p, at);
+      launch_tiles(q, 2, 1, nullptr, s);
+    }
+  }
   prof_end(s);
   return check_launch();
 }

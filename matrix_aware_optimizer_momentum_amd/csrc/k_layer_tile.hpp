@@ -61,6 +61,12 @@ constexpr int ROW = 128;   // bytes of an operand row in a stage
 struct TileArgs {
   Product p;
   int tiles_m, tiles_n, per_prob, total, xcd_chunk;
+  // Of a product whose sums are split (splits > 1), each share of the stages
+  // is a tile of its own and leaves its float32 sums, of every row and column
+  // of the tiles (a gated layer's 32 of Wg and 32 of Wu in turn), to
+  // sums[share][product]: `rows` rows of `width`.
+  int splits, rows, width;
+  float* sums;
 };
 
 // ---------------------------------------------------------------- four results
@@ -391,13 +397,24 @@ __device__ __forceinline__ void mma(f32x16& acc, u32x4 a, u32x4 b) {
 // ---------------------------------------------------------------- tiles
 
 struct Tile {
-  int prob, tm, tn;
+  int share, prob, tm, tn;
 };
+template <int KIND>
 __device__ __forceinline__ Tile decode_tile(const TileArgs& A, int t) {
   Tile r;
-  r.prob = t / A.per_prob;
-  ns_tile_coords(t - r.prob * A.per_prob, A.tiles_m, A.tiles_n, 0, &r.tm, &r.tn);
+  const int q = t / A.per_prob;   // share by share, and in each problem by problem
+  const int probs = KIND == kDw ? A.p.parts : 1;
+  r.share = q / probs;
+  r.prob = q - r.share * probs;
+  ns_tile_coords(t - q * A.per_prob, A.tiles_m, A.tiles_n, 0, &r.tm, &r.tn);
   return r;
+}
+// The stages of a share: from..to - 1 of `all`.
+struct Stages {
+  int from, to;
+};
+__device__ __forceinline__ Stages stages_of(const TileArgs& A, int share, int all) {
+  return {(int)((int64_t)all * share / A.splits), (int)((int64_t)all * (share + 1) / A.splits)};
 }
 
 // Where the loads are: a stage of a tile (or of a part of its sums).
@@ -410,13 +427,17 @@ struct LoadPos {
   uint64_t abase, bbase;    // of the stage
   uint64_t astep, bstep;    // bytes from a stage to the next
   int left;                 // k that exist from the stage's first on
+  int todo;                 // stages of the tile from this one on
   int part, tile;
 
-  __device__ __forceinline__ void set(const TileArgs& A, int t, int q) {
+  static __device__ __forceinline__ int stages(const TileArgs& A) {   // of a part
+    return (A.p.K + G::BK - 1) / G::BK;
+  }
+  // Stage `from` of part q.
+  __device__ __forceinline__ void set(const TileArgs& A, const Tile& tl, int q, int from) {
     const Product& p = A.p;
-    t = uniform(t);
     q = uniform(q);
-    const Tile tl = decode_tile(A, t);
+    from = uniform(from);
     const Operand oa = (KIND == kDw ? tl.prob : KIND == kDx ? q : 0) ? p.a[1] : p.a[0];
     Operand ob = (KIND == kDx && q) ? p.b[1] : p.b[0];
     if constexpr (DUAL)   // odd waves load Wu's rows
@@ -427,26 +448,38 @@ struct LoadPos {
     b.set(ob.ld, bn, p.N);
     abase = reinterpret_cast<uint64_t>(oa.p) + (uint64_t)((AKR ? am : am * oa.ld) * G::SIZE);
     bbase = reinterpret_cast<uint64_t>(ob.p) + (uint64_t)((BKR ? bn : bn * ob.ld) * G::SIZE);
-    abase = uniform64(abase);
-    bbase = uniform64(bbase);
     astep = uniform64((uint64_t)(AKR ? G::BK * oa.ld * G::SIZE : ROW));
     bstep = uniform64((uint64_t)(BKR ? G::BK * ob.ld * G::SIZE : ROW));
-    left = p.K;
+    abase = uniform64(abase + from * astep);
+    bbase = uniform64(bbase + from * bstep);
+    left = p.K - from * G::BK;
     part = q;
+  }
+  __device__ __forceinline__ void set_tile(const TileArgs& A, int t) {
+    t = uniform(t);
+    const Tile tl = decode_tile<KIND>(A, t);
+    const int each = stages(A);
+    const Stages s = stages_of(A, tl.share, each * (KIND == kDx ? A.p.parts : 1));
+    const int q = KIND == kDx && s.from >= each ? 1 : 0;
+    set(A, tl, q, s.from - q * each);
+    todo = s.to - s.from;
     tile = t;
   }
   // The next stage: of this part, of the next part, of the workgroup's next
   // tile; past the last one it stays (that stage is then loaded again, into
   // buffers that nobody multiplies).
   __device__ __forceinline__ void advance(const TileArgs& A, int stride) {
-    if (left > G::BK) {
-      left -= G::BK;
-      abase += astep;
-      bbase += bstep;
-    } else {
-      const bool more = KIND == kDx && part + 1 < A.p.parts;
-      const int t = more ? tile : tile + stride;
-      if (t < A.total) set(A, t, more ? part + 1 : 0);
+    if (todo > 1) {
+      --todo;
+      if (KIND != kDx || left > G::BK) {
+        left -= G::BK;
+        abase += astep;
+        bbase += bstep;
+      } else {
+        set(A, decode_tile<KIND>(A, tile), 1, 0);
+      }
+    } else if (tile + stride < A.total) {
+      set_tile(A, tile + stride);
     }
   }
   // Load q of this wave (A's, then B's) into the stage buffer at LDS address buf.
@@ -650,9 +683,20 @@ __device__ __forceinline__ void epilogue_of(const f32x16 (&acc)[MI][2], const Pr
 }
 
 template <typename T, int KIND, int MI>
-__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const Product& p, Tile t,
+__device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const TileArgs& A, Tile t,
                                          char* patch) {
   typedef Geo<T, MI> G;
+  const Product& p = A.p;
+  if (A.splits > 1) {
+    Product s;
+    s.c[0] = A.sums + (int64_t)(t.share * (KIND == kDw ? p.parts : 1) + t.prob) * A.rows * A.width;
+    s.ldc[0] = A.width;
+    const int wave = uniform(fresh_tid() >> 6);
+    epilogue_inside<float, kDx, SM_ACT_NONE, MI>(acc, s, 0,
+                                                 t.tm * G::ROWS + (wave / G::WN) * (32 * MI),
+                                                 (t.tn * G::WN + wave % G::WN) * 64, patch);
+    return;
+  }
   constexpr int OUT = kind_dual(KIND) ? 32 : 64;   // a wave's result columns
   const int wave = uniform(fresh_tid() >> 6);
   const int row0 = uniform(t.tm * G::ROWS + (wave / G::WN) * (32 * MI));
@@ -688,7 +732,7 @@ void k_tile(TileArgs A) {
       (uint32_t)uniform((int)(uint32_t)(size_t)(__attribute__((address_space(3))) void*)smem) +
       1024u * LQ * wave;
   LoadPos<T, KIND, MI> L;
-  L.set(A, t, 0);
+  L.set_tile(A, t);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -700,8 +744,10 @@ void k_tile(TileArgs A) {
   const FragOffs<T, MI, MI, kind_a_kr(KIND)> fa((wave / G::WN) * 32 * MI);
   const FragOffs<T, MI, 2, kind_b_kr(KIND)> fb((wave % G::WN) * 64);
   int cb = 0;   // the current stage's buffer
-  const int steps = (A.p.K + G::BK - 1) / G::BK * (KIND == kDx ? A.p.parts : 1);
+  const int all = L.stages(A) * (KIND == kDx ? A.p.parts : 1);
   for (; t < A.total; t += stride) {
+    const Stages mine = stages_of(A, decode_tile<KIND>(A, uniform(t)).share, all);
+    const int steps = uniform(mine.to - mine.from);
     f32x16 acc[MI][2];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -722,17 +768,64 @@ void k_tile(TileArgs A) {
       L.advance(A, stride);
       cb ^= 1;
     }
-    epilogue<T, KIND, MI>(acc, A.p, decode_tile(A, uniform(t)), smem + 2 * G::STAGE + 4096 * wave);
+    epilogue<T, KIND, MI>(acc, A, decode_tile<KIND>(A, uniform(t)),
+                          smem + 2 * G::STAGE + 4096 * wave);
   }
   wait_vm<0>();   // loads past the last stage target this workgroup's LDS
 }
 
+// A split product's shares joined, and its results made of them: one thread
+// takes four columns of a row, the shares in order.
+template <typename T, int KIND, int ACT>
+__device__ __forceinline__ void join4(const TileArgs& A, int prob, int row, int col) {
+  const Product& p = A.p;
+  const int probs = KIND == kDw ? p.parts : 1;
+  const int64_t size = (int64_t)A.rows * A.width;
+  const int at = kind_dual(KIND) ? col / 32 * 64 + col % 32 : col;
+  const float* s = A.sums + prob * size + (int64_t)row * A.width + at;
+  f32x4 g = {}, u = {};
+  for (int q = 0; q < A.splits; ++q, s += probs * size) {
+    g += *reinterpret_cast<const f32x4*>(s);
+    if constexpr (kind_dual(KIND)) u += *reinterpret_cast<const f32x4*>(s + 32);
+  }
+  finish4<T, KIND, ACT>(p, prob, row, col, g, u, load_bias<T, KIND>(p, col),
+                        load_in<T, KIND>(p, prob, row, col));
+}
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void k_join(TileArgs A, int fours) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int row = (int)(i / fours), col = 4 * (int)(i % fours), prob = blockIdx.y;
+  if (row >= A.p.M) return;
+  if constexpr (kind_acts(KIND)) {
+    switch (A.p.act) {
+#define SM_ACT(V) \
+  case V: join4<T, KIND, V>(A, prob, row, col); break;
+      SM_ACT(SM_ACT_NONE)
+      SM_ACT(SM_ACT_RELU)
+      SM_ACT(SM_ACT_SILU)
+      SM_ACT(SM_ACT_GELU)
+      SM_ACT(SM_ACT_GELU_TANH)
+#undef SM_ACT
+    }
+  } else {
+    join4<T, KIND, SM_ACT_NONE>(A, prob, row, col);
+  }
+}
+
 template <typename T, int MI>
 void launch_tile(const TileArgs& a, int grid, hipStream_t s) {
+  const int fours = (std::max(a.p.N, a.p.pad) + 3) / 4;
+  const dim3 join((unsigned)(((int64_t)a.p.M * fours + 255) / 256),
+                  a.p.kind == kDw ? a.p.parts : 1);
   constexpr int threads = Geo<T, MI>::THREADS;
   switch (a.p.kind) {
 #define SM_KIND(K) \
-  case K: hipLaunchKernelGGL((k_tile<T, K, MI>), dim3(grid), dim3(threads), 0, s, a); break;
+  case K: \
+    hipLaunchKernelGGL((k_tile<T, K, MI>), dim3(grid), dim3(threads), 0, s, a); \
+    if constexpr (MI == 2) { \
+      if (a.splits > 1) hipLaunchKernelGGL((k_join<T, K>), join, dim3(256), 0, s, a, fours); \
+    } \
+    break;
     SM_KIND(kLinear)
     SM_KIND(kSlope)
     SM_KIND(kGated)

@@ -45,7 +45,9 @@ inline bool few_tokens(int kind, int64_t T) {
 // Launches p.  Unless few_tokens, every operand's rows (as they are stored) are 16-byte aligned,
 // less than 2^31 / 256 bytes apart, and a multiple of 16 bytes long, or have
 // readable memory up to one, zeros if they run along k.
-sm_status launch_product(const Product& p, hipStream_t s);
+// sums: scratch of product_ws bytes, 256-byte aligned.
+size_t product_ws(int kind, int dt, int M, int N, int K, int parts);
+sm_status launch_product(const Product& p, void* sums, hipStream_t s);
 inline bool laid_out(const void* p, int64_t ld, int64_t len, int dt) {
   const int64_t size = (int64_t)dt_size(dt);
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && len * size % 16 == 0 &&

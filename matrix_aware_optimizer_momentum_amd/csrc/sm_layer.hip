@@ -155,7 +155,7 @@ sm_status check_layer(const sm_layer* lp, Call c) {
 // anew, of x from a checkpoint, and of dz.
 struct LayerWs {
   bool lay_x, lay_w, lay_w2, lay_dy;
-  size_t x, w, w2, dy, dz, dz2, bytes;
+  size_t x, w, w2, dy, dz, dz2, sums, bytes;   // sums: of a split product
   int64_t ldd, ldn;   // rows of d and of n entries
 };
 LayerWs layer_ws(const sm_layer& l, Call c) {
@@ -180,6 +180,21 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
   w.dy = take(w.lay_dy, l.T, w.ldn);
   w.dz = take(grad && again, l.T, w.ldn);
   w.dz2 = take(grad && is_gated(c), l.T, w.ldn);
+  const int T = (int)l.T, two = is_gated(c) ? 2 : 1;
+  w.sums = w.bytes;
+  size_t most = 0;
+  auto product = [&](int kind, int M, int N, int K, int parts) {
+    most = std::max(most, product_ws(kind, l.dt, M, N, K, parts));
+  };
+  if (!grad) {
+    product(is_gated(c) ? kGated : kLinear, T, l.n, l.d, 1);
+  } else {
+    if (again) product(is_gated(c) ? kGatedSlope : kSlope, T, l.n, l.d, 1);
+    if (l.dx) product(kDx, T, l.d, l.n, two);
+    const int dws = (l.dw ? 1 : 0) + (is_gated(c) && l.dw2 ? 1 : 0);
+    if (dws) product(kDw, l.n, l.d, T, dws);
+  }
+  w.bytes += (size_t)round_up((int64_t)most, 256);
   return w;
 }
 
@@ -277,7 +292,7 @@ sm_status run_forward(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hip
   if (c == kCallLinear) p.in = {l.residual, l.ldr};
   p.c[0] = l.y;
   p.ldc[0] = l.ldy;
-  return launch_product(p, s);
+  return launch_product(p, static_cast<char*>(ws) + w.sums, s);
 }
 
 sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipStream_t s) {
@@ -307,7 +322,7 @@ sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipSt
     p.pad = (int)w.ldn;
     o.dz[0] = {ws + w.dz, w.ldn};
     o.dz[1] = {ws + w.dz2, w.ldn};
-    SM_TRY(launch_product(p, s));
+    SM_TRY(launch_product(p, ws + w.sums, s));
   }
   if (l.dx) {
     Product p = product_of(l, kDx, o);
@@ -318,7 +333,7 @@ sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipSt
     p.a[1] = o.dz[1];
     p.c[0] = l.dx;
     p.ldc[0] = l.lddx;
-    SM_TRY(launch_product(p, s));
+    SM_TRY(launch_product(p, ws + w.sums, s));
   }
   if (l.dw || dw2) {
     Product p = product_of(l, kDw, o);
@@ -331,7 +346,7 @@ sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipSt
     if (l.dw) p.a[q] = o.dz[0], p.c[q] = l.dw, p.ldc[q++] = l.lddw;
     if (dw2) p.a[q] = o.dz[1], p.c[q] = dw2, p.ldc[q++] = l.lddw2;
     p.parts = q;
-    SM_TRY(launch_product(p, s));
+    SM_TRY(launch_product(p, ws + w.sums, s));
   }
   if (dbias)
     SM_TRY(launch_column_sums(o.dz[0].p, o.dz[0].ld, l.T, l.n, l.dt, dbias, l.accumulate, s));

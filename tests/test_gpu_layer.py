@@ -128,7 +128,8 @@ def test_whole_numbers_gated(gpu_lib, dt, shape, layout):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("T,d,n", [(2900, 2904, 2888), (2883, 2901, 2897), (4200, 72, 4104), (40, 4104, 4200)])
+@pytest.mark.parametrize("T,d,n", [(2900, 2904, 2888), (2883, 2901, 2897), (4200, 72, 4104), (4200, 4104, 72),
+                                   (40, 4104, 4200), (200, 4101, 1003)])
 def test_whole_numbers_large(gpu_lib, dt, T, d, n):
     """Enough rows and columns for the large tiles in every product; float64 on the GPU as the
     reference (whole numbers: exact there too)."""
