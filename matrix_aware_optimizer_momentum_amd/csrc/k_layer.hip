@@ -20,21 +20,60 @@ int cu_count() {
   return cache[dev];
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void k_column_sums(const T* dz, int64_t ld, int64_t rows, int n,
-                                                     T* out, int accumulate) {
-  __shared__ float red[256];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
-  float sum = 0.f;
-  if (col < n)
-    for (int64_t r = threadIdx.x >> 5; r < rows; r += 8) sum += Elem<T>::load(dz + r * ld + col);
-  red[threadIdx.x] = sum;
-  __syncthreads();
-  if (threadIdx.x >= 32 || col >= n) return;
+// Column sums over kSumRows rows: a wave takes every eighth row, a lane two
+// columns, eight rows in flight.  FINAL: those are all rows, and the sums go to
+// out (or onto it); else to sums[blockIdx.y][n] in float32.
+constexpr int kSumRows = 256, kSumCols = 128, kSumWaves = 8;
+template <typename T, bool FINAL>
+__global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const T* dz, int64_t ld,
+                                                                int64_t rows, int n, T* out,
+                                                                float* sums, int accumulate) {
+  __shared__ float red[kSumWaves][kSumCols];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * kSumCols + 2 * lane;
+  const int64_t r0 = (int64_t)blockIdx.y * kSumRows + wave;
+  const int64_t end = r0 - wave + kSumRows < rows ? r0 - wave + kSumRows : rows;
+  const bool one = col < n, two = col + 1 < n;
+  float a = 0.f, b = 0.f;
+  for (int64_t r = r0; r < end; r += 8 * kSumWaves) {
+    T v[8][2];
 #pragma unroll
-  for (int q = 1; q < 8; ++q) sum += red[threadIdx.x + 32 * q];
-  if (accumulate) sum += Elem<T>::load(out + col);
-  Elem<T>::store(out + col, sum);
+    for (int q = 0; q < 8; ++q) {
+      const int64_t at = (r + q * kSumWaves) * ld + col;
+      const bool in = r + q * kSumWaves < end;
+      v[q][0] = in && one ? dz[at] : T(0);
+      v[q][1] = in && two ? dz[at + 1] : T(0);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      a += Elem<T>::load(&v[q][0]);
+      b += Elem<T>::load(&v[q][1]);
+    }
+  }
+  red[wave][2 * lane] = a;
+  red[wave][2 * lane + 1] = b;
+  __syncthreads();
+  const int c = blockIdx.x * kSumCols + (int)threadIdx.x;
+  if (threadIdx.x >= kSumCols || c >= n) return;
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < kSumWaves; ++q) s += red[q][threadIdx.x];
+  if constexpr (FINAL) {
+    if (accumulate) s += Elem<T>::load(out + c);
+    Elem<T>::store(out + c, s);
+  } else {
+    sums[(int64_t)blockIdx.y * n + c] = s;
+  }
+}
+template <typename T>
+__global__ __launch_bounds__(64) void k_column_join(const float* sums, int shares, int n, T* out,
+                                                    int accumulate) {
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (c >= n) return;
+  float s = 0.f;
+  for (int q = 0; q < shares; ++q) s += sums[(int64_t)q * n + c];
+  if (accumulate) s += Elem<T>::load(out + c);
+  Elem<T>::store(out + c, s);
 }
 
 template <typename T>
@@ -77,10 +116,11 @@ Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
   const int steps = ceil_div(K, dt == BF16 ? 64 : 32) * (kind == kDx ? parts : 1);
   const int64_t large = (int64_t)ceil_div(M, tile_rows(4)) * ceil_div(N, tile_cols(kind, 4)) * nprob;
   const int64_t small = (int64_t)ceil_div(M, tile_rows(2)) * ceil_div(N, tile_cols(kind, 2)) * nprob;
-  // us for a step of a large tile, of one small tile on a CU and of two, and
-  // around a tile
-  const double f = dt == BF16 ? 1.0 : 8.0;
-  const double t4 = 1.5 * f, t1 = 0.55 * f, t2 = 1.0 * f, c4 = 9.0, c2 = 6.0;
+  // us, as measured: a step of a large tile, of one small tile on a CU and of
+  // two; around a tile; joining (the sums are written and read)
+  const bool b = dt == BF16;
+  const double t4 = b ? 1.5 : 8.5, t1 = b ? 0.75 : 3.0, t2 = b ? 1.0 : 4.5, c4 = 9.0, c2 = 6.0;
+  const double join = 3.0, per_sum = 8.0 / 8.0e6;
   auto smalls = [&](int64_t n, double st) {   // n small tiles of st steps
     return ceil_div(n, 2 * cus) > 1 || n > cus ? ceil_div(n, 2 * cus) * (st * t2 + c2)
                                                : st * t1 + c2;
@@ -94,7 +134,7 @@ Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
   for (int s = 2; s <= 16 && s * 2 <= steps; ++s) {
     const double sums = (double)ceil_div(M, 128) * 128 * ceil_div(N, tile_cols(kind, 2)) * 128 *
                         nprob * s;
-    consider({2, s, N}, smalls(small * s, (double)steps / s) + 5.0 + sums * 8.0 / 4.0e6);
+    consider({2, s, N}, smalls(small * s, (double)steps / s) + join + sums * per_sum);
   }
   if (nprob == 1 && large > cus) {   // whole rounds of large tiles, the rest by small ones
     const int tm = ceil_div(M, tile_rows(4));
@@ -191,12 +231,31 @@ sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int
   return check_launch();
 }
 
+size_t column_sums_ws(int64_t T, int n) {
+  return T > kSumRows ? (size_t)ceil_div(T, kSumRows) * n * 4 : 0;
+}
+
 sm_status launch_column_sums(const void* dz, int64_t ld, int64_t T, int n, int dt, void* out,
-                             int accumulate, hipStream_t s) {
+                             int accumulate, void* sums, hipStream_t s) {
+  const int shares = ceil_div(T, kSumRows);
+  const dim3 block(64 * kSumWaves);
+  float* f = static_cast<float*>(sums);
   prof_begin(SM_K_ACT8, (double)T * n * dt_size(dt), s);
-  SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_column_sums<E>, dim3((n + 31) / 32), dim3(256), 0, s,
-                                           static_cast<const E*>(dz), ld, T, n,
-                                           static_cast<E*>(out), accumulate));
+  // shares beyond a grid's height: launches of their own
+  for (int q = 0; q < shares; q += 65535) {
+    const dim3 grid((n + kSumCols - 1) / kSumCols, std::min(shares - q, 65535));
+    const int64_t r0 = (int64_t)q * kSumRows;
+    SM_DISPATCH_DT(dt, E, const E* z = static_cast<const E*>(dz) + r0 * ld;
+                   if (shares == 1)
+                     hipLaunchKernelGGL((k_column_sums<E, true>), grid, block, 0, s, z, ld, T, n,
+                                        static_cast<E*>(out), f, accumulate);
+                   else hipLaunchKernelGGL((k_column_sums<E, false>), grid, block, 0, s, z, ld,
+                                           T - r0, n, static_cast<E*>(out), f + (int64_t)q * n,
+                                           accumulate));
+  }
+  if (shares > 1)
+    SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_column_join<E>, dim3((n + 63) / 64), dim3(64), 0, s,
+                                             f, shares, n, static_cast<E*>(out), accumulate));
   prof_end(s);
   return check_launch();
 }

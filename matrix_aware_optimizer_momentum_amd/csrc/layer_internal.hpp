@@ -59,9 +59,10 @@ sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int
                          int64_t ld, hipStream_t s);
 
 // The sums over T rows of dz (ld entries apart) of n columns, in float32, to
-// out (added to it with accumulate).
+// out (added to it with accumulate).  sums: scratch of column_sums_ws bytes.
+size_t column_sums_ws(int64_t T, int n);
 sm_status launch_column_sums(const void* dz, int64_t ld, int64_t T, int n, int dt, void* out,
-                             int accumulate, hipStream_t s);
+                             int accumulate, void* sums, hipStream_t s);
 
 // rows x cols entries (row stride ld) set to 0.
 sm_status launch_zero(void* p, int64_t ld, int64_t rows, int cols, int dt, hipStream_t s);

@@ -193,6 +193,7 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
     if (l.dx) product(kDx, T, l.d, l.n, two);
     const int dws = (l.dw ? 1 : 0) + (is_gated(c) && l.dw2 ? 1 : 0);
     if (dws) product(kDw, l.n, l.d, T, dws);
+    if (!is_gated(c) && l.dbias) most = std::max(most, column_sums_ws(l.T, l.n));
   }
   w.bytes += (size_t)round_up((int64_t)most, 256);
   return w;
@@ -349,7 +350,8 @@ sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipSt
     SM_TRY(launch_product(p, ws + w.sums, s));
   }
   if (dbias)
-    SM_TRY(launch_column_sums(o.dz[0].p, o.dz[0].ld, l.T, l.n, l.dt, dbias, l.accumulate, s));
+    SM_TRY(launch_column_sums(o.dz[0].p, o.dz[0].ld, l.T, l.n, l.dt, dbias, l.accumulate,
+                              ws + w.sums, s));
   return SM_OK;
 }
 

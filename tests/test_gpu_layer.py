@@ -160,6 +160,20 @@ def test_whole_numbers_large(gpu_lib, dt, T, d, n):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,n", [(1, 1), (255, 129), (256, 3), (257, 130), (5000, 77), (300000, 5)])
+def test_bias_gradients_of_any_length(gpu_lib, dt, T, n):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    dy = torch.randint(-2, 3, (T, n), generator=gen, device="cuda").to(DT[dt])
+    x, w = torch.zeros(T, 1, device="cuda", dtype=DT[dt]), torch.zeros(n, 1, device="cuda", dtype=DT[dt])
+    old = torch.randint(-9, 10, (n,), generator=gen, device="cuda").to(DT[dt])
+    _, _, db = sm.linear_grad(dy, x, w, bias=old, need_dx=False, need_dw=False)
+    assert torch.equal(db, dy.double().sum(0).to(DT[dt]))
+    want = (dy.double().sum(0) + old.double()).to(DT[dt])
+    sm.linear_grad(dy, x, w, db=old, need_dx=False, need_dw=False, accumulate=True)
+    assert torch.equal(old, want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("T,d,n", [(5, 40, 24), (70, 130, 90), (200, 64, 300)])
 def test_accumulate_and_left_out_results(gpu_lib, dt, T, d, n):
     rng = np.random.default_rng(T)
