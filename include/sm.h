@@ -608,6 +608,7 @@ sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_
  * dx so, and dw, dw2 and dbias as the sums give.
  * ws: scratch of at least the matching *_ws(...) bytes, 256-byte aligned
  *   (may be NULL if that is 0); the query takes the call's own arguments.
+ *   Calls that may run at the same time need one each.
  * Errors: SM_ERR_ARG (null or misaligned pointers, a row length above its ld,
  *   both or neither of x and x8, a bad act, an overlap, no output wanted),
  *   SM_ERR_SHAPE (T < 0 or > 2^30, d or n < 1 or > 2^20, T d or T n >
@@ -677,12 +678,12 @@ enum {
   SM_K_VOTE_UPDATE = 7,  /* vote + W update                        bytes  */
   SM_K_LION = 8,         /* fused Lion interpolation/EMA/sign/pack bytes  */
   SM_K_POLAR_UPDATE = 9, /* W <- W - lr D                          bytes  */
-  SM_K_MISC = 10,        /* small finalize / copy kernels          bytes  */
+  SM_K_MISC = 10,        /* small finalize / copy / sum kernels    bytes  */
   SM_K_SPECTRAL = 11,    /* power-method passes (diagnostic)       bytes  */
   SM_K_ADAMW = 12,       /* AdamW step over a set                  bytes  */
   SM_K_GRAD_NORM = 13,   /* global gradient norm                   bytes  */
   SM_K_STATE8 = 14,      /* 8-bit states from float32 and back     bytes  */
-  SM_K_ACT8 = 15,        /* 8-bit checkpoints and back, layouts    bytes  */
+  SM_K_ACT8 = 15,        /* 8-bit checkpoints and back             bytes  */
   SM_K_LAYER = 16,       /* feed-forward layers' products          flops  */
   SM_K_NUM_KINDS = 17
 };

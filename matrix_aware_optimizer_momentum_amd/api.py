@@ -789,6 +789,9 @@ def state8_unpack(m8: torch.Tensor, v8: torch.Tensor, m_scale: torch.Tensor,
 
 
 # ------------------------------------------------------------------ feed-forward layers
+#
+# Plain calls, no autograd functions: a backward pass is a call of its own, which
+# writes where the steps read.
 
 @dataclass
 class Act8:
@@ -801,6 +804,9 @@ class Act8:
 def _rows(t: torch.Tensor, name: str, width: int, dtype, device, rows: Optional[int] = None):
     """(pointer, row stride) of t as a matrix [rows, width]: dtype, on device, rows contiguous,
     the leading dimensions at one stride."""
+    if t.is_contiguous() and t.dtype == dtype and t.is_cuda and t.device == device and \
+            t.dim() and t.shape[-1] == width and (rows is None or t.numel() == rows * width):
+        return t.data_ptr(), width   # the common case at a glance
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() < 1 or t.shape[-1] != width:
@@ -841,14 +847,15 @@ def act8_pack(x: torch.Tensor) -> Act8:
     _dt(x)
     if x.dim() < 1:
         raise ValueError("x must be [..., d]")
-    d = x.shape[-1]
-    ptr, ld = _rows(x, "x", d, x.dtype, x.device)
-    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty((*x.shape[:-1], (d + B.ACT8_BLOCK - 1) // B.ACT8_BLOCK), dtype=torch.uint8,
-                        device=x.device).view(torch.float8_e8m0fnu)
-    index = x.device.index
-    _call_on(index, "sm_act8_pack", ptr, ld, _dt(x), x.numel() // max(d, 1), d, codes.data_ptr(),
-             scale.data_ptr(), _stream_of(index))
+    shape, dev = x.shape, x.device
+    d = shape[-1]
+    ptr, ld = _rows(x, "x", d, x.dtype, dev)
+    codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((*shape[:-1], -(-d // B.ACT8_BLOCK)), dtype=torch.float8_e8m0fnu,
+                        device=dev)
+    index = dev.index
+    _call_on(index, "sm_act8_pack", ptr, ld, _DT[x.dtype], x.numel() // max(d, 1), d,
+             codes.data_ptr(), scale.data_ptr(), _stream_of(index))
     return Act8(codes, scale)
 
 
@@ -903,8 +910,7 @@ class _LayerCall:
         if t is not None:
             ptr, ld = _rows(t, name, width, self.dtype, self.device, rows)
             setattr(self.c, field, ptr)
-            ld_name = {"residual": "ldr"}.get(field, "ld" + field)
-            setattr(self.c, ld_name, ld)
+            setattr(self.c, "ldr" if field == "residual" else "ld" + field, ld)
 
     def weights(self, field, t, name=None):
         if t is not None and tuple(t.shape) != (self.n, self.d):
@@ -932,8 +938,8 @@ class _LayerCall:
             self.inputs("x", x)
 
     def __call__(self, name: str, ws: Optional[torch.Tensor]):
-        need = ctypes.c_size_t(0)
-        B.check(getattr(B.lib(), name + "_ws")(ctypes.byref(self.c), ctypes.byref(need)), name)
+        need, c, index = ctypes.c_size_t(0), ctypes.byref(self.c), self.device.index
+        _call_on(index, name + "_ws", c, ctypes.byref(need))
         size = need.value
         if ws is None:
             ws = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
@@ -943,9 +949,7 @@ class _LayerCall:
                 raise ValueError("ws must be on the tensors' device")
             if ws.numel() * ws.element_size() < size:
                 raise ValueError("workspace too small")
-        index = self.device.index
-        _call_on(index, name, ctypes.byref(self.c), ws.data_ptr() if size else None, size,
-                 _stream_of(index))
+        _call_on(index, name, c, ws.data_ptr() if size else None, size, _stream_of(index))
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,

@@ -6,7 +6,8 @@
 // float32) and 8 bytes of codes.  A workgroup takes one or four units of 64
 // blocks, all of whose loads are in flight before the first is used.  Rows and columns
 // come from one scalar division a workgroup: a division per lane in 64 bits
-// cost more than the memory (8192 x 4096 bf16: 44 us with it, 22 without).
+// cost more than the memory (pack of 8192 x 4096 bf16: 44 us with it).  Measured:
+// that pack 16.5 us (6.2 TB/s), unpack of 8192 x 11008 to bf16 39 us (7.0).
 #include "layer_internal.hpp"
 
 namespace sm {
@@ -284,22 +285,28 @@ __global__ __launch_bounds__(kThreads) void k_act8_unpack(const uint8_t* x8, con
   }
 }
 
-// Stores past what the caches can keep are non-temporal.
-constexpr double kStreamBytes = 256.0 * 1024 * 1024;
 // Blocks from which a workgroup takes four units: 256 workgroups of them.
 constexpr int64_t kManyBlocks = 256 * 4 * kBlocks;
+// A checkpoint is read in the backward pass: its stores are non-temporal (8192
+// x 4096 bf16: 16.5 us, 20.7 cacheable).  Its values are used next, so theirs
+// are cacheable up to what the Infinity Cache can keep.
+constexpr double kStreamBytes = 256.0 * 1024 * 1024;
 
 }  // namespace
 
-// Launches kernel<E, units, non-temporal> over rows x blocks blocks.
-#define SM_ACT8_LAUNCH(KERNEL, STREAM, ...)                                                           \
-  do {                                                                                        \
-    const int64_t n = T * blocks;                                                             \
-    const bool many = n >= kManyBlocks, nt = bytes > STREAM;                            \
-    const dim3 grid((unsigned)((n + (many ? 4 : 1) * kBlocks - 1) / ((many ? 4 : 1) * kBlocks))); \
-    if (!many) hipLaunchKernelGGL((KERNEL<E, 1, false>), grid, dim3(kThreads), 0, s, __VA_ARGS__); \
-    else if (!nt) hipLaunchKernelGGL((KERNEL<E, 4, false>), grid, dim3(kThreads), 0, s, __VA_ARGS__); \
-    else hipLaunchKernelGGL((KERNEL<E, 4, true>), grid, dim3(kThreads), 0, s, __VA_ARGS__);   \
+// Launches KERNEL<E, units, non-temporal> over T x blocks blocks.
+#define SM_ACT8_LAUNCH(KERNEL, STREAM, ...)                                              \
+  do {                                                                                   \
+    const int64_t n = T * blocks;                                                        \
+    const bool many = n >= kManyBlocks;                                                  \
+    const int group = (many ? 4 : 1) * kBlocks;                                          \
+    const dim3 grid((unsigned)((n + group - 1) / group)), block(kThreads);               \
+    if (!many)                                                                           \
+      hipLaunchKernelGGL((KERNEL<E, 1, false>), grid, block, 0, s, __VA_ARGS__);         \
+    else if (!(STREAM))                                                                  \
+      hipLaunchKernelGGL((KERNEL<E, 4, false>), grid, block, 0, s, __VA_ARGS__);         \
+    else                                                                                 \
+      hipLaunchKernelGGL((KERNEL<E, 4, true>), grid, block, 0, s, __VA_ARGS__);          \
   } while (0)
 
 sm_status launch_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int d, uint8_t* x8,
@@ -307,7 +314,7 @@ sm_status launch_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int d,
   const int blocks = (d + SM_ACT8_BLOCK - 1) / SM_ACT8_BLOCK;
   const double bytes = (double)T * (d * (1.0 + dt_size(dt)) + blocks);
   prof_begin(SM_K_ACT8, bytes, s);
-  SM_DISPATCH_DT(dt, E, SM_ACT8_LAUNCH(k_act8_pack, 0.0, static_cast<const E*>(x), ldx, T, blocks, d,
+  SM_DISPATCH_DT(dt, E, SM_ACT8_LAUNCH(k_act8_pack, true, static_cast<const E*>(x), ldx, T, blocks, d,
                                        x8, scale));
   prof_end(s);
   return check_launch();
@@ -318,7 +325,7 @@ sm_status launch_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, in
   const int blocks = (d + SM_ACT8_BLOCK - 1) / SM_ACT8_BLOCK;
   const double bytes = (double)T * (d * (1.0 + dt_size(dt)) + blocks);
   prof_begin(SM_K_ACT8, bytes, s);
-  SM_DISPATCH_DT(dt, E, SM_ACT8_LAUNCH(k_act8_unpack, kStreamBytes, x8, scale, T, blocks, d,
+  SM_DISPATCH_DT(dt, E, SM_ACT8_LAUNCH(k_act8_unpack, bytes > kStreamBytes, x8, scale, T, blocks, d,
                                        static_cast<E*>(x), ldx, pad));
   prof_end(s);
   return check_launch();

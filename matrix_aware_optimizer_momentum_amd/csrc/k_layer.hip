@@ -85,15 +85,37 @@ __global__ __launch_bounds__(256) void k_zero(T* p, int64_t ld, int64_t rows, in
   }
 }
 
-// rows x cols entries to rows x ld ones, zeros behind them.
+// rows x cols entries to rows x ld ones (ld a multiple of 8), zeros behind
+// them: a thread takes 8, read at once where they exist at whatever alignment,
+// its row by one scalar division a workgroup and one in 32 bits.
 template <typename T>
 __global__ __launch_bounds__(256) void k_lay_out(const T* p, int64_t ldp, int64_t rows, int cols,
                                                  T* out, int64_t ld) {
-  const int64_t n = rows * ld;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / ld, c = i - r * ld;
-    out[i] = c < cols ? p[r * ldp + c] : T(0);
+  constexpr int N = sizeof(T) / 2;   // 16-byte pieces
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef u32x4 V __attribute__((aligned(2)));
+  const int per_row = (int)(ld / 8);
+  const int64_t first = (int64_t)blockIdx.x * 256;
+  const int64_t row0 = first / per_row;
+  const uint32_t at = (uint32_t)(first - row0 * per_row) + threadIdx.x;
+  const int64_t row = row0 + at / (uint32_t)per_row;
+  if (row >= rows) return;
+  const int col = 8 * (int)(at % (uint32_t)per_row);
+  const T* q = p + row * ldp + col;
+  u32x4 v[N] = {};
+  if (col + 8 <= cols) {
+#pragma unroll
+    for (int h = 0; h < N; ++h) v[h] = reinterpret_cast<const V*>(q)[h];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e) {
+      if (col + e >= cols) continue;
+      if constexpr (sizeof(T) == 2) v[0][e >> 1] |= (uint32_t)q[e] << (16 * (e & 1));
+      else v[e >> 2][e & 3] = __float_as_uint(q[e]);
+    }
   }
+#pragma unroll
+  for (int h = 0; h < N; ++h) reinterpret_cast<u32x4*>(out + row * ld + col)[h] = v[h];
 }
 
 }  // namespace
@@ -188,8 +210,21 @@ size_t product_ws(int kind, int dt, int M, int N, int K, int parts) {
   return (size_t)a.rows * a.width * 4 * (kind == kDw ? parts : 1) * plan.splits;
 }
 
+// Operands read once, results written once (read first if they are added to).
+static double product_bytes(const Product& p) {
+  const double a = (double)p.M * p.K, b = (double)p.N * p.K, c = (double)p.M * p.N;
+  double n = a * p.parts + b + c;
+  if (kind_dual(p.kind)) n += b;
+  if (p.kind == kGatedSlope) n += c;
+  if (p.kind == kDx && p.parts == 2) n += b;
+  if (p.kind == kDw) n += c * (p.parts * (p.accumulate ? 2 : 1) - 1);
+  if (p.in.p) n += c;
+  return n * dt_size(p.dt);
+}
+
 sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
-  prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : p.parts), s, 0.0);
+  prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : p.parts), s,
+             product_bytes(p));
   if (few_tokens(p.kind, p.M)) {
     layer::launch_few(p, s);
   } else {
@@ -221,10 +256,9 @@ sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
 
 sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int dt, void* out,
                          int64_t ld, hipStream_t s) {
-  const int64_t n = rows * ld;
-  const int grid = (int)std::min<int64_t>(4096, (n + 255) / 256);
-  prof_begin(SM_K_ACT8, 2.0 * n * dt_size(dt), s);
-  SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_lay_out<E>, dim3(grid), dim3(256), 0, s,
+  const int64_t n = rows * (ld / 8);
+  prof_begin(SM_K_MISC, 16.0 * n * dt_size(dt), s);
+  SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_lay_out<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
                                            static_cast<const E*>(p), ldp, rows, cols,
                                            static_cast<E*>(out), ld));
   prof_end(s);
@@ -240,7 +274,7 @@ sm_status launch_column_sums(const void* dz, int64_t ld, int64_t T, int n, int d
   const int shares = ceil_div(T, kSumRows);
   const dim3 block(64 * kSumWaves);
   float* f = static_cast<float*>(sums);
-  prof_begin(SM_K_ACT8, (double)T * n * dt_size(dt), s);
+  prof_begin(SM_K_MISC, (double)T * n * dt_size(dt), s);
   // shares beyond a grid's height: launches of their own
   for (int q = 0; q < shares; q += 65535) {
     const dim3 grid((n + kSumCols - 1) / kSumCols, std::min(shares - q, 65535));
@@ -263,7 +297,7 @@ sm_status launch_column_sums(const void* dz, int64_t ld, int64_t T, int n, int d
 sm_status launch_zero(void* p, int64_t ld, int64_t rows, int cols, int dt, hipStream_t s) {
   const int64_t n = rows * cols;
   const int grid = (int)std::min<int64_t>(4096, (n + 255) / 256);
-  prof_begin(SM_K_ACT8, (double)n * dt_size(dt), s);
+  prof_begin(SM_K_MISC, (double)n * dt_size(dt), s);
   SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_zero<E>, dim3(grid), dim3(256), 0, s,
                                            static_cast<E*>(p), ld, rows, cols));
   prof_end(s);

@@ -38,7 +38,9 @@ struct Product {
   int accumulate;     // kDw
 };
 
-// The kernel for few tokens takes the product, operands of any alignment.
+// The kernel for few tokens takes the product, operands of any alignment.  (us
+// by it / by tiles: 17 tokens, gated 4096 x 11008 44.6 / 45.7, linear 11008 x
+// 4096 26.7 / 32.4; 32 tokens 49.5 / 45.4, 31.7 / 34.0.)
 inline bool few_tokens(int kind, int64_t T) {
   return (kind == kLinear || kind == kGated) && T <= 32;
 }

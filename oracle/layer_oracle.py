@@ -76,8 +76,8 @@ def act(name, z):
         return z * expit(z)
     if name == "gelu":
         return z * 0.5 * erfc(-z / np.sqrt(2.0))
-    if name == "gelu_tanh":
-        return 0.5 * z * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+    if name == "gelu_tanh":   # (1 + tanh(u)) / 2, without its cancellation at negative u
+        return z * expit(2 * np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3))
     return z
 
 
@@ -89,9 +89,9 @@ def slope(name, z):
     if name == "gelu":
         return 0.5 * (1 + erf(z / np.sqrt(2.0))) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
     if name == "gelu_tanh":
-        c = np.sqrt(2 / np.pi)
-        t = np.tanh(c * (z + 0.044715 * z ** 3))
-        return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
+        c = 2 * np.sqrt(2 / np.pi)
+        u = c * (z + 0.044715 * z ** 3)
+        return expit(u) * (1 + z * expit(-u) * c * (1 + 3 * 0.044715 * z * z))
     return np.ones_like(z)
 
 

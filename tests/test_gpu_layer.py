@@ -322,6 +322,43 @@ def test_gradients_against_differences(gpu_lib, name):
           lambda x, w, b: float(np.sum(dy * L.linear(x, w, b, name))))
 
 
+@pytest.mark.parametrize("name", L.ACTS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_activations_over_their_whole_range(gpu_lib, dt, name):
+    """Through a 1 x 1 weight of 1, so that z is x.  An exponent's argument (z, z^2 / 2, 2u) is off
+    by a few 2^-24 of it, and the value by as much times itself: 2^-20 (1 + argument) of the value
+    covers that, down to where e^-arg leaves float32's range (1 / (1 + e^88) is 6e-39 or 0, times
+    |z| <= 15 there: 1e-37, and |z| times that in h); a slope by 2^-19 (1 + |z|) (up to 20, where it no longer changes) of 1.  Finite z
+    give finite results, however large."""
+    z = np.concatenate([np.linspace(-30, 30, 6001), [0.0, -0.0, 1e-30, -1e-30, 1e4, -1e4, 1e10, -1e10,
+                                                     1e19, -1e19, 1e30, -1e30, 3e38, -3e38]])
+    x = torch.from_numpy(z).to(DT[dt]).cuda()[:, None]
+    z = np64(x)[:, 0]
+    w = torch.ones(1, 1, dtype=DT[dt], device="cuda")
+    with np.errstate(over="ignore"):
+        cut = np.clip(z, -1e4, 1e4)   # the oracle's own cubes stay finite
+        want = np.where(np.abs(z) <= 1e4, L.act(name, cut), z if name == "none" else np.maximum(z, 0))
+        arg = {"gelu": cut ** 2, "gelu_tanh": 1.6 * np.abs(cut + 0.044715 * cut ** 3)}.get(name, np.abs(cut))
+    half = HALF[dt]
+    got = np64(sm.linear(x, w, act=ACT[name]))[:, 0]
+    assert np.isfinite(got).all()
+    assert np.all(np.abs(got - want) <= (2.0 ** -20 * (1 + np.minimum(arg, 200)) + half) * np.abs(want) + 1e-37)
+    dx, _, db = sm.linear_grad(torch.ones_like(x), x, w, bias=torch.zeros(1, dtype=DT[dt], device="cuda"),
+                               act=ACT[name], need_dw=False)
+    slope = np64(dx)[:, 0]
+    want = L.slope(name, cut)
+    assert np.isfinite(slope).all()
+    assert np.all(np.abs(slope - want) <= 2.0 ** -19 * (1 + np.minimum(np.abs(z), 20)) + 2 * half * np.abs(want))
+    h = np64(sm.gated(x, w, torch.ones_like(w), act=ACT[name]))[:, 0]   # act(z) z
+    ok = np.abs(z) <= 1e4
+    want = L.act(name, cut) * cut
+    assert np.all((np.abs(h - want) <= (2.0 ** -19 * (1 + np.minimum(arg, 200)) + half) * np.abs(want)
+                   + 1e-37 * (1 + np.abs(z)))[ok])
+    x = torch.full_like(x[:1], float("nan"))
+    assert sm.linear(x, w, act=ACT[name]).isnan().all()
+    assert sm.linear_grad(torch.ones_like(x), x, w, act=ACT[name], need_dw=False)[0].isnan().all() or name == "none"
+
+
 # ---------------------------------------------------------------- 8-bit checkpoints
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -527,6 +564,84 @@ def test_the_same_call_gives_the_same_bits(gpu_lib):
             again = [*sm.gated_grad(dy, x, wg, wu), sm.gated(x, wg, wu),
                      *sm.linear_grad(dy, x, wg, bias=b, act=sm.ACT_GELU)]
             assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
+def test_two_streams_at_once_and_graphs_that_share_a_workspace(gpu_lib):
+    gen = torch.Generator().manual_seed(12)
+    t = lambda *s: torch.randn(*s, generator=gen).bfloat16().cuda()
+    T, d, n = 300, 520, 264          # products with split sums: all scratch is in use
+    a = [t(T, n), t(T, d), t(n, d), t(n, d)]
+    b = [t(T, n), t(T, d), t(n, d), t(n, d)]
+    want = [[v.clone() for v in sm.gated_grad(*q)] for q in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, q in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                got.append(sm.gated_grad(*q))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, w in zip(got, want) for p, q in zip(g, w))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for q in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(sm.gated_grad(*q, ws=ws))
+        graphs.append(g)
+    for _ in range(3):               # one after the other on one stream
+        for g in graphs:
+            g.replay()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for g, w in zip(outs, want) for p, q in zip(g, w))
+
+
+def test_a_workspace_too_small_for_the_call(gpu_lib):
+    x, w, dy = (torch.randn(*s, device="cuda") for s in ((300, 520), (264, 520), (300, 264)))
+    with pytest.raises(ValueError, match="workspace too small"):
+        sm.gated_grad(dy, x, w, w, ws=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+
+
+def test_offsets_beyond_32_bits(gpu_lib):
+    """An input of 4.6 GB: its last rows, read along k and across it, and its checkpoint."""
+    T, d, n = 70001, 32776, 24
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    f = lambda top, *s: torch.randint(-top, top + 1, s, generator=gen, device="cuda",
+                                      dtype=torch.int8).bfloat16()
+    x, w, dy = f(1, T, d), f(1, n, d), f(1, T, n)
+    y = sm.linear(x, w)
+    dx, dw, _ = sm.linear_grad(dy, x, w)
+    kept = sm.act8_pack(x)
+    dw8 = sm.linear_grad(dy, kept, w, need_dx=False)[1]
+    assert torch.equal(dw8, dw)      # whole numbers up to 1 are exact in 8 bits
+    del dw8
+    sums = torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    W = w.double()
+    for r in range(0, T, 10000):
+        X, D = x[r:r + 10000].double(), dy[r:r + 10000].double()
+        assert torch.equal(y[r:r + 10000], (X @ W.T).bfloat16())
+        assert torch.equal(dx[r:r + 10000], (D @ W).bfloat16())
+        sums += D.T @ X
+    assert torch.equal(dw, sums.bfloat16())
+    del dx, X, D
+    assert torch.equal(sm.act8_unpack(kept, torch.bfloat16), x)
+
+
+def test_rows_far_apart(gpu_lib):
+    """Rows 32 MB apart (laid out before they are multiplied), results as well."""
+    T, d, n, ld = 40, 24, 40, 1 << 24
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    f = lambda *s: torch.randint(-2, 3, s, generator=gen, device="cuda").bfloat16()
+    wide = torch.zeros(T, ld, dtype=torch.bfloat16, device="cuda")
+    x, out, dx = wide[:, :d], wide[:, 100:100 + n], wide[:, 5000:5000 + d]
+    x.copy_(f(T, d))
+    w, dy = f(n, d), f(T, n)
+    sm.linear(x, w, out=out)
+    assert torch.equal(out.double(), (x.double() @ w.double().T).bfloat16().double())
+    _, dw, _ = sm.linear_grad(dy, x, w, dx=dx)
+    assert torch.equal(dx.double(), (dy.double() @ w.double()).bfloat16().double())
+    assert torch.equal(dw.double(), (dy.double().T @ x.double()).bfloat16().double())
 
 
 # ---------------------------------------------------------------- together
