@@ -85,23 +85,23 @@ __global__ __launch_bounds__(256) void k_zero(T* p, int64_t ld, int64_t rows, in
   }
 }
 
-// rows x cols entries to rows x ld ones (ld a multiple of 8), zeros behind
-// them: a thread takes 8, read at once where they exist at whatever alignment,
-// its row by one scalar division a workgroup and one in 32 bits.
+// A matrix a launch row (blockIdx.y): a thread takes 8 entries of the copy, read at
+// once where they exist at whatever alignment, its row by one scalar division a workgroup and one in 32 bits.
 template <typename T>
-__global__ __launch_bounds__(256) void k_lay_out(const T* p, int64_t ldp, int64_t rows, int cols,
-                                                 T* out, int64_t ld) {
+__global__ __launch_bounds__(256) void k_lay_out(LayOuts all) {
   constexpr int N = sizeof(T) / 2;   // 16-byte pieces
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   typedef u32x4 V __attribute__((aligned(2)));
-  const int per_row = (int)(ld / 8);
+  const LayOut& m = all.m[blockIdx.y];
+  const int cols = m.cols;
+  const int per_row = (int)(m.ld / 8);
   const int64_t first = (int64_t)blockIdx.x * 256;
   const int64_t row0 = first / per_row;
   const uint32_t at = (uint32_t)(first - row0 * per_row) + threadIdx.x;
   const int64_t row = row0 + at / (uint32_t)per_row;
-  if (row >= rows) return;
+  if (row >= m.rows) return;
   const int col = 8 * (int)(at % (uint32_t)per_row);
-  const T* q = p + row * ldp + col;
+  const T* q = static_cast<const T*>(m.p) + row * m.ldp + col;
   u32x4 v[N] = {};
   if (col + 8 <= cols) {
 #pragma unroll
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void k_lay_out(const T* p, int64_t ldp, int64_
     }
   }
 #pragma unroll
-  for (int h = 0; h < N; ++h) reinterpret_cast<u32x4*>(out + row * ld + col)[h] = v[h];
+  for (int h = 0; h < N; ++h) reinterpret_cast<u32x4*>(static_cast<T*>(m.out) + row * m.ld + col)[h] = v[h];
 }
 
 }  // namespace
@@ -139,9 +139,11 @@ Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
   const int64_t large = (int64_t)ceil_div(M, tile_rows(4)) * ceil_div(N, tile_cols(kind, 4)) * nprob;
   const int64_t small = (int64_t)ceil_div(M, tile_rows(2)) * ceil_div(N, tile_cols(kind, 2)) * nprob;
   // us, as measured: a step of a large tile, of one small tile on a CU and of
-  // two; around a tile; joining (the sums are written and read)
+  // two, of up to two least ones; around a tile; joining (the sums
+  // are written and read)
   const bool b = dt == BF16;
-  const double t4 = b ? 1.5 : 8.5, t1 = b ? 0.75 : 3.0, t2 = b ? 1.0 : 4.5, c4 = 9.0, c2 = 6.0;
+  const double t4 = b ? 1.5 : 8.0, t1 = b ? 0.75 : 2.25, t2 = b ? 1.0 : 4.0, c4 = 9.0, c2 = 6.0;
+  const double u1 = b ? 0.4 : 1.4, c1 = 5.0;
   const double join = 3.0, per_sum = 8.0 / 8.0e6;
   auto smalls = [&](int64_t n, double st) {   // n small tiles of st steps
     return ceil_div(n, 2 * cus) > 1 || n > cus ? ceil_div(n, 2 * cus) * (st * t2 + c2)
@@ -153,6 +155,9 @@ Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
     if (us < least) least = us, best = p;
   };
   consider({2, 1, N}, smalls(small, steps));
+  const int64_t least_tiles =
+      (int64_t)ceil_div(M, tile_rows(1)) * ceil_div(N, tile_cols(kind, 1)) * nprob;
+  consider({1, 1, N}, ceil_div(least_tiles, 2 * cus) * (steps * u1 + c1));
   for (int s = 2; s <= 16 && s * 2 <= steps; ++s) {
     const double sums = (double)ceil_div(M, 128) * 128 * ceil_div(N, tile_cols(kind, 2)) * 128 *
                         nprob * s;
@@ -189,8 +194,10 @@ void launch_tiles(const Product& p, int mi, int splits, void* sums, hipStream_t 
   a.sums = static_cast<float*>(sums);
   const int grid = std::min(a.total, mi == 4 ? cu_count() : 2 * cu_count());
   a.xcd_chunk = grid % 8 == 0 ? grid / 8 : 0;
-  if (p.dt == BF16) (mi == 4 ? launch_tile_bf16_4 : launch_tile_bf16_2)(a, grid, s);
-  else (mi == 4 ? launch_tile_f32_4 : launch_tile_f32_2)(a, grid, s);
+  if (p.dt == BF16)
+    (mi == 4 ? launch_tile_bf16_4 : mi == 2 ? launch_tile_bf16_2 : launch_tile_bf16_1)(a, grid, s);
+  else
+    (mi == 4 ? launch_tile_f32_4 : mi == 2 ? launch_tile_f32_2 : launch_tile_f32_1)(a, grid, s);
 }
 
 }  // namespace
@@ -254,13 +261,18 @@ sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
   return check_launch();
 }
 
-sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int dt, void* out,
-                         int64_t ld, hipStream_t s) {
-  const int64_t n = rows * (ld / 8);
-  prof_begin(SM_K_MISC, 16.0 * n * dt_size(dt), s);
-  SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_lay_out<E>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                                           static_cast<const E*>(p), ldp, rows, cols,
-                                           static_cast<E*>(out), ld));
+sm_status launch_lay_out(const LayOuts& all, int dt, hipStream_t s) {
+  if (all.n == 0) return SM_OK;
+  int64_t most = 0;
+  double bytes = 0.0;
+  for (int i = 0; i < all.n; ++i) {
+    const int64_t n = all.m[i].rows * (all.m[i].ld / 8);
+    most = std::max(most, n);
+    bytes += 16.0 * n * dt_size(dt);
+  }
+  const dim3 grid((unsigned)((most + 255) / 256), all.n);
+  prof_begin(SM_K_MISC, bytes, s);
+  SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_lay_out<E>, grid, dim3(256), 0, s, all));
   prof_end(s);
   return check_launch();
 }

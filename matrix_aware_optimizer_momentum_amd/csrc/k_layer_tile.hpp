@@ -2,12 +2,13 @@
 //
 // Work split.  A launch walks the flat list of output tiles (of both results,
 // where a call makes two weight gradients at once) with one workgroup per CU,
-// or two of the small ones; workgroups of one XCD take consecutive tiles, in
+// or two of the smaller ones; workgroups of one XCD take consecutive tiles, in
 // bands of four tile rows (ns_tiles.hpp), so that they share operand panels
 // in that XCD's L2.  A wave owns MI x 2 blocks of 32 x 32 sums; tiles of 256 x
-// 256 have 2 x 4 waves with MI 4, tiles of 128 x 128 2 x 2 with MI 2.  Either
-// way two waves share a SIMD: while one waits, or issues a load (which holds
-// it up for as long as two products), the other multiplies.
+// 256 have 2 x 4 waves with MI 4, tiles of 128 x 128 2 x 2 with MI 2, tiles of
+// 64 x 64, for products with few tiles, 2 x 1 with MI 1.  In the larger ones two
+// waves share a SIMD: while one waits, or issues a load (which holds it up for
+// as long as two products), the other multiplies.
 //
 // A gated layer's tile holds both projections of the same columns: of the 64
 // rows of B that a wave multiplies 32 are Wg's and 32 the same ones of Wu, so
@@ -17,13 +18,14 @@
 // Pipeline.  Operands go HBM -> LDS with direct-to-LDS buffer loads, in stages
 // of 128 bytes a row (64 bf16 or 32 float32 of k): whole lines, since the L2
 // serves a line or half of one in the same time (stages of 64 bytes a row
-// asked it for twice as many).  There are two stage buffers.  A step multiplies
+// asked it for twice as many).  There are two stage buffers (four of the least
+// tiles).  A step multiplies
 // a stage in four slices of its k, reading the next slice's fragments
 // meanwhile; ahead of the last slice each wave waits for its reads of this
 // stage and its loads of the next one, and the workgroup meets; during the
 // last slice the next stage's first fragments are read and the loads of the
-// stage after that are issued into this stage's buffer.  So loads have a step
-// less a slice to land.  The stages run on across tiles and across the two
+// stage that is as many ahead as there are buffers are issued into this one's.
+// So loads have a step (three) less a slice to land.  The stages run on across tiles and across the two
 // parts of a sum (da Wg + db Wu): a tile's first ones load during the last
 // step and the epilogue of the one before.
 //
@@ -265,8 +267,13 @@ struct Geo {
   static constexpr int STAGE = 2 * HALF;
   static constexpr int CPR = ROWS * SIZE / 16;       // chunks of a k row (KR)
   static constexpr int WN = MI;                      // waves: 2 rows of WN
+  // Stage buffers: of small stages more, since a step of theirs is shorter
+  // than memory is far.
+  static constexpr int NBUF = MI == 1 ? 4 : 2;
   static constexpr int THREADS = 128 * WN;
-  static __device__ __forceinline__ int swz(int krow) { return SIZE == 2 ? 4 * (krow & 3) : 0; }
+  static __device__ __forceinline__ int swz(int krow) {
+    return SIZE == 2 ? 4 * (krow & 3) & (CPR - 1) : 0;
+  }
 };
 
 // A wave loads 32 rows' worth of each operand's stage, by four loads of 1 KB.
@@ -508,8 +515,10 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI> (&f)[2], co
     Frags<MI>& then = f[(s + 1) & 1];
     const char* from = s < 3 ? cur : nxt;
     if (s == 3) {
-      // this wave's reads of cur are done, and its loads of nxt
-      __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
+      // this wave's reads of cur are done, and its loads of nxt; those of the
+      // stages after it may be in flight
+      constexpr int FLY = (G::NBUF - 2) * 2 * LQ;
+      __builtin_amdgcn_s_waitcnt((FLY & 15) | (7 << 4) | ((FLY >> 4) << 14));   // lgkmcnt(0)
       meet();
     }
 #pragma unroll
@@ -517,6 +526,7 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI> (&f)[2], co
       mma<T>(acc[q / 2][q % 2], now.b[q % 2], now.a[q / 2]);
       if (q < 2) then.b[q] = fb.read(from + G::HALF, q, (s + 1) & 3);
       else if (q - 2 < MI) then.a[q - 2] = fa.read(from, q - 2, (s + 1) & 3);
+      if (MI == 1 && q == 1) then.a[0] = fa.read(from, 0, (s + 1) & 3);
       if (s == 3) {
 #pragma unroll
         for (int l = 0; l < 2 * LQ / Q; ++l) L.load(ldb, 2 * LQ / Q * q + l);
@@ -722,7 +732,7 @@ template <typename T, int KIND, int MI>
 __global__ __launch_bounds__(128 * MI) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void k_tile(TileArgs A) {
   typedef Geo<T, MI> G;
-  __shared__ __attribute__((aligned(16))) char smem[2 * G::STAGE + 4096 * (2 * G::WN)];
+  __shared__ __attribute__((aligned(16))) char smem[G::NBUF * G::STAGE + 4096 * (2 * G::WN)];
   int t = blockIdx.x;
   if (A.xcd_chunk > 0) t = (t & 7) * A.xcd_chunk + (t >> 3);
   const int stride = gridDim.x;
@@ -734,12 +744,12 @@ void k_tile(TileArgs A) {
   LoadPos<T, KIND, MI> L;
   L.set_tile(A, t);
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < G::NBUF; ++s) {
 #pragma unroll
     for (int q = 0; q < 2 * LQ; ++q) L.load(la0 + s * G::STAGE, q);
     L.advance(A, stride);
   }
-  wait_vm<2 * LQ>();
+  wait_vm<(G::NBUF - 1) * 2 * LQ>();
   meet();
   const FragOffs<T, MI, MI, kind_a_kr(KIND)> fa((wave / G::WN) * 32 * MI);
   const FragOffs<T, MI, 2, kind_b_kr(KIND)> fb((wave % G::WN) * 64);
@@ -763,13 +773,14 @@ void k_tile(TileArgs A) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) f[0].b[j] = fb.read(smem + cb * G::STAGE + G::HALF, j, 0);
     for (int k = 0; k < steps; ++k) {
-      step<T, KIND, MI>(acc, f, smem + cb * G::STAGE, smem + (cb ^ 1) * G::STAGE,
-                        la0 + cb * G::STAGE, L, fa, fb);
+      const int nb = cb + 1 == G::NBUF ? 0 : cb + 1;
+      step<T, KIND, MI>(acc, f, smem + cb * G::STAGE, smem + nb * G::STAGE, la0 + cb * G::STAGE, L,
+                        fa, fb);
       L.advance(A, stride);
-      cb ^= 1;
+      cb = nb;
     }
     epilogue<T, KIND, MI>(acc, A, decode_tile<KIND>(A, uniform(t)),
-                          smem + 2 * G::STAGE + 4096 * wave);
+                          smem + G::NBUF * G::STAGE + 4096 * wave);
   }
   wait_vm<0>();   // loads past the last stage target this workgroup's LDS
 }
@@ -842,8 +853,10 @@ void launch_few(const Product& p, hipStream_t s);
 // One translation unit for each type and tile.
 void launch_tile_bf16_4(const TileArgs& a, int grid, hipStream_t s);
 void launch_tile_bf16_2(const TileArgs& a, int grid, hipStream_t s);
+void launch_tile_bf16_1(const TileArgs& a, int grid, hipStream_t s);
 void launch_tile_f32_4(const TileArgs& a, int grid, hipStream_t s);
 void launch_tile_f32_2(const TileArgs& a, int grid, hipStream_t s);
+void launch_tile_f32_1(const TileArgs& a, int grid, hipStream_t s);
 
 }  // namespace layer
 }  // namespace sm

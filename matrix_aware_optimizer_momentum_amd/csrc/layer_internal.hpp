@@ -55,10 +55,20 @@ inline bool laid_out(const void* p, int64_t ld, int64_t len, int dt) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * size % 16 == 0 && len * size % 16 == 0 &&
          ld * size < (int64_t(1) << 31) / 256;
 }
-// A copy of a matrix that is so: rows x cols entries to rows x ld ones (ld a
-// multiple of 8), zeros behind them.
-sm_status launch_lay_out(const void* p, int64_t ldp, int64_t rows, int cols, int dt, void* out,
-                         int64_t ld, hipStream_t s);
+// Copies of matrices that are so: rows x cols entries (ldp apart) to rows x ld
+// ones (ld a multiple of 8), zeros behind them; all in one launch.
+struct LayOut {
+  const void* p;
+  int64_t ldp, rows;
+  int cols;
+  void* out;
+  int64_t ld;
+};
+struct LayOuts {
+  LayOut m[4];
+  int n;
+};
+sm_status launch_lay_out(const LayOuts& all, int dt, hipStream_t s);
 
 // The sums over T rows of dz (ld entries apart) of n columns, in float32, to
 // out (added to it with accumulate).  sums: scratch of column_sums_ws bytes.

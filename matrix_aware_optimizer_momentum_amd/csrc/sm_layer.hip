@@ -240,23 +240,18 @@ sm_status lay_out(const sm_layer& l, const LayerWs& w, char* ws, Operands* o, bo
     o->x = {ws + w.x, w.ldd};
     SM_TRY(launch_act8_unpack(l.x8, l.x8_scale, l.dt, l.T, l.d, ws + w.x, w.ldd, true, s));
   }
-  if (w.lay_x) {
-    o->x = {ws + w.x, w.ldd};
-    SM_TRY(launch_lay_out(l.x, l.ldx, l.T, l.d, l.dt, ws + w.x, w.ldd, s));
-  }
-  if (w.lay_w) {
-    o->w = {ws + w.w, w.ldd};
-    SM_TRY(launch_lay_out(l.w, l.ldw, l.n, l.d, l.dt, ws + w.w, w.ldd, s));
-  }
-  if (w.lay_w2) {
-    o->w2 = {ws + w.w2, w.ldd};
-    SM_TRY(launch_lay_out(l.w2, l.ldw2, l.n, l.d, l.dt, ws + w.w2, w.ldd, s));
-  }
-  if (w.lay_dy) {
-    o->dz[0] = {ws + w.dy, w.ldn};
-    SM_TRY(launch_lay_out(l.dy, l.lddy, l.T, l.n, l.dt, ws + w.dy, w.ldn, s));
-  }
-  return SM_OK;
+  LayOuts all;
+  all.n = 0;
+  auto lay = [&](bool wanted, Operand* m, int64_t rows, int cols, size_t at, int64_t ld) {
+    if (!wanted) return;
+    all.m[all.n++] = LayOut{m->p, m->ld, rows, cols, ws + at, ld};
+    *m = {ws + at, ld};
+  };
+  lay(w.lay_x, &o->x, l.T, l.d, w.x, w.ldd);
+  lay(w.lay_w, &o->w, l.n, l.d, w.w, w.ldd);
+  lay(w.lay_w2, &o->w2, l.n, l.d, w.w2, w.ldd);
+  lay(w.lay_dy, &o->dz[0], l.T, l.n, w.dy, w.ldn);
+  return launch_lay_out(all, l.dt, s);
 }
 
 sm_status check_ws(const LayerWs& w, const void* ws, size_t ws_bytes) {

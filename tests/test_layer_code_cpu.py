@@ -12,8 +12,8 @@ import pytest
 from matrix_aware_optimizer_momentum_amd import build_lib
 from tests.test_kernel_code_cpu import _sgprs, masked_mfmas_without_skip
 
-UNITS = ["k_act8", "k_layer", "k_layer_few", "k_layer_bf16_4", "k_layer_bf16_2", "k_layer_f32_4",
-         "k_layer_f32_2"]
+TILES = [f"k_layer_{t}_{m}" for t in ("bf16", "f32") for m in (4, 2, 1)]
+UNITS = ["k_act8", "k_layer", "k_layer_few", *TILES]
 
 
 @pytest.fixture(scope="module")
@@ -52,7 +52,7 @@ def test_no_scratch_and_no_packed_float32(asm, unit):
     assert not [o for o in ops if re.fullmatch(r"v_pk_(add|mul|fma)_f32", o)]
 
 
-@pytest.mark.parametrize("unit", [u for u in UNITS if u[-1] in "24"])
+@pytest.mark.parametrize("unit", TILES)
 def test_products_run_two_waves_to_a_simd(asm, unit):
     found = re.findall(r"\.name:\s+(\S*k_tile\S*)\n(?:.*\n)*?\s+\.vgpr_count:\s+(\d+)", asm[unit])
     assert len(found) == 6 and all(int(v) <= 256 for _, v in found), found
@@ -90,7 +90,7 @@ def lds_load_hazards(body):
     return bad
 
 
-@pytest.mark.parametrize("unit", [u for u in UNITS if u[-1] in "24"])
+@pytest.mark.parametrize("unit", TILES)
 def test_wait_states_of_the_loads_into_lds(asm, unit):
     bodies = {k: v for k, v in kernels(asm[unit]).items() if "k_tile" in k}
     for name, body in bodies.items():
