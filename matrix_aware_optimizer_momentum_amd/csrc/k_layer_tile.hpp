@@ -239,12 +239,14 @@ __device__ __forceinline__ void meet() {
 // byte address m0 + 16 lane, zeros where voff is kNowhere.  In inline
 // assembly so that the compiler, which cannot tell which LDS bytes a pending
 // load writes, adds no wait for all of them before every LDS read.  It has no
-// register result.  Its wait states: 5 between a VALU write of the
-// descriptor's registers and the load, 1 between writing M0 and the load.
+// register result.  Of its wait states the one after M0's write is here; the
+// five after a VALU write of the descriptor's registers are kept by the
+// distance (set's s_nop; 8192 x 11008 x 4096 backward 1311 us with five
+// before every load, 1290 without), which a test of the generated code checks.
 constexpr uint32_t kNowhere = 0x80000000u;   // the range that the descriptor allows
 __device__ __forceinline__ void dma16(uint64_t base, uint32_t voff, uint32_t m0) {
   const i32x4 r = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)kNowhere, 0x00020000};
-  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                :
                : "v"(voff), "s"(r), "s"(m0)
                : "memory", "m0");
@@ -461,6 +463,8 @@ struct LoadPos {
     bbase = uniform64(bbase + from * bstep);
     left = p.K - from * G::BK;
     part = q;
+    // the bases come from readfirstlane: see dma16
+    asm volatile("s_nop 4" : "+s"(abase), "+s"(bbase));
   }
   __device__ __forceinline__ void set_tile(const TileArgs& A, int t) {
     t = uniform(t);
@@ -521,6 +525,9 @@ __device__ __forceinline__ void step(f32x16 (&acc)[MI][2], Frags<MI> (&f)[2], co
       __builtin_amdgcn_s_waitcnt((FLY & 15) | (7 << 4) | ((FLY >> 4) << 14));   // lgkmcnt(0)
       meet();
     }
+    // the wave that is past the meeting first goes on first
+    if (s == 3) __builtin_amdgcn_s_setprio(1);
+    if (s == 0) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       mma<T>(acc[q / 2][q % 2], now.b[q % 2], now.a[q / 2]);
