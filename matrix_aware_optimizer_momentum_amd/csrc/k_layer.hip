@@ -95,27 +95,30 @@ __global__ __launch_bounds__(256) void k_lay_out(LayOuts all) {
   const LayOut& m = all.m[blockIdx.y];
   const int cols = m.cols;
   const int per_row = (int)(m.ld / 8);
-  const int64_t first = (int64_t)blockIdx.x * 256;
-  const int64_t row0 = first / per_row;
-  const uint32_t at = (uint32_t)(first - row0 * per_row) + threadIdx.x;
-  const int64_t row = row0 + at / (uint32_t)per_row;
-  if (row >= m.rows) return;
-  const int col = 8 * (int)(at % (uint32_t)per_row);
-  const T* q = static_cast<const T*>(m.p) + row * m.ldp + col;
-  u32x4 v[N] = {};
-  if (col + 8 <= cols) {
+  const int64_t n = m.rows * per_row;
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < n; first += (int64_t)gridDim.x * 256) {
+    const int64_t row0 = first / per_row;
+    const uint32_t at = (uint32_t)(first - row0 * per_row) + threadIdx.x;
+    const int64_t row = row0 + at / (uint32_t)per_row;
+    if (row >= m.rows) break;
+    const int col = 8 * (int)(at % (uint32_t)per_row);
+    const T* q = static_cast<const T*>(m.p) + row * m.ldp + col;
+    u32x4 v[N] = {};
+    if (col + 8 <= cols) {
 #pragma unroll
-    for (int h = 0; h < N; ++h) v[h] = reinterpret_cast<const V*>(q)[h];
-  } else {
+      for (int h = 0; h < N; ++h) v[h] = reinterpret_cast<const V*>(q)[h];
+    } else {
 #pragma unroll
-    for (int e = 0; e < 7; ++e) {
-      if (col + e >= cols) continue;
-      if constexpr (sizeof(T) == 2) v[0][e >> 1] |= (uint32_t)q[e] << (16 * (e & 1));
-      else v[e >> 2][e & 3] = __float_as_uint(q[e]);
+      for (int e = 0; e < 7; ++e) {
+        if (col + e >= cols) continue;
+        if constexpr (sizeof(T) == 2) v[0][e >> 1] |= (uint32_t)q[e] << (16 * (e & 1));
+        else v[e >> 2][e & 3] = __float_as_uint(q[e]);
+      }
     }
-  }
 #pragma unroll
-  for (int h = 0; h < N; ++h) reinterpret_cast<u32x4*>(static_cast<T*>(m.out) + row * m.ld + col)[h] = v[h];
+    for (int h = 0; h < N; ++h)
+      reinterpret_cast<u32x4*>(static_cast<T*>(m.out) + row * m.ld + col)[h] = v[h];
+  }
 }
 
 }  // namespace
@@ -139,8 +142,11 @@ Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
   const int64_t large = (int64_t)ceil_div(M, tile_rows(4)) * ceil_div(N, tile_cols(kind, 4)) * nprob;
   const int64_t small = (int64_t)ceil_div(M, tile_rows(2)) * ceil_div(N, tile_cols(kind, 2)) * nprob;
   // us, as measured: a step of a large tile, of one small tile on a CU and of
-  // two, of up to two least ones; around a tile; joining (the sums
-  // are written and read)
+  // two, of up to two least ones; around a tile; joining (the sums are written
+  // and read).  What the choice gains: GPT-2 large's first product for 4096
+  // tokens 81 -> 66 us (the cut), gated backward 1003 x 1280 x 3416 140 -> 91,
+  // float32 backward 515 x 771 x 1283 239 -> 99 (the shares), 1000 x 1024 x
+  // 1024 bf16 19 -> 14 (the least tiles).
   const bool b = dt == BF16;
   const double t4 = b ? 1.5 : 8.0, t1 = b ? 0.75 : 2.25, t2 = b ? 1.0 : 4.0, c4 = 9.0, c2 = 6.0;
   const double u1 = b ? 0.4 : 1.4, c1 = 5.0;
@@ -270,7 +276,7 @@ sm_status launch_lay_out(const LayOuts& all, int dt, hipStream_t s) {
     most = std::max(most, n);
     bytes += 16.0 * n * dt_size(dt);
   }
-  const dim3 grid((unsigned)((most + 255) / 256), all.n);
+  const dim3 grid((unsigned)std::min<int64_t>((most + 255) / 256, 1 << 20), all.n);
   prof_begin(SM_K_MISC, bytes, s);
   SM_DISPATCH_DT(dt, E, hipLaunchKernelGGL(k_lay_out<E>, grid, dim3(256), 0, s, all));
   prof_end(s);

@@ -9,7 +9,7 @@ namespace sm {
 // 1 / (1 + e^-z).  FINE (float32 layers): the compiler's exact division and
 // expf.  Else (bf16 layers) the hardware's exp2 and reciprocal, off by a few
 // 2^-23 and by |z| 2^-24 from the argument's rounding: far below bf16's half
-// step of 2^-9 for every |z| that leaves a value above 1e-30.
+// step of 2^-8 for every |z| that leaves a value above 1e-30.
 template <bool FINE>
 __device__ __forceinline__ float logistic(float z) {
   if constexpr (FINE) return 1.0f / (1.0f + expf(-z));

@@ -42,9 +42,9 @@ def rnd(dt):
 
 class Guarded:
     """A [rows, cols] tensor inside a larger buffer: `shift` entries off a 256-byte boundary, rows
-    `cols + gap` apart, sentinels everywhere else."""
+    `cols + gap` apart, sentinels (NaN) everywhere else."""
 
-    MARK = 0x5A
+    MARK = 0xFF   # NaN in both types
 
     def __init__(self, value, dt, shift=0, gap=0):
         rows, cols = value.shape
