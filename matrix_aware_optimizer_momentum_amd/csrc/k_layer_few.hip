@@ -7,6 +7,10 @@
 // loads, and is handed the same k of a token, so that a 16 x 16 product of the
 // matrix cores takes 16 rows and 16 tokens whatever the order of the k.  The
 // waves' sums meet in LDS, in a fixed order.  Nothing has to be aligned.
+//
+// Bound: HBM.  One token: gated 4096 x 11008 32.9 us (5.5 TB/s; a kernel that
+// only reads as many bytes in this order took 31), linear 11008 x 4096 17.8 (5.1 TB/s); 19
+// tokens, gated, 44 us: x comes out of the L2 for every 16 columns.
 #include "k_layer_tile.hpp"
 
 namespace sm {

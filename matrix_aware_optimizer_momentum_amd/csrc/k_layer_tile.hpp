@@ -4,11 +4,11 @@
 // where a call makes two weight gradients at once) with one workgroup per CU,
 // or two of the smaller ones; workgroups of one XCD take consecutive tiles, in
 // bands of four tile rows, so that they share operand panels in that XCD's L2.
-// A wave owns MI x 2 blocks of 32 x 32 sums; tiles of 256 x
-// 256 have 2 x 4 waves with MI 4, tiles of 128 x 128 2 x 2 with MI 2, tiles of
-// 64 x 64, for products with few tiles, 2 x 1 with MI 1.  In the larger ones two
-// waves share a SIMD: while one waits, or issues a load (which holds it up for
-// as long as two products), the other multiplies.
+// A wave owns MI x 2 blocks of 32 x 32 sums; tiles of 256 x 256 have 2 x 4 waves
+// with MI 4, tiles of 128 x 128 2 x 2 with MI 2, tiles of 64 x 64, for products
+// with few tiles, 2 x 1 with MI 1.  In the larger ones two waves share a SIMD:
+// while one waits, or issues a load (which holds it up for as long as two
+// products), the other multiplies (four waves of 128 x 128 took 7 % longer).
 //
 // A gated layer's tile holds both projections of the same columns: of the 64
 // rows of B that a wave multiplies 32 are Wg's and 32 the same ones of Wu, so
@@ -29,10 +29,12 @@
 // tiles and across the two parts of a sum (da Wg + db Wu): a tile's first ones
 // load during the last step and the epilogue of the one before.
 //
-// Bound.  8192 tokens, 4096 x 11008, bf16, sustained: 1.17-1.31 PFLOP/s
-// executed by the three kinds of product, the matrix pipes 65 % busy at 1.5 to
-// 1.7 GHz: the chip lowers its clock under this load, so that what counts is
-// the data moved for a product, not the instructions around it.
+// Bound.  8192 tokens, 4096 x 11008, bf16: 1.29 PFLOP/s by both projections (a
+// long run; the others by a profile), 1.27 with the backward epilogue, 1.30 by
+// da Wg + db Wu, 1.12 by the weight gradients; the matrix pipes 75, 69, 75 and
+// 59 % busy at 1.3 to 1.7 GHz while counted.  The chip lowers its clock under
+// this load, so that what counts is the data moved for a product, not only the
+// instructions around it.
 //
 // Edges.  Rows past an operand's last read the last one (their sums are not
 // stored).  Where k ends inside a stage, the lanes past it load from beyond

@@ -44,9 +44,9 @@ struct Product {
 inline bool few_tokens(int kind, int64_t T) {
   return (kind == kLinear || kind == kGated) && T <= 32;
 }
-// Launches p.  Unless few_tokens, every operand's rows (as they are stored) are 16-byte aligned,
-// less than 2^31 / 256 bytes apart, and a multiple of 16 bytes long, or have
-// readable memory up to one, zeros if they run along k.
+// Launches p.  Unless few_tokens, every operand's rows (as they are stored) are
+// 16-byte aligned, less than 2^31 / 256 bytes apart, and a multiple of 16 bytes
+// long, or have readable memory up to one, zeros if they run along k.
 // sums: scratch of product_ws bytes, 256-byte aligned.
 size_t product_ws(int kind, int dt, int M, int N, int K, int parts);
 sm_status launch_product(const Product& p, void* sums, hipStream_t s);
