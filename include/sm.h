@@ -554,9 +554,10 @@ sm_status sm_state8_unpack(const uint8_t* m8, const uint8_t* v8, const float* m_
  * or NaN entry is stored as NaN and does not touch its block's scale.
  * x8: [T][d] bytes.  scale: [T][ceil(d/32)] bytes, e + 127 (OCP e8m0).
  * Both are contiguous, at any alignment.
- * Errors: SM_ERR_ARG (null or misaligned pointers, ldx < d, an output
- *   overlapping another buffer), SM_ERR_SHAPE (T < 0 or > 2^30, d < 1 or
- *   > 2^20, T d > 2^40), SM_ERR_DTYPE, SM_ERR_HIP.  T == 0 is a no-op.
+ * Errors: SM_ERR_ARG (null or misaligned pointers, ldx < d or > 2^40, rows
+ *   over more than 2^46 entries, an output overlapping another buffer),
+ *   SM_ERR_SHAPE (T < 0 or > 2^30, d < 1 or > 2^20, T d > 2^40),
+ *   SM_ERR_DTYPE, SM_ERR_HIP.  T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 #define SM_ACT8_BLOCK 32
 sm_status sm_act8_pack(const void* x, int64_t ldx, int dt, int64_t T, int32_t d, uint8_t* x8,
@@ -610,7 +611,8 @@ sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_
  *   (may be NULL if that is 0); the query takes the call's own arguments.
  *   Calls that may run at the same time need one each.
  * Errors: SM_ERR_ARG (null or misaligned pointers, a row length above its ld,
- *   both or neither of x and x8, a bad act, an overlap, no output wanted),
+ *   an ld above 2^40 or rows over more than 2^46 entries, both or neither of x
+ *   and x8, a bad act, an overlap, no output wanted),
  *   SM_ERR_SHAPE (T < 0 or > 2^30, d or n < 1 or > 2^20, T d or T n >
  *   2^40), SM_ERR_DTYPE, SM_ERR_WORKSPACE, SM_ERR_HIP.
  * ---------------------------------------------------------------------- */

@@ -10,6 +10,7 @@ constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int kMaxWidth = 1 << 20;
 constexpr int64_t kMaxCount = int64_t(1) << 40;   // entries of x or y: their tiles stay countable
 constexpr int64_t kMaxLd = int64_t(1) << 40;
+constexpr int64_t kMaxSpan = int64_t(1) << 46;   // entries from a matrix's first row to past its last
 
 bool multiple_of(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
@@ -53,8 +54,9 @@ sm_status check_sizes(int64_t T, int d, int dt) {
   if (T < 0 || T > kMaxTokens || d < 1 || d > kMaxWidth) return SM_ERR_SHAPE;
   return SM_OK;
 }
-sm_status check_matrix(const void* p, int64_t ld, int64_t len, size_t size) {
-  return !p || !multiple_of(p, size) || ld < len || ld > kMaxLd ? SM_ERR_ARG : SM_OK;
+sm_status check_matrix(const void* p, int64_t ld, int64_t rows, int64_t len, size_t size) {
+  if (!p || !multiple_of(p, size) || ld < len || ld > kMaxLd) return SM_ERR_ARG;
+  return rows > 1 && ld > kMaxSpan / rows ? SM_ERR_ARG : SM_OK;
 }
 
 int act8_blocks(int d) { return (d + SM_ACT8_BLOCK - 1) / SM_ACT8_BLOCK; }
@@ -64,7 +66,7 @@ sm_status check_act8(const void* x, int64_t ldx, int dt, int64_t T, int32_t d, c
   SM_TRY(check_sizes(T, d, dt));
   if (T * d > kMaxCount) return SM_ERR_SHAPE;
   if (T == 0) return SM_OK;
-  SM_TRY(check_matrix(x, ldx, d, dt_size(dt)));
+  SM_TRY(check_matrix(x, ldx, T, d, dt_size(dt)));
   if (!x8 || !scale) return SM_ERR_ARG;
   const int64_t size = (int64_t)dt_size(dt);
   Areas a;
@@ -96,10 +98,10 @@ sm_status check_layer(const sm_layer* lp, Call c) {
   const size_t z = dt_size(l.dt);
   const int64_t size = (int64_t)z;
   Areas areas;
-  SM_TRY(check_matrix(l.w, l.ldw, l.d, z));
+  SM_TRY(check_matrix(l.w, l.ldw, l.n, l.d, z));
   areas.add(l.w, l.ldw * size, l.n, l.d * size, false);
   if (is_gated(c)) {
-    SM_TRY(check_matrix(l.w2, l.ldw2, l.d, z));
+    SM_TRY(check_matrix(l.w2, l.ldw2, l.n, l.d, z));
     areas.add(l.w2, l.ldw2 * size, l.n, l.d * size, false);
   } else if (l.bias) {
     if (!multiple_of(l.bias, z)) return SM_ERR_ARG;
@@ -110,15 +112,15 @@ sm_status check_layer(const sm_layer* lp, Call c) {
     areas.add(l.x8, l.d, l.T, l.d, false);
     areas.add(l.x8_scale, act8_blocks(l.d), l.T, act8_blocks(l.d), false);
   } else if (l.T > 0) {
-    SM_TRY(check_matrix(l.x, l.ldx, l.d, z));
+    SM_TRY(check_matrix(l.x, l.ldx, l.T, l.d, z));
     areas.add(l.x, l.ldx * size, l.T, l.d * size, false);
   }
   if (!is_grad(c)) {
     if (l.T > 0) {
-      SM_TRY(check_matrix(l.y, l.ldy, l.n, z));
+      SM_TRY(check_matrix(l.y, l.ldy, l.T, l.n, z));
       areas.add(l.y, l.ldy * size, l.T, l.n * size, true);
       if (c == kCallLinear && l.residual) {
-        SM_TRY(check_matrix(l.residual, l.ldr, l.n, z));
+        SM_TRY(check_matrix(l.residual, l.ldr, l.T, l.n, z));
         if (l.residual != l.y || l.ldr != l.ldy)
           areas.add(l.residual, l.ldr * size, l.T, l.n * size, false);
       }
@@ -129,19 +131,19 @@ sm_status check_layer(const sm_layer* lp, Call c) {
   const void* dbias = is_gated(c) ? nullptr : l.dbias;
   if (!l.dx && !l.dw && !dw2 && !dbias) return SM_ERR_ARG;
   if (l.T > 0) {
-    SM_TRY(check_matrix(l.dy, l.lddy, l.n, z));
+    SM_TRY(check_matrix(l.dy, l.lddy, l.T, l.n, z));
     areas.add(l.dy, l.lddy * size, l.T, l.n * size, false);
     if (l.dx) {
-      SM_TRY(check_matrix(l.dx, l.lddx, l.d, z));
+      SM_TRY(check_matrix(l.dx, l.lddx, l.T, l.d, z));
       areas.add(l.dx, l.lddx * size, l.T, l.d * size, true);
     }
   }
   if (l.dw) {
-    SM_TRY(check_matrix(l.dw, l.lddw, l.d, z));
+    SM_TRY(check_matrix(l.dw, l.lddw, l.n, l.d, z));
     areas.add(l.dw, l.lddw * size, l.n, l.d * size, true);
   }
   if (dw2) {
-    SM_TRY(check_matrix(l.dw2, l.lddw2, l.d, z));
+    SM_TRY(check_matrix(l.dw2, l.lddw2, l.n, l.d, z));
     areas.add(l.dw2, l.lddw2 * size, l.n, l.d * size, true);
   }
   if (dbias) {

@@ -212,6 +212,24 @@ def test_act8_refusals(kw, want):
     assert lib.sm_last_hip_error() == 0
 
 
+@pytest.mark.parametrize("T,ldx,want", [
+    (1 << 30, 1 << 34, ARG),    # 2^64 entries: rows whose distance no int64 holds
+    (1 << 30, 1 << 40, ARG), (1 << 25, 1 << 40, ARG),
+    ((1 << 20) + 1, 1 << 26, ARG), (1 << 20, 1 << 26, OK),   # 2^46 entries are the most
+    (1, 1 << 40, OK), (1 << 6, 1 << 40, OK),
+])
+def test_rows_that_no_address_reaches_are_refused(T, ldx, want):
+    """Where x ends is not judged by a sum that wraps round."""
+    f = dict(T=T, ldx=ldx, x=1 << 60, y=1 << 56, dx=3 << 55, dy=1 << 57, residual=None)
+    for call in ("linear", "gated", "linear_grad", "gated_grad"):
+        assert _refusal(call, **f) == want, call
+    if want != OK:
+        lib = B.lib()
+        assert lib.sm_act8_pack(0x100000, ldx, B.F32, T, 16, 1 << 56, 1 << 57, None) == want
+        assert lib.sm_act8_unpack(1 << 56, 1 << 57, B.F32, T, 16, 0x100000, ldx, None) == want
+        assert lib.sm_last_hip_error() == 0
+
+
 def test_act8_codes_over_scales_are_refused():
     assert B.lib().sm_act8_pack(0x100000, 70, B.F32, 5, 70, 0x200000, 0x200000 + 5 * 70 - 1,
                                 None) == ARG
