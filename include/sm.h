@@ -602,14 +602,15 @@ sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_
  * and a multiple of 16 bytes long are read in place, others are laid out in
  * the workspace first.  y may be residual itself (same pointer and ld); apart
  * from that no output may overlap another buffer, but matrices of one ld may
- * be columns of one wider matrix.
+ * be columns of one wider matrix, and a vector may lie between two rows.
  * T == 0: sm_linear, sm_gated and dx are no-ops; dw, dw2 and dbias are set to
  * 0, or left as they are with accumulate.
  * A row of x or dy that holds a NaN or infinity makes its own rows of y and
  * dx so, and dw, dw2 and dbias as the sums give.
  * ws: scratch of at least the matching *_ws(...) bytes, 256-byte aligned
- *   (may be NULL if that is 0); the query takes the call's own arguments.
- *   Calls that may run at the same time need one each.
+ *   (may be NULL if that is 0), over none of the call's buffers; the query
+ *   takes the call's own arguments.  Calls that may run at the same time need
+ *   one each.
  * Errors: SM_ERR_ARG (null or misaligned pointers, a row length above its ld,
  *   an ld above 2^40 or rows over more than 2^46 entries, both or neither of x
  *   and x8, a bad act, an overlap, no output wanted),

@@ -22,12 +22,13 @@ struct Area {
   bool written;
 };
 // Some byte lies in both.  Matrices of one ld may be columns of one wider
-// matrix: they share none if their rows' places modulo ld do not meet.
+// matrix, and a single row may lie between a matrix's: they share none if their
+// rows' places modulo ld do not meet.
 bool meet(const Area& x, const Area& y) {
   const Area &a = x.p <= y.p ? x : y, &b = x.p <= y.p ? y : x;
   const uintptr_t off = b.p - a.p;
   if (off >= (uintptr_t)((a.rows - 1) * a.ld + a.len)) return false;
-  if (a.ld != b.ld) return true;
+  if (a.ld != b.ld && b.rows > 1) return true;
   const int64_t at = (int64_t)(off % (uintptr_t)a.ld);
   return at < a.len || at + b.len > a.ld;
 }
@@ -88,16 +89,17 @@ bool reads_x(const sm_layer& l, Call c) {
   return !is_grad(c) || makes_dz(l, c) || l.dw;
 }
 
-sm_status check_layer(const sm_layer* lp, Call c) {
+// all: empty, gets the call's matrices.
+sm_status check_layer(const sm_layer* lp, Call c, Areas* all) {
   if (!lp) return SM_ERR_ARG;
   const sm_layer& l = *lp;
+  Areas& areas = *all;
   SM_TRY(check_sizes(l.T, l.d, l.dt));
   if (l.n < 1 || l.n > kMaxWidth) return SM_ERR_SHAPE;
   if (l.T * std::max(l.d, l.n) > kMaxCount) return SM_ERR_SHAPE;
   if (l.act < SM_ACT_NONE || l.act > SM_ACT_GELU_TANH) return SM_ERR_ARG;
   const size_t z = dt_size(l.dt);
   const int64_t size = (int64_t)z;
-  Areas areas;
   SM_TRY(check_matrix(l.w, l.ldw, l.n, l.d, z));
   areas.add(l.w, l.ldw * size, l.n, l.d * size, false);
   if (is_gated(c)) {
@@ -203,7 +205,8 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
 
 sm_status layer_query(const sm_layer* l, Call c, size_t* bytes) {
   if (!bytes) return SM_ERR_ARG;
-  SM_TRY(check_layer(l, c));
+  Areas areas;
+  SM_TRY(check_layer(l, c, &areas));
   *bytes = layer_ws(*l, c).bytes;
   return SM_OK;
 }
@@ -256,9 +259,12 @@ sm_status lay_out(const sm_layer& l, const LayerWs& w, char* ws, Operands* o, bo
   return launch_lay_out(all, l.dt, s);
 }
 
-sm_status check_ws(const LayerWs& w, const void* ws, size_t ws_bytes) {
+// What the call uses of the workspace lies over none of its matrices.
+sm_status check_ws(const LayerWs& w, const void* ws, size_t ws_bytes, Areas* areas) {
   if (w.bytes && (!ws || !multiple_of(ws, 256))) return SM_ERR_ARG;
-  return ws_bytes < w.bytes ? SM_ERR_WORKSPACE : SM_OK;
+  if (ws_bytes < w.bytes) return SM_ERR_WORKSPACE;
+  areas->add(ws, 0, w.bytes ? 1 : 0, (int64_t)w.bytes, true);
+  return areas->conflict() ? SM_ERR_ARG : SM_OK;
 }
 
 Product product_of(const sm_layer& l, int kind, const Operands& o) {
@@ -279,10 +285,11 @@ Product product_of(const sm_layer& l, int kind, const Operands& o) {
 }
 
 sm_status run_forward(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hipStream_t s) {
-  SM_TRY(check_layer(lp, c));
+  Areas areas;
+  SM_TRY(check_layer(lp, c, &areas));
   const sm_layer& l = *lp;
   const LayerWs w = layer_ws(l, c);
-  SM_TRY(check_ws(w, ws, ws_bytes));
+  SM_TRY(check_ws(w, ws, ws_bytes, &areas));
   if (l.T == 0) return SM_OK;
   Operands o;
   SM_TRY(lay_out(l, w, static_cast<char*>(ws), &o, false, s));
@@ -294,13 +301,14 @@ sm_status run_forward(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hip
 }
 
 sm_status run_grad(const sm_layer* lp, Call c, void* wsp, size_t ws_bytes, hipStream_t s) {
-  SM_TRY(check_layer(lp, c));
+  Areas areas;
+  SM_TRY(check_layer(lp, c, &areas));
   const sm_layer& l = *lp;
   const bool gated = is_gated(c);
   void* dw2 = gated ? l.dw2 : nullptr;
   void* dbias = gated ? nullptr : l.dbias;
   const LayerWs w = layer_ws(l, c);
-  SM_TRY(check_ws(w, wsp, ws_bytes));
+  SM_TRY(check_ws(w, wsp, ws_bytes, &areas));
   if (l.T == 0) {
     if (l.accumulate) return SM_OK;
     if (l.dw) SM_TRY(launch_zero(l.dw, l.lddw, l.n, l.d, l.dt, s));
