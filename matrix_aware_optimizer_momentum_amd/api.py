@@ -983,25 +983,26 @@ def linear_grad(dy: torch.Tensor, x, w: torch.Tensor, bias: Optional[torch.Tenso
                 act: int = B.ACT_NONE, dx: Optional[torch.Tensor] = None,
                 dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
                 need_dx: bool = True, need_dw: bool = True, accumulate: bool = False,
-                ws: Optional[torch.Tensor] = None):
+                ws: Optional[torch.Tensor] = None, need_db: bool = True):
     """(dx, dw, db) of linear for the gradient dy [..., n] of its result; x is the
     input or its Act8 checkpoint.  dw (and db, if bias or db is given) may be a
     worker's gradients of a MatrixBuffers (a ParamBuffers), which accumulate
-    adds to; need_dx, need_dw: False leaves that one out (None)."""
+    adds to; need_dx, need_dw, need_db: False leaves that one out (None)."""
     c = _LayerCall(w, act, dy)
     c.bias("bias", bias, "bias")
     c.kept(x)
     c.outputs("dy", dy)
     if accumulate and need_dw and dw is None:
         raise ValueError("accumulate needs dw")
-    if accumulate and bias is not None and db is None:
+    if accumulate and need_db and bias is not None and db is None:
         raise ValueError("accumulate needs db")
     dx = _out_rows(dx, dy, c.d, "dx") if need_dx else None
     if need_dw and dw is None:
         dw = torch.empty_like(w, memory_format=torch.contiguous_format)
     dw = dw if need_dw else None
-    if bias is not None and db is None:
+    if need_db and bias is not None and db is None:
         db = torch.empty_like(bias)
+    db = db if need_db else None
     c.inputs("dx", dx)
     c.weights("dw", dw)
     c.bias("dbias", db, "db")
@@ -1013,21 +1014,24 @@ def linear_grad(dy: torch.Tensor, x, w: torch.Tensor, bias: Optional[torch.Tenso
 def gated_grad(dy: torch.Tensor, x, wg: torch.Tensor, wu: torch.Tensor, act: int = B.ACT_SILU,
                dx: Optional[torch.Tensor] = None, dwg: Optional[torch.Tensor] = None,
                dwu: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
-               accumulate: bool = False, ws: Optional[torch.Tensor] = None):
+               accumulate: bool = False, ws: Optional[torch.Tensor] = None,
+               need_dwg: bool = True, need_dwu: bool = True):
     """(dx, dwg, dwu) of gated for the gradient dy [..., n] of its result; x, the
-    outputs and the rest as for linear_grad."""
+    outputs and the rest as for linear_grad.  need_dw: False leaves out both of
+    dwg and dwu, need_dwg and need_dwu one."""
     c = _LayerCall(wg, act, dy)
     c.weights("w2", wu, "wu")
     c.kept(x)
     c.outputs("dy", dy)
-    if accumulate and need_dw and (dwg is None or dwu is None):
+    need_dwg, need_dwu = need_dw and need_dwg, need_dw and need_dwu
+    if accumulate and ((need_dwg and dwg is None) or (need_dwu and dwu is None)):
         raise ValueError("accumulate needs dwg and dwu")
     dx = _out_rows(dx, dy, c.d, "dx") if need_dx else None
-    if need_dw:
-        dwg = torch.empty_like(wg, memory_format=torch.contiguous_format) if dwg is None else dwg
-        dwu = torch.empty_like(wu, memory_format=torch.contiguous_format) if dwu is None else dwu
-    else:
-        dwg = dwu = None
+    if need_dwg and dwg is None:
+        dwg = torch.empty_like(wg, memory_format=torch.contiguous_format)
+    if need_dwu and dwu is None:
+        dwu = torch.empty_like(wu, memory_format=torch.contiguous_format)
+    dwg, dwu = dwg if need_dwg else None, dwu if need_dwu else None
     c.inputs("dx", dx)
     c.weights("dw", dwg, "dwg")
     c.weights("dw2", dwu, "dwu")
