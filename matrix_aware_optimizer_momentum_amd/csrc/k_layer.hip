@@ -125,59 +125,8 @@ __global__ __launch_bounds__(256) void k_lay_out(LayOuts all) {
 
 namespace {
 
-// How a product is launched: tiles of 64 mi rows, columns from `cut` on by a
-// second launch of small tiles, sums in `splits` shares.
-struct Plan {
-  int mi, splits, cut;
-};
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
-int tile_rows(int mi) { return 64 * mi; }
-int tile_cols(int kind, int mi) { return kind_dual(kind) ? 32 * mi : 64 * mi; }
-
-Plan plan_product(int kind, int dt, int M, int N, int K, int parts) {
-  const int cus = cu_count();
-  const int nprob = kind == kDw ? parts : 1;
-  const int steps = ceil_div(K, dt == BF16 ? 64 : 32) * (kind == kDx ? parts : 1);
-  const int64_t large = (int64_t)ceil_div(M, tile_rows(4)) * ceil_div(N, tile_cols(kind, 4)) * nprob;
-  const int64_t small = (int64_t)ceil_div(M, tile_rows(2)) * ceil_div(N, tile_cols(kind, 2)) * nprob;
-  // us, as measured: a step of a large tile, of one small tile on a CU and of
-  // two, of up to two least ones; around a tile; joining (the sums are written
-  // and read).  What the choice gains: GPT-2 large's first product for 4096
-  // tokens 81 -> 66 us (the cut), gated backward 1003 x 1280 x 3416 140 -> 91,
-  // float32 backward 515 x 771 x 1283 239 -> 99 (the shares), 1000 x 1024 x
-  // 1024 bf16 19 -> 14 (the least tiles).
-  const bool b = dt == BF16;
-  const double t4 = b ? 1.5 : 8.0, t1 = b ? 0.75 : 2.25, t2 = b ? 1.0 : 4.0, c4 = 9.0, c2 = 6.0;
-  const double u1 = b ? 0.4 : 1.4, c1 = 5.0;
-  const double join = 3.0, per_sum = 8.0 / 8.0e6;
-  auto smalls = [&](int64_t n, double st) {   // n small tiles of st steps
-    return ceil_div(n, 2 * cus) > 1 || n > cus ? ceil_div(n, 2 * cus) * (st * t2 + c2)
-                                               : st * t1 + c2;
-  };
-  Plan best = {4, 1, N};
-  double least = ceil_div(large, cus) * (steps * t4 + c4);
-  auto consider = [&](Plan p, double us) {
-    if (us < least) least = us, best = p;
-  };
-  consider({2, 1, N}, smalls(small, steps));
-  const int64_t least_tiles =
-      (int64_t)ceil_div(M, tile_rows(1)) * ceil_div(N, tile_cols(kind, 1)) * nprob;
-  consider({1, 1, N}, ceil_div(least_tiles, 2 * cus) * (steps * u1 + c1));
-  for (int s = 2; s <= 16 && s * 2 <= steps; ++s) {
-    const double sums = (double)ceil_div(M, 128) * 128 * ceil_div(N, tile_cols(kind, 2)) * 128 *
-                        nprob * s;
-    consider({2, s, N}, smalls(small * s, (double)steps / s) + join + sums * per_sum);
-  }
-  if (nprob == 1 && large > cus) {   // whole rounds of large tiles, the rest by small ones
-    const int tm = ceil_div(M, tile_rows(4));
-    const int n1 = (int)(large / cus * cus / tm) * tile_cols(kind, 4);
-    if (n1 > 0 && n1 < N) {
-      const int64_t rest = (int64_t)ceil_div(M, 128) * ceil_div(N - n1, tile_cols(kind, 2));
-      consider({4, 1, n1}, large / cus * (steps * t4 + c4) + smalls(rest, steps) + 2.0);
-    }
-  }
-  return best;
+Plan plan_of(int kind, int dt, int M, int N, int K, int parts) {
+  return plan_product(kind, dt == BF16, M, N, K, parts, cu_count());
 }
 
 layer::TileArgs tile_args(const Product& p, int mi, int splits) {
@@ -210,7 +159,7 @@ void launch_tiles(const Product& p, int mi, int splits, void* sums, hipStream_t 
 
 size_t product_ws(int kind, int dt, int M, int N, int K, int parts) {
   if (few_tokens(kind, M)) return 0;
-  const Plan plan = plan_product(kind, dt, M, N, K, parts);
+  const Plan plan = plan_of(kind, dt, M, N, K, parts);
   if (plan.splits == 1) return 0;
   Product p;
   std::memset(&p, 0, sizeof(p));
@@ -241,7 +190,7 @@ sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
   if (few_tokens(p.kind, p.M)) {
     layer::launch_few(p, s);
   } else {
-    const Plan plan = plan_product(p.kind, p.dt, p.M, p.N, p.K, p.parts);
+    const Plan plan = plan_of(p.kind, p.dt, p.M, p.N, p.K, p.parts);
     Product q = p;
     q.N = std::min(p.N, plan.cut);
     if (plan.cut < p.N && p.pad) q.pad = q.N;

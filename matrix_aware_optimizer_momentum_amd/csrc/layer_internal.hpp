@@ -2,24 +2,10 @@
 // k_act8.hip) and their C ABI (sm_layer.hip).
 #pragma once
 
+#include "layer_plan.hpp"
 #include "sm_internal.hpp"
 
 namespace sm {
-
-// What a product of a layer computes, and with it its operands' layouts.
-// An operand is k-contiguous (KC: rows x K, row-major) or k-major (KR: K x
-// rows).
-//   kLinear      c = act(A B^T + bias) + in          A = x KC,  B = W KC
-//   kSlope       c = in * act'(A B^T + bias)         A = x KC,  B = W KC
-//   kGated       c = act(a) b,  a = A B^T, b = A B2^T      x, Wg and Wu KC
-//   kGatedSlope  c = in b act'(a),  c2 = in act(a)         x, Wg and Wu KC
-//   kDx          c = A B (+ A2 B2)                   A = dz KC, B = W KR
-//   kDw          c (+)= A^T B  (and c2 (+)= A2^T B)  A = dz KR, B = x KR
-enum ProductKind : int { kLinear, kSlope, kGated, kGatedSlope, kDx, kDw };
-constexpr bool kind_dual(int k) { return k == kGated || k == kGatedSlope; }
-constexpr bool kind_acts(int k) { return k == kLinear || k == kSlope || kind_dual(k); }
-constexpr bool kind_a_kr(int k) { return k == kDw; }
-constexpr bool kind_b_kr(int k) { return k == kDx || k == kDw; }
 
 struct Operand {
   const void* p;
@@ -38,12 +24,6 @@ struct Product {
   int accumulate;     // kDw
 };
 
-// The kernel for few tokens takes the product, operands of any alignment.  (us
-// by it / by tiles: 17 tokens, gated 4096 x 11008 44.6 / 45.7, linear 11008 x
-// 4096 26.7 / 32.4; 32 tokens 49.5 / 45.4, 31.7 / 34.0.)
-inline bool few_tokens(int kind, int64_t T) {
-  return (kind == kLinear || kind == kGated) && T <= 32;
-}
 // Launches p.  Unless few_tokens, every operand's rows (as they are stored) are
 // 16-byte aligned, less than 2^31 / 256 bytes apart, and a multiple of 16 bytes
 // long, or have readable memory up to one, zeros if they run along k.
