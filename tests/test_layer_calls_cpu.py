@@ -2,9 +2,12 @@
 the workspace, and of buffers between a matrix's rows (no GPU needed)."""
 import ctypes
 
+import numpy as np
 import pytest
+import torch
 
 from matrix_aware_optimizer_momentum_amd import _binding as B
+from oracle import layer_oracle as L
 from tests.test_layer_cpu import ARG, CALLS, OK, WORKSPACE, _layer, _refusal
 
 # every operand is laid out, every product has scratch of its own
@@ -49,3 +52,18 @@ def test_a_workspace_over_a_checkpoint_is_refused():
 ])
 def test_vectors_between_rows(call, kw, want):
     assert _refusal(call, **kw) == want
+
+
+def test_the_vectorised_reference_of_checkpoints_is_the_oracle():
+    from tests.test_gpu_act8 import pack_reference, values_of
+    rng = np.random.default_rng(0)
+    v = rng.standard_normal((60, 100)) * np.exp(4 * rng.standard_normal((60, 1)))
+    for value in (np.inf, -np.inf, np.nan, 3.3e38, -3.4e38, 1e-38, 448.0, 0.0):
+        v[rng.random(v.shape) < 0.05] = value
+    v[7], v[8], v[9] = 3.4e38, 0.0, np.nan
+    x = torch.from_numpy(v).float()
+    codes, scales = pack_reference(x)
+    want = L.act8_pack(x.double().numpy())
+    np.testing.assert_array_equal(codes.numpy(), want[0])
+    np.testing.assert_array_equal(scales.numpy(), want[1])
+    np.testing.assert_array_equal(values_of(codes, scales, "cpu").numpy(), L.act8_unpack(*want))
