@@ -157,8 +157,11 @@ void launch_tiles(const Product& p, int mi, int splits, void* sums, hipStream_t 
 
 }  // namespace
 
+bool few_tokens(int kind, int dt, int64_t T, int n, int d, bool w_in_place, bool x_in_place) {
+  return takes_few(kind, dt == BF16, T, n, d, w_in_place, x_in_place, cu_count());
+}
+
 size_t product_ws(int kind, int dt, int M, int N, int K, int parts) {
-  if (few_tokens(kind, M)) return 0;
   const Plan plan = plan_of(kind, dt, M, N, K, parts);
   if (plan.splits == 1) return 0;
   Product p;
@@ -187,7 +190,7 @@ static double product_bytes(const Product& p) {
 sm_status launch_product(const Product& p, void* sums, hipStream_t s) {
   prof_begin(SM_K_LAYER, 2.0 * p.M * p.N * p.K * (kind_dual(p.kind) ? 2 : p.parts), s,
              product_bytes(p));
-  if (few_tokens(p.kind, p.M)) {
+  if (p.few) {
     layer::launch_few(p, s);
   } else {
     const Plan plan = plan_of(p.kind, p.dt, p.M, p.N, p.K, p.parts);

@@ -9,8 +9,11 @@
 // waves' sums meet in LDS, in a fixed order.  Nothing has to be aligned.
 //
 // Bound: HBM.  One token: gated 4096 x 11008 32.9 us (5.5 TB/s; a kernel that
-// only reads as many bytes in this order took 31), linear 11008 x 4096 17.8 (5.1 TB/s); 19
-// tokens, gated, 44 us: x comes out of the L2 for every 16 columns.
+// only reads as many bytes in this order took 31), linear 11008 x 4096 17.8 (5.1
+// TB/s; those with three sets of weights in turn, some of whose bytes are still
+// in the Infinity Cache; with nine sets 34.1 and 22.1).  With more tokens x,
+// which comes out of the L2 for every 16 columns, and outputs too narrow for
+// all CUs: takes_few leaves those to the tiles.
 #include "k_layer_tile.hpp"
 
 namespace sm {
@@ -137,11 +140,17 @@ __global__ __launch_bounds__(1024) void k_few(Product p) {
   }
 }
 
-// 16 waves, where the rows have a piece for each.  (One token, us, with 4 / 8 /
-// 16 waves: gated 4096 x 11008 36.5 / 35.1 / 32.8, linear 11008 x 4096 24.2 /
-// 20.0 / 20.5; one piece in flight instead of two 35.5 / 36.2 / 34.3 and 32.8 /
-// 21.3 / 19.5.  19 tokens, gated: one piece 51.6 / 44.8 / 45.9, two 46.9 / 48.4
-// / 47.7.)
+// 16 waves, where the rows have a piece for each, two pieces in flight up to 16
+// tokens and one beyond.  No choice is the best everywhere; us, bf16 (nine sets
+// of weights):
+//                    waves x pieces   8 x 1  8 x 2  16 x 1  16 x 2
+//   gated 4096 -> 11008, 1 token       35.5   35.3    34.3    34.1
+//   linear 11008 -> 4096, 1 token      22.3   21.3    20.8    22.0
+//   gated 4096 -> 11008, 16 tokens     38.3   42.2    38.1    41.1
+//   gated 1280 -> 5120, 1 token         8.8    9.3     8.8    11.1
+//   gated 11008 -> 4096, 19 tokens     42.4   48.7    44.2    48.0
+// and float32, linear 4096 -> 11008, 1 token: 43.4, 38.8, 38.7, 36.6; 19 tokens:
+// 59.6, 62.0, 57.4, 63.6.
 template <typename T, int KIND>
 void launch_kind(const Product& p, hipStream_t s) {
   constexpr int PIECE = 128 / sizeof(T);

@@ -22,12 +22,15 @@ struct Product {
   int64_t ldc[2];
   int pad;            // kSlope, kGatedSlope: columns N .. pad - 1 of c get zeros
   int accumulate;     // kDw
+  int few;            // by the kernel for few tokens
 };
 
-// Launches p.  Unless few_tokens, every operand's rows (as they are stored) are
+// takes_few of layer_plan.hpp on this GPU.
+bool few_tokens(int kind, int dt, int64_t T, int n, int d, bool w_in_place, bool x_in_place);
+// Launches p.  Unless p.few, every operand's rows (as they are stored) are
 // 16-byte aligned, less than 2^31 / 256 bytes apart, and a multiple of 16 bytes
 // long, or have readable memory up to one, zeros if they run along k.
-// sums: scratch of product_ws bytes, 256-byte aligned.
+// sums: scratch of product_ws bytes (none if p.few), 256-byte aligned.
 size_t product_ws(int kind, int dt, int M, int N, int K, int parts);
 sm_status launch_product(const Product& p, void* sums, hipStream_t s);
 inline bool laid_out(const void* p, int64_t ld, int64_t len, int dt) {

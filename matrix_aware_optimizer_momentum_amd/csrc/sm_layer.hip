@@ -158,6 +158,7 @@ sm_status check_layer(const sm_layer* lp, Call c, Areas* all) {
 // What a call keeps in its workspace: offsets of the operands that it lays out
 // anew, of x from a checkpoint, and of dz.
 struct LayerWs {
+  bool few;   // a forward product by the kernel for few tokens: nothing of this
   bool lay_x, lay_w, lay_w2, lay_dy;
   size_t x, w, w2, dy, dz, dz2, sums, bytes;   // sums: of a split product
   int64_t ldd, ldn;   // rows of d and of n entries
@@ -171,7 +172,14 @@ LayerWs layer_ws(const sm_layer& l, Call c) {
   };
   w.ldd = round_up(l.d, 8);
   w.ldn = round_up(l.n, 8);
-  if (l.T == 0 || (!is_grad(c) && few_tokens(is_gated(c) ? kGated : kLinear, l.T))) return w;
+  if (l.T == 0) return w;
+  if (!is_grad(c)) {
+    const bool in_place = laid_out(l.w, l.ldw, l.d, l.dt) &&
+                          (!is_gated(c) || laid_out(l.w2, l.ldw2, l.d, l.dt));
+    w.few = few_tokens(is_gated(c) ? kGated : kLinear, l.dt, l.T, l.n, l.d, in_place,
+                       laid_out(l.x, l.ldx, l.d, l.dt));
+    if (w.few) return w;
+  }
   const bool grad = is_grad(c), x8 = grad && l.x8;
   const bool again = !grad || makes_dz(l, c);   // x W^T is computed
   w.lay_x = !x8 && reads_x(l, c) && !laid_out(l.x, l.ldx, l.d, l.dt);
@@ -297,6 +305,7 @@ sm_status run_forward(const sm_layer* lp, Call c, void* ws, size_t ws_bytes, hip
   if (c == kCallLinear) p.in = {l.residual, l.ldr};
   p.c[0] = l.y;
   p.ldc[0] = l.ldy;
+  p.few = w.few;
   return launch_product(p, static_cast<char*>(ws) + w.sums, s);
 }
 

@@ -108,3 +108,31 @@ def test_curved_activations_gated(gpu_lib, T, d, n, dt, name):
     close(dx, da @ G + db @ U, eda @ g + edb @ u + sum_error(2 * n, ma @ g + mb @ u), half, "dx")
     close(dwg, da.T @ X, eda.T @ ax + sum_error(T, ma.T @ ax), half, "dwg")
     close(dwu, db.T @ X, edb.T @ ax + sum_error(T, mb.T @ ax), half, "dwu")
+
+
+# both kernels that few tokens may take: narrow outputs of long sums, wide ones, odd ones
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("gap", [0, 5, 8])
+@pytest.mark.parametrize("d,n", [(11008, 512), (2304, 768), (4096, 64), (4100, 1003), (264, 4096)])
+def test_few_tokens(gpu_lib, d, n, gap, dt):
+    """Whole numbers: every sum is exact, whichever kernel takes it and however it is split."""
+    gen = torch.Generator(device="cuda").manual_seed(d + n + gap)
+
+    def whole(top, *s):
+        wide = torch.randint(-top, top + 1, (*s[:-1], s[-1] + gap), generator=gen, device="cuda")
+        return wide.to(DT[dt])[..., :s[-1]]
+
+    wg, wu, bias = whole(2, n, d), whole(1, n, d), whole(9, n).contiguous()
+    G, U, BI = (v.double() for v in (wg, wu, bias))
+    for T in (1, 2, 8, 15, 16, 17, 24, 31, 32, 33):
+        x, res = whole(1, T, d), whole(20, T, n)
+        X = x.double()
+        a, b = X @ G.T, X @ U.T
+        wide = torch.full((T + 2, n + gap), float("nan"), device="cuda", dtype=DT[dt])
+        out = wide[1:T + 1, :n]
+        sm.linear(x, wg, bias=bias, act=sm.ACT_RELU, residual=res, out=out)
+        assert torch.equal(out, ((a + BI).relu() + res.double()).to(DT[dt]))
+        sm.gated(x, wg, wu, act=sm.ACT_RELU, out=out)
+        assert torch.equal(out, (a.relu() * b).to(DT[dt]))
+        out.fill_(float("nan"))
+        assert bool(wide.isnan().all())

@@ -21,7 +21,9 @@ def rules(tmp_path_factory):
                    'extern "C" void plan(int kind, int b, int M, int N, int K, int parts, int cus, '
                    'int* out) {\n'
                    '  const sm::Plan p = sm::plan_product(kind, b, M, N, K, parts, cus);\n'
-                   '  out[0] = p.mi; out[1] = p.splits; out[2] = p.cut;\n}\n')
+                   '  out[0] = p.mi; out[1] = p.splits; out[2] = p.cut;\n}\n'
+                   'extern "C" int few(int kind, int b, int T, int n, int d, int w, int x) {\n'
+                   f'  return sm::takes_few(kind, b, T, n, d, w, x, {CUS});\n}}\n')
     lib = folder / "plan.so"
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-O1", "-shared", "-fPIC",
                     f"-I{build_lib.CSRC}", str(src), "-o", str(lib)], check=True)
@@ -67,3 +69,28 @@ def test_plans_are_ones_that_the_kernels_run(rules, kind, parts, bf16):
                     cols = (32 if k == GATED else 64) * mi
                     assert cut == N or (mi == 4 and 0 < cut < N and cut % cols == 0
                                         and not (k == DW and q == 2))
+
+
+# Where one kernel takes at least a ninth longer than the other, as measured (us by the kernel for
+# few tokens, by tiles).
+FASTER = [("bf16", LINEAR, 1, 4096, 11008, 20.5, 30.7), ("bf16", LINEAR, 17, 11008, 4096, 28.5, 34.1),
+          ("bf16", LINEAR, 32, 4096, 11008, 34.8, 29.4), ("bf16", GATED, 1, 4096, 11008, 34.1, 41.1),
+          ("bf16", GATED, 24, 4096, 11008, 45.9, 40.3), ("bf16", GATED, 32, 4096, 11008, 49.2, 41.1),
+          ("bf16", GATED, 24, 11008, 4096, 44.9, 50.3), ("bf16", LINEAR, 32, 1280, 5120, 9.7, 13.2),
+          ("bf16", LINEAR, 16, 11008, 512, 21.7, 19.2), ("bf16", LINEAR, 32, 11008, 512, 30.8, 19.3),
+          ("bf16", GATED, 1, 11008, 512, 25.0, 20.6), ("bf16", GATED, 32, 11008, 512, 40.8, 21.2),
+          ("bf16", GATED, 24, 4096, 64, 15.5, 12.2), ("bf16", GATED, 32, 768, 2304, 5.4, 9.5),
+          ("bf16", GATED, 24, 3416, 1280, 13.6, 16.9), ("bf16", LINEAR, 8, 11008, 64, 17.7, 14.8),
+          ("f32", LINEAR, 32, 4096, 11008, 67.2, 112.0), ("f32", GATED, 32, 4096, 11008, 104.5, 163.4),
+          ("f32", GATED, 24, 11008, 512, 89.2, 58.9),
+          ("f32", LINEAR, 1, 11008, 512, 31.1, 56.7)]
+
+
+@pytest.mark.parametrize("dt,kind,T,d,n,few,tiles", FASTER)
+def test_few_tokens_take_the_faster_kernel(rules, dt, kind, T, d, n, few, tiles):
+    bf16 = dt == "bf16"
+    assert max(few, tiles) >= min(few, tiles) * 10 / 9
+    assert bool(rules.few(kind, bf16, T, n, d, 1, 1)) == (few < tiles)
+    # weights that would have to be laid out for the tiles, tokens past the kernel's, other products
+    assert rules.few(kind, bf16, T, n, d, 0, 1) and not rules.few(kind, bf16, 33, n, d, 0, 0)
+    assert not rules.few(SLOPE, bf16, T, n, d, 1, 1) and not rules.few(GATED_SLOPE, bf16, T, n, d, 0, 0)
