@@ -6,8 +6,11 @@
 // float32) and 8 bytes of codes.  A workgroup takes one or four units of 64
 // blocks, all of whose loads are in flight before the first is used.  Rows and columns
 // come from one scalar division a workgroup: a division per lane in 64 bits
-// cost more than the memory (pack of 8192 x 4096 bf16: 44 us with it).  Measured:
-// that pack 16.5 us (6.2 TB/s), unpack of 8192 x 11008 to bf16 39 us (7.0).
+// cost more than the memory (pack of 8192 x 4096 bf16: 44 us with it).
+// Measured with one or two sets of buffers in turn, three, and six (less and less
+// of what is read is still in the Infinity Cache): that pack 16.5, 16.5 and 20.0
+// us (6.2, 6.2, 5.1 TB/s), unpack of 8192 x 11008 to bf16 39.5, 43.9 and 48.5
+// (6.9, 6.2, 5.6).
 #include "layer_internal.hpp"
 
 namespace sm {
@@ -288,8 +291,13 @@ __global__ __launch_bounds__(kThreads) void k_act8_unpack(const uint8_t* x8, con
 // Blocks from which a workgroup takes four units: 256 workgroups of them.
 constexpr int64_t kManyBlocks = 256 * 4 * kBlocks;
 // A checkpoint is read in the backward pass: its stores are non-temporal (8192
-// x 4096 bf16: 16.5 us, 20.7 cacheable).  Its values are used next, so theirs
-// are cacheable up to what the Infinity Cache can keep.
+// x 4096 bf16: 16.5 us, 20.7 cacheable).  Values are used sooner, and theirs
+// are cacheable as long as all that a call moves (codes, scales and values)
+// may stay in the Infinity Cache.  Just beyond, the call itself is faster with
+// non-temporal ones, a reader right behind it with the others: 8192 x 11008 to
+// bf16 (273 MB, 180 of them values) 39.6 us and 45.5, with a reading of the
+// values 113 and 104; a backward pass with weight gradients alone 660 and 655,
+// with dx ahead of them 1246 both.
 constexpr double kStreamBytes = 256.0 * 1024 * 1024;
 
 }  // namespace
