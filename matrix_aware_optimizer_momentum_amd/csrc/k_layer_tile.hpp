@@ -743,8 +743,10 @@ __device__ __forceinline__ void epilogue(const f32x16 (&acc)[MI][2], const TileA
   }
 }
 
+// Two waves to a SIMD; of the least tiles, whose workgroups of two waves fill
+// the LDS of a CU in pairs, one.
 template <typename T, int KIND, int MI>
-__global__ __launch_bounds__(128 * MI) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(128 * MI) __attribute__((amdgpu_waves_per_eu(MI == 1 ? 1 : 2, 2)))
 void k_tile(TileArgs A) {
   typedef Geo<T, MI> G;
   __shared__ __attribute__((aligned(16))) char smem[G::NBUF * G::STAGE + 4096 * (2 * G::WN)];

@@ -104,3 +104,20 @@ def test_the_scan_finds_the_hazards():
                       "\tv_readfirstlane_b32 s40, v7", "\ts_nop 4", "\ts_mov_b32 m0, s42",
                       "\tbuffer_load_dwordx4 v61, s[40:43], 0 offen lds"])
     assert [b[0] for b in lds_load_hazards(body)] == [3, 7]
+
+
+@pytest.mark.parametrize("unit", TILES)
+def test_waves_that_share_a_simd(asm, unit):
+    """By what the hardware holds: 512 VGPRs of a SIMD's lane (in eights), 160 KB of LDS of a CU,
+    eight waves of a SIMD, four SIMDs."""
+    mi = int(unit[-1])
+    number = lambda entry, key: int(re.search(rf"\.{key}:\s+(\d+)", entry).group(1))
+    found = [e for e in asm[unit].split("- .agpr_count:")[1:]
+             if re.search(r"\.name:\s+\S*k_tile", e)]
+    assert len(found) == 6
+    for e in found:
+        threads = number(e, "max_flat_workgroup_size")
+        assert threads == 128 * mi
+        by_lds = 163840 // number(e, "group_segment_fixed_size") * (threads // 64) // 4
+        by_vgprs = 512 // (-(-number(e, "vgpr_count") // 8) * 8)
+        assert min(by_lds, by_vgprs, 8) == (1 if mi == 1 else 2), e[:400]
