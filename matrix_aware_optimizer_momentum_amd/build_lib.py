@@ -23,7 +23,7 @@ HIP_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-ffp-contract=off",  # roundings happen where the source writes them
-    "-Wall", "-Wno-unused-function", "-Werror=return-type",
+    "-Wall", "-Werror=return-type", "-Werror=unused-function",
     "-Wno-inline-asm",  # the direct-to-LDS loads name M0 as clobbered on purpose
 ]
 

@@ -219,25 +219,6 @@ sm_status layer_query(const sm_layer* l, Call c, size_t* bytes) {
   return SM_OK;
 }
 
-Product product_of(const sm_layer& l, int kind) {
-  Product p;
-  std::memset(&p, 0, sizeof(p));
-  p.kind = kind;
-  p.dt = l.dt;
-  p.act = l.act;
-  p.M = (int)l.T;
-  p.N = l.n;
-  p.K = l.d;
-  p.parts = 1;
-  p.a[0] = {l.x, l.ldx};
-  p.b[0] = {l.w, l.ldw};
-  p.b[1] = {l.w2, l.ldw2};
-  p.bias = l.bias;
-  p.c[0] = l.y;
-  p.ldc[0] = l.ldy;
-  return p;
-}
-
 // The operands of a call, laid out if they have to be.
 struct Operands {
   Operand x, w, w2, dz[2];
