@@ -605,8 +605,10 @@ sm_status sm_act8_unpack(const uint8_t* x8, const uint8_t* scale, int dt, int64_
  * be columns of one wider matrix, and a vector may lie between two rows.
  * T == 0: sm_linear, sm_gated and dx are no-ops; dw, dw2 and dbias are set to
  * 0, or left as they are with accumulate.
- * A row of x or dy that holds a NaN or infinity makes its own rows of y and
- * dx so, and dw, dw2 and dbias as the sums give.
+ * A NaN or infinity in a row of x or dy reaches no other row of y or dx.  Its
+ * own rows, and dw, dw2 and dbias, are what the formulas give in float32: a
+ * NaN stays one, relu makes 0 of -infinity (and its slope), and an infinity
+ * times 0, as in the curved activations' formulas, is NaN.
  * ws: scratch of at least the matching *_ws(...) bytes, 256-byte aligned
  *   (may be NULL if that is 0), over none of the call's buffers; the query
  *   takes the call's own arguments.  Calls that may run at the same time need

@@ -1,5 +1,7 @@
-"""Calls of the feed-forward layers that leave gradients out, on the GPU: against
-the same call with all of them.  Bit for bit, but for the two weight gradients
+"""Calls of the feed-forward layers that leave gradients out, workspaces over
+tensors, and values that are not finite, on the GPU.
+
+Gradients left out: against the same call with all of them.  Bit for bit, but for the two weight gradients
 of a gated layer: they are one launch if both are wanted, whose sums may be
 split otherwise than one's.  Two float32 sums of T products (and an addend) in
 another order are apart by twice (T + 1) * 2^-23 of the magnitudes' sum, and
@@ -79,3 +81,30 @@ def test_a_workspace_over_a_tensor_is_refused(gpu_lib):
     with pytest.raises(sm.SmError):
         sm.gated_grad(out, x, w, w, ws=flat)
     assert bool((flat == 0).all()) and torch.equal(x, before)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", [sm.ACT_NONE, sm.ACT_RELU, sm.ACT_SILU, sm.ACT_GELU, sm.ACT_GELU_TANH])
+@pytest.mark.parametrize("T,d,n", [(20, 264, 520), (300, 1000, 264), (2051, 260, 2053), (4090, 72, 4091)])
+def test_values_that_are_not_finite_reach_their_rows_alone(gpu_lib, T, d, n, act, dtype):
+    """In every way that the products are launched; the other rows keep their bits."""
+    x, wg, wu, dy, res = tensors(4, dtype, (T, d), (n, d), (n, d), (T, n), (T, n))
+    wg[0], wg[1], wu[0] = 0.0, -wg[2], 0.0
+    bad_x, bad_dy = x.clone(), dy.clone()
+    bad_x[T - 1, d - 1], bad_x[3, 0], bad_x[7, 5] = float("nan"), float("inf"), -float("inf")
+    bad_dy[T // 2, n - 1], bad_dy[11, 1] = float("nan"), float("inf")
+    rows = torch.ones(T, dtype=torch.bool, device="cuda")
+    rows[[T - 1, 3, 7]] = False
+    for call in (lambda x: sm.linear(x, wg, act=act, residual=res), lambda x: sm.gated(x, wg, wu, act=act)):
+        got, want = call(bad_x), call(x)
+        assert torch.equal(got[rows], want[rows]) and got[T - 1].isnan().all()
+    if act == sm.ACT_RELU:   # infinity by the sign of its weight; times 0 it is NaN
+        y = sm.linear(bad_x, wg, act=act)
+        want = torch.where(wg[1:, 0] > 0, float("inf"), 0.0)
+        assert torch.equal(y[3, 1:].float(), want) and y[3, 0].isnan()
+    rows[[T // 2, 11]] = False
+    for call in (lambda x, dy: sm.linear_grad(dy, x, wg, act=act, need_dw=False),
+                 lambda x, dy: sm.gated_grad(dy, x, wg, wu, act=act, need_dw=False)):
+        got, want = call(bad_x, bad_dy)[0], call(x, dy)[0]
+        assert torch.equal(got[rows], want[rows])
+        assert not got[T // 2].isfinite().any()
