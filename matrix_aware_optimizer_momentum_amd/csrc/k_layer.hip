@@ -20,7 +20,9 @@ int cu_count() {
   return cache[dev];
 }
 
-// Column sums over kSumRows rows: a wave takes every eighth row, a lane two
+// Column sums over kSumRows rows, of dz as it was rounded for the products (in
+// bf16 an error as large as the rounding of the sums themselves, where terms of
+// both signs cancel to a root of their number): a wave takes every eighth row, a lane two
 // columns, eight rows in flight.  FINAL: those are all rows, and the sums go to
 // out (or onto it); else to sums[blockIdx.y][n] in float32.
 constexpr int kSumRows = 256, kSumCols = 128, kSumWaves = 8;
