@@ -45,6 +45,11 @@
 // consecutive columns of one row at a time.  Results are made from them in the
 // registers; residual, dy or old gradients come to them, and they go to
 // memory, through 4 KB of LDS of the wave's own.
+// dz, da and db are rounded to the layer's type there, as operands of the
+// products that follow: in bf16 the gradients' error is then the square root of
+// two times what rounding them alone leaves (2.4e-3 of a result, 1.7e-3).  A
+// second operand with what the rounding cut off would double the products of
+// dx and dW (8192 tokens, 4096 x 11008: 2.45 ms more on 3.6).
 #pragma once
 
 #include "layer_math.hpp"

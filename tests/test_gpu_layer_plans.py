@@ -136,3 +136,30 @@ def test_few_tokens(gpu_lib, d, n, gap, dt):
         assert torch.equal(out, (a.relu() * b).to(DT[dt]))
         out.fill_(float("nan"))
         assert bool(wide.isnan().all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d,n", [(11008, 512), (4096, 11008)])
+def test_few_tokens_that_are_laid_out(gpu_lib, d, n, dt):
+    """x off alignment beside weights that are read in place; scratch full of NaN, of the size asked
+    for; the same bits again, and from a graph."""
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    whole = lambda top, *s: torch.randint(-top, top + 1, s, generator=gen, device="cuda").to(DT[dt])
+    wg, wu = whole(2, n, d), whole(1, n, d)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    for T in (1, 19, 32):
+        x = whole(1, T, d + 3)[:, 3:]
+        want = ((x.double() @ wg.double().T).relu() * (x.double() @ wu.double().T)).to(DT[dt])
+        first = sm.gated(x, wg, wu, act=sm.ACT_RELU, ws=ws)
+        assert torch.equal(first, want)
+        assert torch.equal(sm.linear(x, wu, ws=ws), (x.double() @ wu.double().T).to(DT[dt]))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = sm.gated(x, wg, wu, act=sm.ACT_RELU)
+        for _ in range(3):
+            out.fill_(float("nan"))
+            ws.fill_(255)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        del g
